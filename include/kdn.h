@@ -82,7 +82,8 @@ typedef enum {
     KDN_ERR_CUDA = 7,         /* a CUDA runtime call or kernel launch failed         */
     KDN_ERR_TIMEOUT = 8,      /* device: a bounded wait gave up (results invalid)    */
     KDN_ERR_RANGE = 9,        /* device: a chunk's cumulative log-decay left the
-                                 range the factored decay supports (results invalid) */
+                                 range the factored decay supports (results invalid);
+                                 attention calls: a length or table entry out of range */
     KDN_ERR_ALIAS = 10        /* an output overlaps an input (other than S/p resume) */
 } kdn_status;
 
@@ -441,6 +442,158 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
                                const float *S0, const float *p0,
                                void *o, float *S_T, float *p_T, uint32_t *status_out,
                                kdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention layers beside the mixer.  The pages' hybrid backbone alternates KDN
+ * layers with sliding-window attention layers; these calls run such a layer when
+ * a stack is served: attention over whole prompts, a paged key/value cache held
+ * in 4 bits, and attention of one new token per sequence over that cache.
+ *
+ * Conventions, besides the ones above
+ *   - Head h of H reads key head h / (H / H_kv); H is a multiple of H_kv.
+ *   - q, k and v are [rows, heads, d] with the last axis dense.  Their row and
+ *     head strides are given in elements, are multiples of 16 bytes and keep
+ *     rows and heads apart (a slice of a fused qkv projection is fine); the
+ *     stride of an axis of length one is not read.  Outputs are dense.
+ *   - scale multiplies q.k; 0 selects 1 / sqrt(d); negative or not finite:
+ *     KDN_ERR_SHAPE.
+ *   - window > 0: a query sees the last `window` keys up to its own place;
+ *     window == 0: all of them.
+ *   - lse [rows, H] fp32 is log(sum over the visible keys of exp(scale q.k)).
+ *     A row that sees no key gives o = 0 and lse = -infinity.
+ *   - What a query does not see has no influence on its row, infinities and NaN
+ *     included.
+ *   - Lengths, tables and slots are device data.  What lies outside its range is
+ *     never followed: it is skipped or cut off, and KDN_ERR_RANGE is recorded in
+ *     the status word of the calls that have a workspace.
+ *
+ * The cache is an array of pages of `page` tokens (a multiple of 16 up to 1024);
+ * d is 32, 64 or 128; kdn_cache_size() bytes.  A slot is page id * page + place
+ * in the page.  Keys and values are held as 4-bit codes with one fp16 scale per
+ * 32 neighbouring channels of a token and head (4.5 bits a value):
+ *
+ *   s = fp16(min(max |x| / 7, 65504)),  code = clamp(rint(x / s), -7, 7) + 8
+ *   (8 where s = 0),  value = (code - 8) s;  a group that holds a NaN or an
+ *   infinity has s = NaN.
+ *
+ * Layout: [page id][key head][page / 16] blocks of 16 tokens, 18 d bytes each, with
+ * G = d / 32 groups, written for the fragments of the warp-level matrix products:
+ *   K codes   8 d bytes: per token t, 32-bit words w = c G + g (c < 4): channels
+ *             32 g + 8 c .. + 7, lowest bits first;
+ *   K scales  d bytes: [t][g];
+ *   V codes   8 d bytes: words [t / 8][i < 8][t / 2 % 4][g]; the low 16 bits belong
+ *             to the even token and the high 16 to the odd one: channels
+ *             32 g + 8 n + i, n = 0..3, lowest bits first;
+ *   V scales  d bytes: [t / 8][t / 2 % 4][g][t % 2].
+ */
+
+/*
+ * Block tables and slot maps of one batch, from the requests' lengths, on the GPU.
+ * Request r holds context_len[r] tokens (in the first ceil(context_len / page)
+ * entries of row r of block_table) and gets new_len[r] more.  Requests are
+ * granted in order: a request that needs new pages is granted when they and all
+ * pages wanted before it fit into the free list, one that needs none always.
+ * Pages are taken from the end of the free list: free_pages[0 .. free_count).
+ *
+ * Inputs : context_len, new_len [n_req]; free_pages [n_free], free_count [1]
+ *          (all int32).
+ * In/out : block_table [n_req, table_width] int32: the entries of granted
+ *          requests' new pages are written, nothing else (so a repeated call
+ *          with the same inputs gives the same table).
+ * Outputs: slot_map [capacity] int64 and position [capacity] int32: the slot and
+ *          the place in its sequence of every new token, packed request after
+ *          request; the slot is -1 for tokens of a request that was not granted
+ *          and past the last token (position 0 there);
+ *          cu_new [n_req + 1]: first packed token of each request;
+ *          seq_len [n_req]: context_len + new_len if granted, else context_len;
+ *          granted [n_req]: 1 or 0; free_left [1]: the free_count that remains
+ *          (int32).
+ * Status : KDN_ERR_RANGE when a length is negative or does not fit the table
+ *          (that request is not granted; a negative new_len counts as 0), when
+ *          free_count is outside [0, n_free] (cut off), or when the tokens exceed
+ *          capacity.
+ * Sizes  : n_req <= 16384 (else KDN_ERR_UNSUPPORTED), table_width * page < 2^31.
+ * Workspace: 256 bytes, the device status word.
+ */
+kdn_status kdn_cache_plan(int n_req, int page, int table_width, int n_free, int capacity,
+                          const int32_t *context_len, const int32_t *new_len, int32_t *block_table,
+                          const int32_t *free_pages, const int32_t *free_count,
+                          int64_t *slot_map, int32_t *position, int32_t *cu_new, int32_t *seq_len,
+                          int32_t *granted, int32_t *free_left,
+                          void *workspace, size_t workspace_bytes, kdn_stream_t stream);
+
+/* Bytes of a cache of n_pages pages; 0 for unsupported sizes. */
+size_t kdn_cache_size(int n_pages, int page, int H_kv, int d);
+
+/*
+ * Quantise tokens into the cache: k, v [n_tok, H_kv, d] (io_dtype) to the slots
+ * slot_map [n_tok] int64.  A slot outside [0, n_pages * page) is skipped (no
+ * workspace, no status).  Two tokens of one call must not share a slot.
+ */
+kdn_status kdn_cache_write(int n_tok, int n_pages, int page, int H_kv, int d, int io_dtype,
+                           const void *k, int64_t k_row, int64_t k_head,
+                           const void *v, int64_t v_row, int64_t v_head,
+                           const int64_t *slot_map, void *cache, kdn_stream_t stream);
+
+/*
+ * The values that slots hold, as k, v [n_tok, H_kv, d] (io_dtype, dense): zeros for
+ * a slot outside the cache.  With kdn_prompt_attention (cu_k beside cu_q) this
+ * continues a prompt over a cached prefix.
+ */
+kdn_status kdn_cache_read(int n_tok, int n_pages, int page, int H_kv, int d, int io_dtype,
+                          const void *cache, const int64_t *slot_map, void *k, void *v,
+                          kdn_stream_t stream);
+
+/*
+ * Attention of one query token per sequence over the cache (the token's own key and
+ * value are already in it): sequence r attends to its first seq_len[r] tokens,
+ * held in the pages of row r of block_table.
+ *
+ * Inputs : q [n_seq, H, d] io_dtype; cache; block_table [n_seq, table_width],
+ *          seq_len [n_seq] int32; max_len: a bound on seq_len that the host knows
+ *          (it sets how many parts a long sequence is split into).
+ * Outputs: o [n_seq, H, d] io_dtype; lse [n_seq, H] fp32.
+ * Status : KDN_ERR_RANGE when a seq_len is negative or above max_len or
+ *          table_width * page (cut off), or a table entry in use is outside the
+ *          cache (its keys count as not visible).
+ * Workspace: kdn_cache_attention_workspace_size() bytes.
+ */
+size_t kdn_cache_attention_workspace_size(int n_seq, int H, int H_kv, int d, int max_len, int window);
+kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int n_pages, int table_width,
+                               int max_len, int window, float scale, int io_dtype,
+                               const void *q, int64_t q_row, int64_t q_head,
+                               const void *cache, const int32_t *block_table, const int32_t *seq_len,
+                               void *o, float *lse,
+                               void *workspace, size_t workspace_bytes, kdn_stream_t stream);
+
+/*
+ * Causal attention over whole prompts, packed one after another: sequence s has
+ * the queries cu_q[s] .. cu_q[s + 1] and the keys cu_k[s] .. cu_k[s + 1].  The last
+ * query stands at the last key's place, so with more keys than queries the prompt
+ * continues a prefix, and with fewer the first queries see nothing.
+ *
+ * Inputs : q [total_q, H, d], k, v [total_k, H_kv, d] io_dtype; cu_q, cu_k
+ *          [n_seq + 1] int32 (cu_k NULL: the same as cu_q).
+ * Outputs: o [total_q, H, d] io_dtype; lse [total_q, H] fp32.  Rows of no sequence
+ *          are left unwritten.
+ * flags  : 0, KDN_FLAG_PORTABLE (the CUDA-core path) or KDN_FLAG_TIMEOUT_PROBE;
+ *          others: KDN_ERR_UNSUPPORTED.
+ * Sizes  : d in {16, 32, 64, 128}.  bf16 io with d = 64 or 128 runs on tcgen05
+ *          tensor cores, everything else on the CUDA-core path (fp32 products in
+ *          3xTF32).
+ * Status : KDN_ERR_RANGE when the bounds of a sequence run backwards or outside
+ *          the totals (its rows are left unwritten); KDN_ERR_TIMEOUT.
+ * Workspace: kdn_prompt_attention_workspace_size() bytes.
+ */
+size_t kdn_prompt_attention_workspace_size(int n_seq, int total_q, int H, int H_kv, int d, int io_dtype,
+                                           uint32_t flags);
+kdn_status kdn_prompt_attention(int n_seq, int total_q, int total_k, int H, int H_kv, int d, int window,
+                                float scale, int io_dtype, uint32_t flags,
+                                const void *q, int64_t q_row, int64_t q_head,
+                                const void *k, int64_t k_row, int64_t k_head,
+                                const void *v, int64_t v_row, int64_t v_head,
+                                const int32_t *cu_q, const int32_t *cu_k, void *o, float *lse,
+                                void *workspace, size_t workspace_bytes, kdn_stream_t stream);
 
 /*
  * Synchronise `stream` and return the device status word the last call that

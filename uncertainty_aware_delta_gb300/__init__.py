@@ -34,3 +34,14 @@ from .binding import (  # noqa: F401
     status_string,
     workspace_size,
 )
+from .attention import (  # noqa: F401
+    CachePlan,
+    cache_alloc,
+    cache_attention_workspace_size,
+    kdn_cache_attention,
+    kdn_cache_plan,
+    kdn_cache_read,
+    kdn_cache_write,
+    kdn_prompt_attention,
+    prompt_attention_workspace_size,
+)

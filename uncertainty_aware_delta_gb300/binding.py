@@ -28,7 +28,9 @@ EXPORTED = (
     "kdn_read_device_status", "kdn_status_string", "kdn_abi_version", "kdn_forward_kernel_count",
     "kdn_forward_noalloc", "kdn_pkda_forward", "kdn_pkda_step", "kdn_dense_forward", "kdn_step_ex",
     "kdn_backward", "kdn_backward_workspace_size", "kdn_gated_forward", "kdn_gated_workspace_size",
-    "kdn_dense_workspace_size",
+    "kdn_dense_workspace_size", "kdn_cache_plan", "kdn_cache_size", "kdn_cache_write", "kdn_cache_read",
+    "kdn_cache_attention", "kdn_cache_attention_workspace_size", "kdn_prompt_attention",
+    "kdn_prompt_attention_workspace_size",
 )
 
 
@@ -94,6 +96,23 @@ def library():
             lib.kdn_gated_forward.restype = i32
             lib.kdn_gated_forward.argtypes = [i32] * 7 + [f32, f32, i32, u32] + [vp] * 6 + [fp, fp] + \
                 [vp, fp, fp, fp] + [vp, sz, vp]
+            st = [vp, ctypes.c_int64, ctypes.c_int64]
+            lib.kdn_cache_plan.restype = i32
+            lib.kdn_cache_plan.argtypes = [i32] * 5 + [vp] * 11 + [vp, sz, vp]
+            lib.kdn_cache_size.restype = sz
+            lib.kdn_cache_size.argtypes = [i32] * 4
+            lib.kdn_cache_write.restype = i32
+            lib.kdn_cache_write.argtypes = [i32] * 6 + st * 2 + [vp] * 3
+            lib.kdn_cache_read.restype = i32
+            lib.kdn_cache_read.argtypes = [i32] * 6 + [vp] * 5
+            lib.kdn_cache_attention_workspace_size.restype = sz
+            lib.kdn_cache_attention_workspace_size.argtypes = [i32] * 6
+            lib.kdn_cache_attention.restype = i32
+            lib.kdn_cache_attention.argtypes = [i32] * 9 + [f32, i32] + st + [vp] * 5 + [vp, sz, vp]
+            lib.kdn_prompt_attention_workspace_size.restype = sz
+            lib.kdn_prompt_attention_workspace_size.argtypes = [i32] * 6 + [u32]
+            lib.kdn_prompt_attention.restype = i32
+            lib.kdn_prompt_attention.argtypes = [i32] * 7 + [f32, i32, u32] + st * 3 + [vp] * 4 + [vp, sz, vp]
             lib.kdn_abi_version.restype = i32
             lib.kdn_abi_version.argtypes = []
             _lib = lib

@@ -7,15 +7,11 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "abi_checks.h"
 #include "kdn.h"
 #include "kdn_internal.h"
 
 namespace {
-
-constexpr size_t kAlign = 256;
-constexpr size_t kStatusBytes = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
@@ -25,19 +21,6 @@ int resolve_chunk(int chunk, int T) {
     if (T > 32) return 64;
     if (T > 16) return 32;
     return 16;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    const void* p;
-    size_t n;
-};
-
-bool overlaps(Range a, Range b) {
-    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
 // Tensor-core path availability (set by chunk_tc.cu when compiled in).
