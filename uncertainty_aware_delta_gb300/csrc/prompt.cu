@@ -6,6 +6,7 @@
 
 #include "attention.h"
 #include "common.cuh"
+#include "kdn.h"
 #include "mma_tf32x3.cuh"
 
 namespace kdn {
@@ -173,6 +174,7 @@ template <typename T> cudaError_t by_size(const PromptArgs& a, cudaStream_t s) {
 size_t prompt_scratch(int, int, int, int, int, int, uint32_t) { return 0; }
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s) {
+    if (!(a.flags & KDN_FLAG_PORTABLE) && prompt_tc_supported(a.io, a.d)) return launch_prompt_tc(a, s);
     return a.io == 1 ? by_size<__nv_bfloat16>(a, s) : by_size<float>(a, s);
 }
 

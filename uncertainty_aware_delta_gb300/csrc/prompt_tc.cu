@@ -1,0 +1,570 @@
+// Causal attention over packed prompts on tcgen05 tensor cores: bf16, heads of 64 or 128.
+//
+// One block takes two units of 128 query rows that read the same keys: two heads of one key
+// head where there are an even number of them, else two neighbouring row tiles of one head.
+// Per key tile of 128 and unit: S = Q K^T into TMEM, the softmax by one warpgroup with a row
+// a thread, P = exp(S - m) as bf16 back into S's TMEM columns, O += P V with P read from
+// TMEM.  While one unit's warpgroup works on its scores, the tensor cores run the other
+// unit's P V and next Q K^T: the products (4 x 128 x 128 x d multiply-adds a pair of tiles, 2048
+// cycles for d = 128) are what should bound it, with 2 x 128 x 128 exponentials beside them.
+//
+// The running maximum is raised only when a row's score passes it by 2^8: fp32 sums and
+// accumulators and bf16 weights have the range, and O (in TMEM) is then hardly ever rescaled.
+// Weights are rounded to bf16 for the product (the type of V in the MMA); their sum is taken
+// before rounding, in fp32.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <mutex>
+
+#include "attention.h"
+#include "common.cuh"
+#include "kdn.h"
+#include "sm100.cuh"
+
+namespace kdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr int kThreads = 384;                 // loader, MMA, 2 guard warps; 2 softmax warpgroups
+constexpr int kGuardThreads = 64;
+// registers: launched with 168 a thread (3 x 128 x 168); 88 + 2 x 208 = 3 x 168
+constexpr int kAuxRegs = 88, kSoftmaxRegs = 208;
+constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
+constexpr float kLazy = 8.0f;                 // powers of two a score may pass the running maximum by
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct PromptParams {
+    CUtensorMap tq, tk, tv;
+    const __nv_bfloat16* v;
+    long long v_row, v_head;
+    const int32_t *cu_q, *cu_k;
+    __nv_bfloat16* o;
+    float* lse;
+    uint32_t* status;
+    int n_seq, total_q, total_k, H, H_kv, window, groups, items, probe;
+    float scale_log2;
+};
+
+template <int D> struct Layout {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTileBytes = kHalves * 16384;      // 128 rows of d bf16 in 128-byte-swizzled halves
+    static constexpr int kSlots = D == 128 ? 5 : 8;         // K and V tiles in turn
+    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
+};
+
+// TMEM columns: scores (then weights) of the units, their outputs
+constexpr uint32_t kTmS = 0, kTmO = 256, kTmCols = 512;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+// After tmem_wait_ld(): ties the loaded registers to that point of the program.
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// What a block works on.
+struct Item {
+    int q0, n_q, k0, n_k;    // the sequence's rows
+    int row;                 // first row of the item in its sequence; negative: nothing to do
+};
+struct Unit {
+    int head, row, rows;     // rows: valid ones
+    int place;               // place of its first row among the keys
+    int lo, hi;              // key tiles; hi < lo: none
+};
+template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int h0, int window) {
+    Unit u;
+    u.head = PAIR ? h0 + s : h0;
+    u.row = it.row + (PAIR ? 0 : s * kTileRows);
+    u.rows = min(kTileRows, it.n_q - u.row);
+    u.place = it.n_k - it.n_q + u.row;
+    const int last = u.place + u.rows - 1, first = window > 0 ? max(u.place - window + 1, 0) : 0;
+    u.lo = first / kTileKeys;
+    u.hi = u.rows > 0 && last >= 0 ? last / kTileKeys : u.lo - 1;
+    return u;
+}
+// Whether some valid row of an active unit does not see all of key tile b.
+__device__ __forceinline__ bool masked(const Unit& u, int b, int window) {
+    return b * kTileKeys + kTileKeys - 1 > u.place || (window > 0 && b * kTileKeys <= u.place + u.rows - 1 - window);
+}
+__device__ __forceinline__ bool active(const Unit& u, int b) { return b >= u.lo && b <= u.hi; }
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptParams P) {
+    using L = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * L::kSlots + 16];
+    __shared__ Item item;
+    __shared__ int before[kThreads / 32], dirty;
+    __shared__ volatile int aborted;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes;
+    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * L::kSlots, bar_q = bar_empty + 8 * L::kSlots,
+                   bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_v = bar_o + 16, bar_cut = bar_v + 32, bar_drain = bar_cut + 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = blockIdx.x % P.groups;
+    // the longest rows first: each sequence's last tiles have the most keys
+    const int want = P.items - 1 - static_cast<int>(blockIdx.x / P.groups);
+
+    // ---- the item: sequences' tiles one after another, found by a scan over all sequences
+    constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
+    {
+        const int per = (P.n_seq + kThreads - 1) / kThreads, s0 = min(tid * per, P.n_seq), s1 = min(s0 + per, P.n_seq);
+        auto tiles_of = [&](int s, Item& it) {
+            const int q0 = P.cu_q[s], q1 = P.cu_q[s + 1], k0 = P.cu_k[s], k1 = P.cu_k[s + 1];
+            if (q0 < 0 || q1 < q0 || q1 > P.total_q || k0 < 0 || k1 < k0 || k1 > P.total_k) {
+                if (blockIdx.x == 0) set_status(P.status, kStatusRange);
+                return 0;
+            }
+            it = Item{q0, q1 - q0, k0, k1 - k0, 0};
+            return (q1 - q0 + kItemRows - 1) / kItemRows;
+        };
+        Item it;
+        int mine = 0;
+        for (int s = s0; s < s1; ++s) mine += tiles_of(s, it);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 31) before[warp] = upto;
+        if (tid == 0) {
+            item.row = -1;
+            aborted = 0;
+            dirty = 0;
+            for (int i = 0; i < L::kSlots; ++i) {
+                mbar_init(bar_full + 8 * i, 1);
+                mbar_init(bar_empty + 8 * i, 1);
+            }
+            mbar_init(bar_q, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar_s + 8 * i, 1);
+                mbar_init(bar_p + 8 * i, 4);
+                mbar_init(bar_o + 8 * i, 1);
+            }
+            // four in turn: the loader may be several tiles ahead of the guard, and it of the products
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(bar_v + 8 * i, kGuardThreads);
+                mbar_init(bar_cut + 8 * i, 1);
+            }
+            mbar_init(bar_drain, 1);   // also the probe's: completed by nothing before the end
+            mbar_fence_init();
+        }
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += before[w];
+        if (want < upto && want >= upto - mine) {
+            int x = upto - mine;
+            for (int s = s0; s < s1; ++s) {
+                const int n = tiles_of(s, it);
+                if (want < x + n) {
+                    it.row = (want - x) * kItemRows;
+                    item = it;
+                    break;
+                }
+                x += n;
+            }
+        }
+        __syncthreads();
+    }
+    const Item it = item;
+    if (it.row < 0) return;   // fewer tiles than blocks
+    if (warp == 0) {
+        tmem_alloc(smem_addr(&tmem_slot), kTmCols);
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    // a block's heads: two query heads of a key head, or one
+    const int rep = P.H / P.H_kv, h0 = PAIR ? 2 * group : group, kvh = h0 / rep;
+    const Unit u0 = unit_of<PAIR>(it, 0, h0, P.window), u1 = unit_of<PAIR>(it, 1, h0, P.window);
+    const bool any0 = u0.hi >= u0.lo, any1 = u1.hi >= u1.lo;
+    const int lo = any0 && any1 ? min(u0.lo, u1.lo) : any0 ? u0.lo : u1.lo;
+    const int hi = any0 && any1 ? max(u0.hi, u1.hi) : any0 ? u0.hi : u1.hi;   // hi < lo: no key is seen
+    auto cut = [&](int b) { return (active(u0, b) && masked(u0, b, P.window)) || (active(u1, b) && masked(u1, b, P.window)); };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        for (uint32_t i = 0; i < kWaitLimit; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (aborted) return false;
+        }
+        aborted = 1;
+        set_status(P.status, kStatusTimeout);
+        return false;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        if (warp == 0 && lane == 0 && hi >= lo) {
+            // ---- loader: Q, then K and V tiles in turn
+            mbar_expect_tx(bar_q, (any0 ? L::kTileBytes : 0) + (any1 ? L::kTileBytes : 0));
+            for (int s = 0; s < 2; ++s) {
+                const Unit& u = s ? u1 : u0;
+                if (s ? any1 : any0)
+                    for (int f = 0; f < L::kHalves; ++f)
+                        tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row, bar_q);
+            }
+            int n = 0;
+            uint32_t nc = 0;
+            bool ok = true;
+            for (int b = lo; ok && b <= hi; ++b)
+                for (int i = 0; i < 2; ++i, ++n) {
+                    const int slot = n % L::kSlots;
+                    if (n >= L::kSlots && !wait(bar_empty + 8 * slot, (n / L::kSlots - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar_full + 8 * slot, L::kTileBytes);
+                    for (int f = 0; f < L::kHalves; ++f)
+                        tma_load_3d(skv + slot * L::kTileBytes + f * 16384, i ? &P.tv : &P.tk, 64 * f, kvh,
+                                    it.k0 + b * kTileKeys, bar_full + 8 * slot);
+                    if (i && cut(b)) mbar_arrive(bar_cut + 8 * (nc++ & 3));
+                    if (P.probe && n == 0) {
+                        if (!mbar_wait(bar_drain, 0, kProbeLimit)) {
+                            aborted = 1;
+                            set_status(P.status, kStatusTimeout);
+                        }
+                    }
+                    if (aborted) {
+                        ok = false;
+                        ++n;
+                        break;
+                    }
+                }
+            if (!ok) {   // copies already issued land before the block's shared memory goes away
+                mbar_wait(bar_q, 0, kWaitLimit);
+                for (int j = max(n - L::kSlots, 0); j < n; ++j)
+                    mbar_wait(bar_full + 8 * (j % L::kSlots), (j / L::kSlots) & 1, kWaitLimit);
+            }
+        } else if (warp == 1 && lane == 0 && hi >= lo) {
+            // ---- MMA: P V of a key tile and Q K^T of the next, unit after unit
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0, 0), id_o = idesc_bf16(128, D, 0, 1, 0);
+            auto scores = [&](int s, int slot) {
+                const uint64_t a = sw128_desc(sq + s * L::kTileBytes, 16, 1024), b = sw128_desc(skv + slot * L::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+                    mma_bf16(tmem + kTmS + 128 * s, desc_add(a, off), desc_add(b, off), id_s, k > 0);
+                }
+                mma_commit(bar_s + 8 * s);
+            };
+            auto output = [&](int s, int slot, bool add) {
+                const uint64_t b = sw128_desc(skv + slot * L::kTileBytes, 16384, 1024);
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    mma_bf16_tmem_a(tmem + kTmO + 128 * s, tmem + kTmS + 128 * s + 8 * k, desc_add(b, k * 2048), id_o, add || k > 0);
+            };
+            auto full = [&](int n) { return wait(bar_full + 8 * (n % L::kSlots), (n / L::kSlots) & 1); };
+            bool ok = wait(bar_q, 0) && full(0);
+            if (ok) {
+                tc_fence_after();
+                if (active(u0, lo)) scores(0, 0);
+                if (active(u1, lo)) scores(1, 0);
+                mma_commit(bar_empty);
+            }
+            uint32_t np[2] = {0, 0}, nv = 0;
+            for (int b = lo; ok && b <= hi; ++b) {
+                const int kn = 2 * (b + 1 - lo), vn = 2 * (b - lo) + 1, vslot = vn % L::kSlots, kslot = kn % L::kSlots;
+                const bool more = b < hi;
+                ok = full(vn);
+                if (ok && cut(b)) {
+                    ok = wait(bar_v + 8 * (nv & 3), (nv >> 2) & 1);
+                    ++nv;
+                }
+                for (int s = 0; ok && s < 2; ++s) {
+                    const Unit& u = s ? u1 : u0;
+                    if (active(u, b)) {
+                        if (!(ok = wait(bar_p + 8 * s, np[s]++ & 1))) break;
+                        tc_fence_after();
+                        output(s, vslot, b > u.lo);
+                        if (b == u.hi) mma_commit(bar_o + 8 * s);
+                    }
+                    if (more && s == 0 && !(ok = full(kn))) break;
+                    if (more && active(u, b + 1)) scores(s, kslot);
+                }
+                if (ok) {
+                    mma_commit(bar_empty + 8 * vslot);
+                    if (more) mma_commit(bar_empty + 8 * kslot);
+                }
+            }
+            if (!ok) {   // products already issued end before TMEM goes away
+                mma_commit(bar_drain);
+                mbar_wait(bar_drain, 0, kWaitLimit);
+            }
+        } else if (warp >= 2 && hi >= lo) {
+            // ---- guard: in tiles that some row does not see all of, a value that is not finite is taken out
+            // (a weight of zero would not stop it in the product), and keys past the sequence are zeroed; the
+            // rows that see such a value get it at the end
+            const int g = tid - 64;
+            uint32_t nv = 0;
+            for (int b = lo; b <= hi; ++b) {
+                if (!cut(b)) continue;
+                const int vn = 2 * (b - lo) + 1, slot = vn % L::kSlots;
+                // only once its copy is under way does the slot's phase tell whether it has landed
+                if (!wait(bar_cut + 8 * (nv & 3), (nv >> 2) & 1)) break;
+                if (!wait(bar_full + 8 * slot, (vn / L::kSlots) & 1)) break;
+                uint8_t* tile = smem_raw + (skv - smem_addr(smem_raw)) + slot * L::kTileBytes;
+                const int keys = it.n_k - b * kTileKeys;
+                for (int i = g; i < L::kTileBytes / 16; i += kGuardThreads) {
+                    uint4* p = reinterpret_cast<uint4*>(tile) + i;
+                    if (i % 1024 / 8 >= keys) {
+                        *p = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 v = *p;
+                    // the exponent field's ones carry into the sign's place
+                    auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                    if (odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w)) {
+                        auto fix = [&](uint32_t w) {
+                            const uint32_t m = odd(w);
+                            return w & ~((m & 0x8000u ? 0xffffu : 0u) | (m & 0x80000000u ? 0xffff0000u : 0u));
+                        };
+                        *p = make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
+                        dirty = 1;
+                    }
+                }
+                fence_proxy_async();
+                mbar_arrive(bar_v + 8 * (nv++ & 3));
+            }
+        }
+    } else {
+        // ---- softmax: warpgroup s has unit s, a row a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int s = (warp - 4) / 4, row = tid % 128;
+        const Unit u = s ? u1 : u0;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + kTmS + 128 * s + lanes, to = tmem + kTmO + 128 * s + lanes;
+        const float c = P.scale_log2;
+        float m = -INFINITY, l = 0.f;   // m: running maximum, in powers of two
+        bool ok = true;
+        for (int b = u.lo; b <= u.hi; ++b) {
+            if (!(ok = __all_sync(kAll, wait(bar_s + 8 * s, (b - u.lo) & 1)))) break;
+            tc_fence_after();
+            uint32_t r[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, r[i]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) loaded(r[i]);
+            if (masked(u, b, P.window)) {
+                const int last = u.place + row - b * kTileKeys, first = P.window > 0 ? last - P.window + 1 : 0;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i > last || i < first) r[i / 32][i % 32] = 0xff800000u;
+            }
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                t0 = fmaxf(t0, fmaxf(__uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1])));
+                t1 = fmaxf(t1, fmaxf(__uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1])));
+            }
+            float t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                t2 = fmaxf(t2, fmaxf(__uint_as_float(r[2][i]), __uint_as_float(r[2][i + 1])));
+                t3 = fmaxf(t3, fmaxf(__uint_as_float(r[3][i]), __uint_as_float(r[3][i + 1])));
+            }
+            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
+            const bool raise = top > m + kLazy;
+            if (__any_sync(kAll, raise)) {
+                const float f = raise ? ex2(m - top) : 1.f;   // (0 from -infinity)
+                if (raise) m = top;
+                l *= f;
+                if (b > u.lo) {
+                    // the scores are complete, so the product before them is: O may be changed
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(to + i, x);
+                        tmem_wait_ld();
+                        loaded(x);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                        tmem_st32(to + i, x);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : -m;
+            const float2 cc = make_float2(c, c), bb = make_float2(base, base);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int at = 2 * (i % 16);
+                    uint32_t(&x)[32] = r[2 * h + i / 16];
+                    float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, bb);
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    if (i & 1) sum1 = add2(sum1, y);
+                    else sum0 = add2(sum0, y);
+                    p[i] = pack_bf16(y.x, y.y);
+                }
+                tmem_st32(ts + 32 * h, p);
+            }
+            sum0 = add2(sum0, sum1);
+            l += sum0.x + sum0.y;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p + 8 * s);
+        }
+        // ---- output
+        const bool some = u.hi >= u.lo;
+        if (ok && some) ok = __all_sync(kAll, wait(bar_o + 8 * s, 0));
+        if (ok && u.rows > 0) {
+            tc_fence_after();
+            const float f = l != 0.f ? 1.f / l : 0.f;
+            const bool mine = row < u.rows;
+            const long long at = static_cast<long long>(it.q0 + u.row + row) * P.H + u.head;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+                uint32_t x[32];
+                __syncwarp();
+                if (some) {
+                    tmem_ld32(to + i, x);
+                    tmem_wait_ld();
+                    loaded(x);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = some ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
+                if (dirty && mine) {   // what the guard took out and this row sees
+                    const int last = u.place + row, first = P.window > 0 ? last - P.window + 1 : 0;
+                    for (int b = lo; b <= hi; ++b) {
+                        if (!cut(b)) continue;
+                        for (int k = max(b * kTileKeys, first); k <= min(b * kTileKeys + kTileKeys - 1, last); ++k) {
+                            const __nv_bfloat16* v = P.v + (static_cast<long long>(it.k0) + k) * P.v_row + kvh * P.v_head + i;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float y = __bfloat162float(v[j]);
+                                if ((__float_as_uint(y) & 0x7f800000u) == 0x7f800000u)
+                                    x[j] = __float_as_uint(__uint_as_float(x[j]) + y);
+                            }
+                        }
+                    }
+                }
+                if (mine) {
+                    uint4* o = reinterpret_cast<uint4*>(P.o + at * D + i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 w;
+                        w.x = pack_bf16(__uint_as_float(x[8 * j]), __uint_as_float(x[8 * j + 1]));
+                        w.y = pack_bf16(__uint_as_float(x[8 * j + 2]), __uint_as_float(x[8 * j + 3]));
+                        w.z = pack_bf16(__uint_as_float(x[8 * j + 4]), __uint_as_float(x[8 * j + 5]));
+                        w.w = pack_bf16(__uint_as_float(x[8 * j + 6]), __uint_as_float(x[8 * j + 7]));
+                        o[j] = w;
+                    }
+                }
+            }
+            if (mine) P.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmCols);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// [rows, heads, d] bf16, tiles of 128 rows and 64 channels of one head.
+bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.head) * 2, static_cast<cuuint64_t>(x.row) * 2};
+    const cuuint32_t box[3] = {64, 1, kTileKeys}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
+    PromptParams P;
+    // without keys nothing is loaded; the maps then describe the queries
+    const Strided &k = a.total_k ? a.k : a.q, &v = a.total_k ? a.v : a.q;
+    const int nk = a.total_k ? a.total_k : a.total_q, hk = a.total_k ? a.H_kv : a.H;
+    if (!encode(&P.tq, a.q, a.total_q, a.H, D) || !encode(&P.tk, k, nk, hk, D) || !encode(&P.tv, v, nk, hk, D))
+        return cudaErrorInvalidValue;
+    P.v = static_cast<const __nv_bfloat16*>(a.v.p);
+    P.v_row = a.v.row; P.v_head = a.v.head;
+    P.cu_q = a.cu_q; P.cu_k = a.cu_k;
+    P.o = static_cast<__nv_bfloat16*>(a.o); P.lse = a.lse; P.status = a.status;
+    P.n_seq = a.n_seq; P.total_q = a.total_q; P.total_k = a.total_k; P.H = a.H; P.H_kv = a.H_kv; P.window = a.window;
+    P.probe = (a.flags & KDN_FLAG_TIMEOUT_PROBE) ? 1 : 0;
+    P.scale_log2 = a.scale * kLog2e;
+    constexpr int rows = PAIR ? kTileRows : 2 * kTileRows;
+    P.groups = PAIR ? a.H / 2 : a.H;
+    // no more tiles than this, whatever the lengths
+    P.items = a.total_q / rows + (a.n_seq < a.total_q ? a.n_seq : a.total_q);
+    const long long grid = static_cast<long long>(P.items) * P.groups;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Layout<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    prompt_tc_kernel<D, PAIR><<<static_cast<int>(grid), kThreads, Layout<D>::kSmem, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prompt_tc_supported(int io, int d) { return io == 1 && (d == 64 || d == 128); }
+
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s) {
+    const bool pair = (a.H / a.H_kv) % 2 == 0;
+    if (a.d == 128) return pair ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return pair ? launch<64, true>(a, s) : launch<64, false>(a, s);
+}
+
+}  // namespace kdn
