@@ -70,6 +70,31 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The MMA warp runs as a whole, so that descriptors stay in uniform registers, and one lane's
+// predicate issues.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead));
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead));
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lead)
+        : "memory");
+}
 // two fp32 operations an instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -101,6 +126,7 @@ struct Unit {
     int head, row, rows;     // rows: valid ones
     int place;               // place of its first row among the keys
     int lo, hi;              // key tiles; hi < lo: none
+    int all_from, all_to;    // of these, tiles all_from < b < all_to are seen whole by every valid row
 };
 template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int h0, int window) {
     Unit u;
@@ -111,13 +137,11 @@ template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int
     const int last = u.place + u.rows - 1, first = window > 0 ? max(u.place - window + 1, 0) : 0;
     u.lo = first / kTileKeys;
     u.hi = u.rows > 0 && last >= 0 ? last / kTileKeys : u.lo - 1;
+    u.all_to = max(u.place + 1, 0) / kTileKeys;
+    u.all_from = window > 0 && last >= window ? (last - window) / kTileKeys : -1;
     return u;
 }
-// Whether some valid row of an active unit does not see all of key tile b.
-__device__ __forceinline__ bool masked(const Unit& u, int b, int window) {
-    return b * kTileKeys + kTileKeys - 1 > u.place || (window > 0 && b * kTileKeys <= u.place + u.rows - 1 - window);
-}
-__device__ __forceinline__ bool active(const Unit& u, int b) { return b >= u.lo && b <= u.hi; }
+__device__ __forceinline__ bool masked(const Unit& u, int b) { return b >= u.all_to || b <= u.all_from; }
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptParams P) {
@@ -210,11 +234,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 
     // a block's heads: two query heads of a key head, or one
     const int rep = P.H / P.H_kv, h0 = PAIR ? 2 * group : group, kvh = h0 / rep;
-    const Unit u0 = unit_of<PAIR>(it, 0, h0, P.window), u1 = unit_of<PAIR>(it, 1, h0, P.window);
+    Unit u0 = unit_of<PAIR>(it, 0, h0, P.window), u1 = unit_of<PAIR>(it, 1, h0, P.window);
     const bool any0 = u0.hi >= u0.lo, any1 = u1.hi >= u1.lo;
     const int lo = any0 && any1 ? min(u0.lo, u1.lo) : any0 ? u0.lo : u1.lo;
     const int hi = any0 && any1 ? max(u0.hi, u1.hi) : any0 ? u0.hi : u1.hi;   // hi < lo: no key is seen
-    auto cut = [&](int b) { return (active(u0, b) && masked(u0, b, P.window)) || (active(u1, b) && masked(u1, b, P.window)); };
+    // tiles that the guard looks at: all that some unit masks
+    const int cut_to = min(any0 ? u0.all_to : 0x7fffffff, any1 ? u1.all_to : 0x7fffffff),
+              cut_from = max(any0 ? u0.all_from : -1, any1 ? u1.all_from : -1);
+    auto cut = [&](int b) { return b >= cut_to || b <= cut_from; };
     auto wait = [&](uint32_t bar, uint32_t parity) {
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
@@ -268,59 +295,82 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 for (int j = max(n - L::kSlots, 0); j < n; ++j)
                     mbar_wait(bar_full + 8 * (j % L::kSlots), (j / L::kSlots) & 1, kWaitLimit);
             }
-        } else if (warp == 1 && lane == 0 && hi >= lo) {
+        } else if (warp == 1 && hi >= lo) {
             // ---- MMA: P V of a key tile and Q K^T of the next, unit after unit
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0, 0), id_o = idesc_bf16(128, D, 0, 1, 0);
+            const uint32_t lead = elect_one();
+            auto one = [](int x) { return __shfl_sync(kAll, x, 0); };
+            const int first = one(lo), last = one(hi), lo0 = one(any0 ? u0.lo : 0x7ffffff0), hi0 = one(any0 ? u0.hi : -1),
+                      lo1 = one(any1 ? u1.lo : 0x7ffffff0), hi1 = one(any1 ? u1.hi : -1), c_to = one(cut_to), c_from = one(cut_from);
+            const uint32_t tm = one(tmem), q = one(sq), kv = one(skv), fb = one(bar_full), eb = one(bar_empty);
+            auto await = [&](uint32_t bar, uint32_t parity) { return __all_sync(kAll, wait(bar, parity)); };
+            const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(kv, 16, 1024), vd = sw128_desc(kv, 16384, 1024);
             auto scores = [&](int s, int slot) {
-                const uint64_t a = sw128_desc(sq + s * L::kTileBytes, 16, 1024), b = sw128_desc(skv + slot * L::kTileBytes, 16, 1024);
+                const uint64_t a = desc_add(qd, s * L::kTileBytes), b = desc_add(kd, slot * L::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-                    mma_bf16(tmem + kTmS + 128 * s, desc_add(a, off), desc_add(b, off), id_s, k > 0);
+                    mma_ss(lead, tm + kTmS + 128 * s, desc_add(a, off), desc_add(b, off), id_s, k > 0);
                 }
-                mma_commit(bar_s + 8 * s);
+                commit(lead, bar_s + 8 * s);
             };
             auto output = [&](int s, int slot, bool add) {
-                const uint64_t b = sw128_desc(skv + slot * L::kTileBytes, 16384, 1024);
+                const uint64_t b = desc_add(vd, slot * L::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < kTileKeys / 16; ++k)
-                    mma_bf16_tmem_a(tmem + kTmO + 128 * s, tmem + kTmS + 128 * s + 8 * k, desc_add(b, k * 2048), id_o, add || k > 0);
+                    mma_ts(lead, tm + kTmO + 128 * s, tm + kTmS + 128 * s + 8 * k, desc_add(b, k * 2048), id_o, k > 0 ? 1u : add);
             };
-            auto full = [&](int n) { return wait(bar_full + 8 * (n % L::kSlots), (n / L::kSlots) & 1); };
-            bool ok = wait(bar_q, 0) && full(0);
+            bool ok = await(bar_q, 0) && await(fb, 0);
             if (ok) {
                 tc_fence_after();
-                if (active(u0, lo)) scores(0, 0);
-                if (active(u1, lo)) scores(1, 0);
-                mma_commit(bar_empty);
+                if (first >= lo0) scores(0, 0);
+                if (first >= lo1) scores(1, 0);
+                commit(lead, eb);
             }
-            uint32_t np[2] = {0, 0}, nv = 0;
-            for (int b = lo; ok && b <= hi; ++b) {
-                const int kn = 2 * (b + 1 - lo), vn = 2 * (b - lo) + 1, vslot = vn % L::kSlots, kslot = kn % L::kSlots;
-                const bool more = b < hi;
-                ok = full(vn);
-                if (ok && cut(b)) {
-                    ok = wait(bar_v + 8 * (nv & 3), (nv >> 2) & 1);
+            uint32_t slot = 0, phase = 0;   // of the tile used last
+            auto next = [&]() {
+                if (++slot == L::kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            uint32_t np0 = 0, np1 = 0, nv = 0;
+            for (int b = first; ok && b <= last; ++b) {
+                const bool more = b < last;
+                next();
+                const uint32_t vslot = slot;
+                ok = await(fb + 8 * vslot, phase);
+                if (ok && (b >= c_to || b <= c_from)) {
+                    ok = await(bar_v + 8 * (nv & 3), (nv >> 2) & 1);
                     ++nv;
                 }
-                for (int s = 0; ok && s < 2; ++s) {
-                    const Unit& u = s ? u1 : u0;
-                    if (active(u, b)) {
-                        if (!(ok = wait(bar_p + 8 * s, np[s]++ & 1))) break;
-                        tc_fence_after();
-                        output(s, vslot, b > u.lo);
-                        if (b == u.hi) mma_commit(bar_o + 8 * s);
-                    }
-                    if (more && s == 0 && !(ok = full(kn))) break;
-                    if (more && active(u, b + 1)) scores(s, kslot);
+                if (ok && b >= lo0 && b <= hi0) {
+                    if (!(ok = await(bar_p, np0))) break;
+                    np0 ^= 1;
+                    tc_fence_after();
+                    output(0, vslot, b > lo0);
+                    if (b == hi0) commit(lead, bar_o);
                 }
+                if (ok && more) {
+                    next();
+                    ok = await(fb + 8 * slot, phase);
+                    if (ok && b + 1 >= lo0 && b + 1 <= hi0) scores(0, slot);
+                }
+                if (ok && b >= lo1 && b <= hi1) {
+                    if (!(ok = await(bar_p + 8, np1))) break;
+                    np1 ^= 1;
+                    tc_fence_after();
+                    output(1, vslot, b > lo1);
+                    if (b == hi1) commit(lead, bar_o + 8);
+                }
+                if (ok && more && b + 1 >= lo1 && b + 1 <= hi1) scores(1, slot);
                 if (ok) {
-                    mma_commit(bar_empty + 8 * vslot);
-                    if (more) mma_commit(bar_empty + 8 * kslot);
+                    commit(lead, eb + 8 * vslot);
+                    if (more) commit(lead, eb + 8 * slot);
                 }
             }
             if (!ok) {   // products already issued end before TMEM goes away
-                mma_commit(bar_drain);
+                commit(lead, bar_drain);
                 mbar_wait(bar_drain, 0, kWaitLimit);
             }
         } else if (warp >= 2 && hi >= lo) {
@@ -378,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 4; ++i) loaded(r[i]);
-            if (masked(u, b, P.window)) {
+            if (masked(u, b)) {
                 const int last = u.place + row - b * kTileKeys, first = P.window > 0 ? last - P.window + 1 : 0;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
