@@ -256,7 +256,8 @@ kdn_status kdn_prompt_attention(int n_seq, int total_q, int total_k, int H, int 
     a.status = static_cast<uint32_t*>(workspace);
     a.scratch = static_cast<char*>(workspace) + kStatusBytes;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
+    // the status word and the kernel's item counter beside it
+    if (cudaMemsetAsync(a.status, 0, 2 * sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
     if (!any) return KDN_OK;
     return done(kdn::launch_prompt_attention(a, s));
 }

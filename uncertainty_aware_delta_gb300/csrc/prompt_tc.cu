@@ -28,11 +28,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
-constexpr int kThreads = 384;                 // loader, MMA, 2 guard warps; 2 softmax warpgroups
-constexpr int kGuardThreads = 64;
+constexpr int kThreads = 384;                 // loader, products, guard and finder warps; 2 softmax warpgroups
+constexpr int kItems = 3, kChunks = 128;     // items known ahead; chunks of sequences
 // registers: launched with 168 a thread (3 x 128 x 168); 88 + 2 x 208 = 3 x 168
 constexpr int kAuxRegs = 88, kSoftmaxRegs = 208;
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
+constexpr int kSMs = 152;                     // GB300
 constexpr float kLazy = 8.0f;                 // powers of two a score may pass the running maximum by
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -44,8 +45,8 @@ struct PromptParams {
     const int32_t *cu_q, *cu_k;
     __nv_bfloat16* o;
     float* lse;
-    uint32_t* status;
-    int n_seq, total_q, total_k, H, H_kv, window, groups, items, probe;
+    uint32_t *status, *counter;   // counter: items taken
+    int n_seq, total_q, total_k, H, H_kv, window, groups, items, chunk, chunks, probe, wide;
     float scale_log2;
 };
 
@@ -64,6 +65,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
+}
+// One look at a barrier, without the suspension of mbar_try_wait (which costs some 300 cycles
+// even where the phase is complete).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -117,20 +128,23 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// What a block works on.
+// What a block works on: a row tile of one sequence and a group of heads.
 struct Item {
     int q0, n_q, k0, n_k;    // the sequence's rows
-    int row;                 // first row of the item in its sequence; negative: nothing to do
+    int row;                 // first row of the item in its sequence; negative: no more items
+    int group;
 };
 struct Unit {
     int head, row, rows;     // rows: valid ones
     int place;               // place of its first row among the keys
     int lo, hi;              // key tiles; hi < lo: none
     int all_from, all_to;    // of these, tiles all_from < b < all_to are seen whole by every valid row
+    __device__ __forceinline__ bool any() const { return hi >= lo; }
+    __device__ __forceinline__ bool masked(int b) const { return b >= all_to || b <= all_from; }
 };
-template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int h0, int window) {
+template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int window) {
     Unit u;
-    u.head = PAIR ? h0 + s : h0;
+    u.head = PAIR ? 2 * it.group + s : it.group;
     u.row = it.row + (PAIR ? 0 : s * kTileRows);
     u.rows = min(kTileRows, it.n_q - u.row);
     u.place = it.n_k - it.n_q + u.row;
@@ -141,90 +155,126 @@ template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int
     u.all_from = window > 0 && last >= window ? (last - window) / kTileKeys : -1;
     return u;
 }
-__device__ __forceinline__ bool masked(const Unit& u, int b) { return b >= u.all_to || b <= u.all_from; }
+// Key tiles of an item: all, and those the guard looks at (all that some unit masks).
+struct Tiles {
+    int lo, hi, cut_from, cut_to;
+    __device__ __forceinline__ bool cut(int b) const { return b >= cut_to || b <= cut_from; }
+};
+__device__ __forceinline__ Tiles tiles_of(const Unit& u0, const Unit& u1) {
+    const bool a0 = u0.any(), a1 = u1.any();
+    Tiles t;
+    t.lo = min(a0 ? u0.lo : 0x7ffffff0, a1 ? u1.lo : 0x7ffffff0);
+    t.hi = max(a0 ? u0.hi : -1, a1 ? u1.hi : -1);
+    t.cut_to = min(a0 ? u0.all_to : 0x7fffffff, a1 ? u1.all_to : 0x7fffffff);
+    t.cut_from = max(a0 ? u0.all_from : -1, a1 ? u1.all_from : -1);
+    return t;
+}
 
+// 32 bytes, at once (a whole sector) where the output starts on 32 bytes
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&x)[8], bool wide) {
+    if (!wide) {
+        uint4* q = reinterpret_cast<uint4*>(p);
+        q[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        q[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
+// Values that are not finite in the tiles that the guard looked at, added to a row that sees
+// them (channels i .. i + 31; its weights are positive, so they come out as they are).
+template <bool PAIR>
+__device__ __forceinline__ void give_back(const PromptParams& P, const Item& it, int last, int head, int i, uint32_t (&x)[32]) {
+    const Tiles t = tiles_of(unit_of<PAIR>(it, 0, P.window), unit_of<PAIR>(it, 1, P.window));
+    const int first = P.window > 0 ? last - P.window + 1 : 0, kvh = head / (P.H / P.H_kv);
+#pragma unroll 1
+    for (int b = t.lo; b <= t.hi; ++b) {
+        if (!t.cut(b)) continue;
+#pragma unroll 1
+        for (int k = max(b * kTileKeys, first); k <= min(b * kTileKeys + kTileKeys - 1, last); ++k) {
+            const __nv_bfloat16* v = P.v + (static_cast<long long>(it.k0) + k) * P.v_row + kvh * P.v_head + i;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float y = __bfloat162float(v[j]);
+                if ((__float_as_uint(y) & 0x7f800000u) == 0x7f800000u) x[j] = __float_as_uint(__uint_as_float(x[j]) + y);
+            }
+        }
+    }
+}
+
+// Blocks stay (one an SM) and take items from a counter.  Warp 0 loads, warps 1 and 2 issue
+// the units' products, warp 3 finds the items and guards; the softmax warpgroups write the
+// outputs.  Everything is counted on from item to item, so the next item's first products run
+// while the last one's outputs are written.
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptParams P) {
     using L = Layout<D>;
+    constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * L::kSlots + 16];
-    __shared__ Item item;
-    __shared__ int before[kThreads / 32], dirty;
+    __shared__ uint64_t bars[2 * L::kSlots + 20 + 2 * kItems];
+    __shared__ Item items[kItems];
+    __shared__ int chunk_tiles[kChunks], dirty[kItems];
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes;
     const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * L::kSlots, bar_q = bar_empty + 8 * L::kSlots,
-                   bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_v = bar_o + 16, bar_cut = bar_v + 32, bar_drain = bar_cut + 32;
+                   bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
+                   bar_o_free = bar_o + 16, bar_v = bar_o_free + 16, bar_cut = bar_v + 32, bar_item = bar_cut + 32,
+                   bar_item_free = bar_item + 8 * kItems, bar_drain = bar_item_free + 8 * kItems;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = blockIdx.x % P.groups;
-    // the longest rows first: each sequence's last tiles have the most keys
-    const int want = P.items - 1 - static_cast<int>(blockIdx.x / P.groups);
 
-    // ---- the item: sequences' tiles one after another, found by a scan over all sequences
-    constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
-    {
-        const int per = (P.n_seq + kThreads - 1) / kThreads, s0 = min(tid * per, P.n_seq), s1 = min(s0 + per, P.n_seq);
-        auto tiles_of = [&](int s, Item& it) {
-            const int q0 = P.cu_q[s], q1 = P.cu_q[s + 1], k0 = P.cu_k[s], k1 = P.cu_k[s + 1];
-            if (q0 < 0 || q1 < q0 || q1 > P.total_q || k0 < 0 || k1 < k0 || k1 > P.total_k) {
-                if (blockIdx.x == 0) set_status(P.status, kStatusRange);
-                return 0;
-            }
-            it = Item{q0, q1 - q0, k0, k1 - k0, 0};
-            return (q1 - q0 + kItemRows - 1) / kItemRows;
-        };
-        Item it;
-        int mine = 0;
-        for (int s = s0; s < s1; ++s) mine += tiles_of(s, it);
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kAll, upto, o);
-            if (lane >= o) upto += y;
+    if (tid == 0) {
+        aborted = 0;
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 2);   // both units' products
         }
-        if (lane == 31) before[warp] = upto;
-        if (tid == 0) {
-            item.row = -1;
-            aborted = 0;
-            dirty = 0;
-            for (int i = 0; i < L::kSlots; ++i) {
-                mbar_init(bar_full + 8 * i, 1);
-                mbar_init(bar_empty + 8 * i, 1);
-            }
-            mbar_init(bar_q, 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(bar_s + 8 * i, 1);
-                mbar_init(bar_p + 8 * i, 4);
-                mbar_init(bar_o + 8 * i, 1);
-            }
-            // four in turn: the loader may be several tiles ahead of the guard, and it of the products
-            for (int i = 0; i < 4; ++i) {
-                mbar_init(bar_v + 8 * i, kGuardThreads);
-                mbar_init(bar_cut + 8 * i, 1);
-            }
-            mbar_init(bar_drain, 1);   // also the probe's: completed by nothing before the end
-            mbar_fence_init();
+        mbar_init(bar_q, 1);
+        mbar_init(bar_q_free, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_s + 8 * i, 1);
+            mbar_init(bar_p + 8 * i, 4);
+            mbar_init(bar_o + 8 * i, 1);
+            mbar_init(bar_o_free + 8 * i, 4);
         }
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += before[w];
-        if (want < upto && want >= upto - mine) {
-            int x = upto - mine;
-            for (int s = s0; s < s1; ++s) {
-                const int n = tiles_of(s, it);
-                if (want < x + n) {
-                    it.row = (want - x) * kItemRows;
-                    item = it;
-                    break;
-                }
-                x += n;
-            }
+        // four in turn: the loader may be several tiles ahead of the guard, and it of the products
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar_v + 8 * i, 1);
+            mbar_init(bar_cut + 8 * i, 1);
         }
-        __syncthreads();
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(bar_item + 8 * i, 1);
+            mbar_init(bar_item_free + 8 * i, 4 + 8);   // loader, products, guard; softmax warps
+        }
+        mbar_init(bar_drain, 1);   // also the probe's: completed by nothing before the end
+        mbar_init(bar_drain + 8, 1);
+        mbar_fence_init();
     }
-    const Item it = item;
-    if (it.row < 0) return;   // fewer tiles than blocks
+    // row tiles of every chunk of sequences (32, or more where there are many)
+    auto tiles_of_sequence = [&](int s, Item& it) {
+        const int q0 = P.cu_q[s], q1 = P.cu_q[s + 1], k0 = P.cu_k[s], k1 = P.cu_k[s + 1];
+        if (q0 < 0 || q1 < q0 || q1 > P.total_q || k0 < 0 || k1 < k0 || k1 > P.total_k) {
+            if (blockIdx.x == 0) set_status(P.status, kStatusRange);
+            return 0;
+        }
+        it.q0 = q0; it.n_q = q1 - q0; it.k0 = k0; it.n_k = k1 - k0;
+        return (q1 - q0 + kItemRows - 1) / kItemRows;
+    };
+    for (int i = warp; i < P.chunks; i += kThreads / 32) {
+        int n = 0;
+        Item it;
+        for (int j = lane; j < P.chunk; j += 32)
+            if (i * P.chunk + j < P.n_seq) n += tiles_of_sequence(i * P.chunk + j, it);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+        if (lane == 0) chunk_tiles[i] = n;
+    }
+    __syncthreads();
     if (warp == 0) {
+        __syncwarp();
         tmem_alloc(smem_addr(&tmem_slot), kTmCols);
         tc_fence_before();
     }
@@ -232,17 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // a block's heads: two query heads of a key head, or one
-    const int rep = P.H / P.H_kv, h0 = PAIR ? 2 * group : group, kvh = h0 / rep;
-    Unit u0 = unit_of<PAIR>(it, 0, h0, P.window), u1 = unit_of<PAIR>(it, 1, h0, P.window);
-    const bool any0 = u0.hi >= u0.lo, any1 = u1.hi >= u1.lo;
-    const int lo = any0 && any1 ? min(u0.lo, u1.lo) : any0 ? u0.lo : u1.lo;
-    const int hi = any0 && any1 ? max(u0.hi, u1.hi) : any0 ? u0.hi : u1.hi;   // hi < lo: no key is seen
-    // tiles that the guard looks at: all that some unit masks
-    const int cut_to = min(any0 ? u0.all_to : 0x7fffffff, any1 ? u1.all_to : 0x7fffffff),
-              cut_from = max(any0 ? u0.all_from : -1, any1 ? u1.all_from : -1);
-    auto cut = [&](int b) { return b >= cut_to || b <= cut_from; };
     auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (mbar_test(bar, parity)) return true;
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
             if (aborted) return false;
@@ -251,295 +292,413 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         set_status(P.status, kStatusTimeout);
         return false;
     };
+    // the item in place n of a role's walk; false when the walk is over
+    auto take = [&](int n, Item& it, bool& ok) {
+        ok = wait(bar_item + 8 * (n % kItems), (n / kItems) & 1);
+        if (!ok) return false;
+        it = items[n % kItems];
+        return it.row >= 0;
+    };
+    auto release = [&](int n) { mbar_arrive(bar_item_free + 8 * (n % kItems)); };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
-        if (warp == 0 && lane == 0 && hi >= lo) {
+        if (warp == 0 && lane == 0) {
             // ---- loader: Q, then K and V tiles in turn
-            mbar_expect_tx(bar_q, (any0 ? L::kTileBytes : 0) + (any1 ? L::kTileBytes : 0));
-            for (int s = 0; s < 2; ++s) {
-                const Unit& u = s ? u1 : u0;
-                if (s ? any1 : any0)
-                    for (int f = 0; f < L::kHalves; ++f)
-                        tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row, bar_q);
-            }
-            int n = 0;
+            const int rep = P.H / P.H_kv;
+            int n = 0, nq = 0;
             uint32_t nc = 0;
             bool ok = true;
-            for (int b = lo; ok && b <= hi; ++b)
-                for (int i = 0; i < 2; ++i, ++n) {
-                    const int slot = n % L::kSlots;
-                    if (n >= L::kSlots && !wait(bar_empty + 8 * slot, (n / L::kSlots - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar_full + 8 * slot, L::kTileBytes);
-                    for (int f = 0; f < L::kHalves; ++f)
-                        tma_load_3d(skv + slot * L::kTileBytes + f * 16384, i ? &P.tv : &P.tk, 64 * f, kvh,
-                                    it.k0 + b * kTileKeys, bar_full + 8 * slot);
-                    if (i && cut(b)) mbar_arrive(bar_cut + 8 * (nc++ & 3));
-                    if (P.probe && n == 0) {
-                        if (!mbar_wait(bar_drain, 0, kProbeLimit)) {
+            Item it;
+            for (int w = 0; take(w, it, ok); ++w) {
+                release(w);
+                const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                const Tiles t = tiles_of(u0, u1);
+                if (t.hi < t.lo) continue;
+                const int kvh = u0.head / rep;
+                if (nq > 0 && !(ok = wait(bar_q_free, (nq - 1) & 1))) break;
+                mbar_expect_tx(bar_q, (u0.any() ? L::kTileBytes : 0) + (u1.any() ? L::kTileBytes : 0));
+                ++nq;
+                for (int s = 0; s < 2; ++s) {
+                    const Unit& u = s ? u1 : u0;
+                    if (u.any())
+                        for (int f = 0; f < L::kHalves; ++f)
+                            tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row, bar_q);
+                }
+                for (int b = t.lo; ok && b <= t.hi; ++b)
+                    for (int i = 0; i < 2; ++i) {
+                        const int slot = n % L::kSlots;
+                        if (n >= L::kSlots && !(ok = wait(bar_empty + 8 * slot, (n / L::kSlots - 1) & 1))) break;
+                        mbar_expect_tx(bar_full + 8 * slot, L::kTileBytes);
+                        for (int f = 0; f < L::kHalves; ++f)
+                            tma_load_3d(skv + slot * L::kTileBytes + f * 16384, i ? &P.tv : &P.tk, 64 * f, kvh,
+                                        it.k0 + b * kTileKeys, bar_full + 8 * slot);
+                        ++n;
+                        if (i && t.cut(b)) mbar_arrive(bar_cut + 8 * (nc++ & 3));
+                        if (P.probe && n == 1 && !mbar_wait(bar_drain, 0, kProbeLimit)) {
                             aborted = 1;
                             set_status(P.status, kStatusTimeout);
                         }
+                        if (aborted) {
+                            ok = false;
+                            break;
+                        }
                     }
-                    if (aborted) {
-                        ok = false;
-                        ++n;
-                        break;
-                    }
-                }
-            if (!ok) {   // copies already issued land before the block's shared memory goes away
-                mbar_wait(bar_q, 0, kWaitLimit);
+                if (!ok) break;
+            }
+            if (aborted) {   // copies already issued land before the block's shared memory goes away
+                if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, kWaitLimit);
                 for (int j = max(n - L::kSlots, 0); j < n; ++j)
                     mbar_wait(bar_full + 8 * (j % L::kSlots), (j / L::kSlots) & 1, kWaitLimit);
             }
-        } else if (warp == 1 && hi >= lo) {
-            // ---- MMA: P V of a key tile and Q K^T of the next, unit after unit
+        } else if (warp == 1 || warp == 2) {
+            // ---- products of a unit: P V of a key tile, then Q K^T of the next (of this item or the one after it).
+            // A warp a unit: while one waits for its weights, the other's products run.
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0, 0), id_o = idesc_bf16(128, D, 0, 1, 0);
             const uint32_t lead = elect_one();
             auto one = [](int x) { return __shfl_sync(kAll, x, 0); };
-            const int first = one(lo), last = one(hi), lo0 = one(any0 ? u0.lo : 0x7ffffff0), hi0 = one(any0 ? u0.hi : -1),
-                      lo1 = one(any1 ? u1.lo : 0x7ffffff0), hi1 = one(any1 ? u1.hi : -1), c_to = one(cut_to), c_from = one(cut_from);
-            const uint32_t tm = one(tmem), q = one(sq), kv = one(skv), fb = one(bar_full), eb = one(bar_empty);
+            const int s = one(warp - 1);
+            const uint32_t ts = one(tmem) + kTmS + 128 * s, to = one(tmem) + kTmO + 128 * s, fb = one(bar_full), eb = one(bar_empty),
+                           bs = one(bar_s) + 8 * s, bp = one(bar_p) + 8 * s, bo = one(bar_o) + 8 * s, bf = one(bar_o_free) + 8 * s;
             auto await = [&](uint32_t bar, uint32_t parity) { return __all_sync(kAll, wait(bar, parity)); };
-            const uint64_t qd = sw128_desc(q, 16, 1024), kd = sw128_desc(kv, 16, 1024), vd = sw128_desc(kv, 16384, 1024);
-            auto scores = [&](int s, int slot) {
-                const uint64_t a = desc_add(qd, s * L::kTileBytes), b = desc_add(kd, slot * L::kTileBytes);
+            const uint64_t qd = sw128_desc(one(sq) + s * L::kTileBytes, 16, 1024), kd = sw128_desc(one(skv), 16, 1024),
+                           vd = sw128_desc(one(skv), 16384, 1024);
+            auto scores = [&](int slot) {
+                const uint64_t b = desc_add(kd, slot * L::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-                    mma_ss(lead, tm + kTmS + 128 * s, desc_add(a, off), desc_add(b, off), id_s, k > 0);
+                    mma_ss(lead, ts, desc_add(qd, off), desc_add(b, off), id_s, k > 0);
                 }
-                commit(lead, bar_s + 8 * s);
+                commit(lead, bs);
             };
-            auto output = [&](int s, int slot, bool add) {
+            auto output = [&](int slot, bool add) {
                 const uint64_t b = desc_add(vd, slot * L::kTileBytes);
 #pragma unroll
-                for (int k = 0; k < kTileKeys / 16; ++k)
-                    mma_ts(lead, tm + kTmO + 128 * s, tm + kTmS + 128 * s + 8 * k, desc_add(b, k * 2048), id_o, k > 0 ? 1u : add);
+                for (int k = 0; k < kTileKeys / 16; ++k) mma_ts(lead, to, ts + 8 * k, desc_add(b, k * 2048), id_o, k > 0 ? 1u : add);
             };
-            bool ok = await(bar_q, 0) && await(fb, 0);
-            if (ok) {
-                tc_fence_after();
-                if (first >= lo0) scores(0, 0);
-                if (first >= lo1) scores(1, 0);
-                commit(lead, eb);
-            }
-            uint32_t slot = 0, phase = 0;   // of the tile used last
+            struct Walk {   // key tile b of an item (tiles lo .. hi), of which the unit has mine_lo .. mine_hi
+                int b, lo, hi, mine_lo, mine_hi, cut_from, cut_to;
+            };
+            int w = 0;
+            bool ok = true;
+            // the first tile of the next item that has any; false when there is none
+            auto next_item = [&](Walk& x) {
+                for (;;) {
+                    Item it;
+                    bool fine;
+                    const bool got = take(w, it, fine);
+                    if (!__all_sync(kAll, fine)) {
+                        ok = false;
+                        return false;
+                    }
+                    if (!one(got)) return false;
+                    if (lead) release(w);
+                    ++w;
+                    const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                    const Unit& u = s ? u1 : u0;
+                    const Tiles t = tiles_of(u0, u1);
+                    x = Walk{one(t.lo), one(t.lo), one(t.hi), one(u.any() ? u.lo : 0x7ffffff0), one(u.any() ? u.hi : -1),
+                             one(t.cut_from), one(t.cut_to)};
+                    if (x.hi >= x.lo) return true;
+                }
+            };
+            uint32_t slot = L::kSlots - 1, phase = 1;   // of the tile used last
             auto next = [&]() {
                 if (++slot == L::kSlots) {
                     slot = 0;
                     phase ^= 1;
                 }
             };
-            uint32_t np0 = 0, np1 = 0, nv = 0;
-            for (int b = first; ok && b <= last; ++b) {
-                const bool more = b < last;
+            uint32_t nq = 0, np = 0, no = 1, nv = 0;
+            // scores of the walk's tile, whose K is the next in the ring
+            auto begin = [&](const Walk& x) {
                 next();
-                const uint32_t vslot = slot;
-                ok = await(fb + 8 * vslot, phase);
-                if (ok && (b >= c_to || b <= c_from)) {
-                    ok = await(bar_v + 8 * (nv & 3), (nv >> 2) & 1);
+                if (!await(fb + 8 * slot, phase)) return false;
+                if (x.b == x.lo) {
+                    if (!await(bar_q, nq)) return false;
+                    nq ^= 1;
+                }
+                tc_fence_after();
+                if (x.b >= x.mine_lo && x.b <= x.mine_hi) scores(slot);
+                commit(lead, eb + 8 * slot);
+                if (x.b == x.hi) commit(lead, bar_q_free);
+                return true;
+            };
+            Walk cur, nxt;
+            bool more = next_item(cur);
+            if (more) ok = begin(cur);
+            while (ok && more) {
+                nxt = cur;
+                if (cur.b < cur.hi) ++nxt.b;
+                else more = next_item(nxt);
+                if (!ok) break;
+                next();
+                if (!(ok = await(fb + 8 * slot, phase))) break;
+                if (cur.b >= cur.cut_to || cur.b <= cur.cut_from) {
+                    if (!(ok = await(bar_v + 8 * (nv & 3), (nv >> 2) & 1))) break;
                     ++nv;
                 }
-                if (ok && b >= lo0 && b <= hi0) {
-                    if (!(ok = await(bar_p, np0))) break;
-                    np0 ^= 1;
+                if (cur.b >= cur.mine_lo && cur.b <= cur.mine_hi) {
+                    if (cur.b == cur.mine_lo) {   // the last item's output has been read
+                        if (!(ok = await(bf, no))) break;
+                        no ^= 1;
+                    }
+                    if (!(ok = await(bp, np))) break;
+                    np ^= 1;
                     tc_fence_after();
-                    output(0, vslot, b > lo0);
-                    if (b == hi0) commit(lead, bar_o);
+                    output(slot, cur.b > cur.mine_lo);
+                    if (cur.b == cur.mine_hi) commit(lead, bo);
                 }
-                if (ok && more) {
-                    next();
-                    ok = await(fb + 8 * slot, phase);
-                    if (ok && b + 1 >= lo0 && b + 1 <= hi0) scores(0, slot);
-                }
-                if (ok && b >= lo1 && b <= hi1) {
-                    if (!(ok = await(bar_p + 8, np1))) break;
-                    np1 ^= 1;
-                    tc_fence_after();
-                    output(1, vslot, b > lo1);
-                    if (b == hi1) commit(lead, bar_o + 8);
-                }
-                if (ok && more && b + 1 >= lo1 && b + 1 <= hi1) scores(1, slot);
-                if (ok) {
-                    commit(lead, eb + 8 * vslot);
-                    if (more) commit(lead, eb + 8 * slot);
-                }
+                commit(lead, eb + 8 * slot);
+                if (more && !(ok = begin(nxt))) break;
+                cur = nxt;
             }
             if (!ok) {   // products already issued end before TMEM goes away
-                commit(lead, bar_drain);
-                mbar_wait(bar_drain, 0, kWaitLimit);
+                commit(lead, bar_drain + 8 * s);
+                mbar_wait(bar_drain + 8 * s, 0, kWaitLimit);
             }
-        } else if (warp >= 2 && hi >= lo) {
-            // ---- guard: in tiles that some row does not see all of, a value that is not finite is taken out
-            // (a weight of zero would not stop it in the product), and keys past the sequence are zeroed; the
-            // rows that see such a value get it at the end
-            const int g = tid - 64;
-            uint32_t nv = 0;
-            for (int b = lo; b <= hi; ++b) {
-                if (!cut(b)) continue;
-                const int vn = 2 * (b - lo) + 1, slot = vn % L::kSlots;
-                // only once its copy is under way does the slot's phase tell whether it has landed
-                if (!wait(bar_cut + 8 * (nv & 3), (nv >> 2) & 1)) break;
-                if (!wait(bar_full + 8 * slot, (vn / L::kSlots) & 1)) break;
-                uint8_t* tile = smem_raw + (skv - smem_addr(smem_raw)) + slot * L::kTileBytes;
-                const int keys = it.n_k - b * kTileKeys;
-                for (int i = g; i < L::kTileBytes / 16; i += kGuardThreads) {
-                    uint4* p = reinterpret_cast<uint4*>(tile) + i;
-                    if (i % 1024 / 8 >= keys) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
+        } else if (warp == 3) {
+            // ---- finder: the next item, the longest rows first (a sequence's last tiles have the most keys); false
+            // when there is none
+            const int all = P.items * P.groups;
+            auto find = [&](int w) {
+                int found = -1;
+                Item it;
+                while (found < 0) {
+                    int i = 0;
+                    if (lane == 0) i = static_cast<int>(atomicAdd(P.counter, 1u));
+                    i = __shfl_sync(kAll, i, 0);
+                    if (i >= all) break;
+                    int want = P.items - 1 - i / P.groups;
+                    // its chunk of sequences
+                    int c = -1;
+                    for (int c0 = 0; c0 < P.chunks; c0 += 32) {
+                        const int mine = c0 + lane < P.chunks ? chunk_tiles[c0 + lane] : 0;
+                        int upto = mine;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int y = __shfl_up_sync(kAll, upto, o);
+                            if (lane >= o) upto += y;
+                        }
+                        const uint32_t hit = __ballot_sync(kAll, want < upto);
+                        if (hit) {
+                            const int at = __ffs(hit) - 1;
+                            c = c0 + at;
+                            want -= __shfl_sync(kAll, upto - mine, at);
+                            break;
+                        }
+                        want -= __shfl_sync(kAll, upto, 31);
                     }
-                    uint4 v = *p;
-                    // the exponent field's ones carry into the sign's place
-                    auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                    if (odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w)) {
-                        auto fix = [&](uint32_t w) {
-                            const uint32_t m = odd(w);
-                            return w & ~((m & 0x8000u ? 0xffffu : 0u) | (m & 0x80000000u ? 0xffff0000u : 0u));
-                        };
-                        *p = make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
-                        dirty = 1;
+                    if (c < 0) continue;   // fewer tiles than there could be
+                    for (int j0 = 0; j0 < P.chunk; j0 += 32) {
+                        const int q = c * P.chunk + j0 + lane;
+                        const int mine = j0 + lane < P.chunk && q < P.n_seq ? tiles_of_sequence(q, it) : 0;
+                        int upto = mine;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int y = __shfl_up_sync(kAll, upto, o);
+                            if (lane >= o) upto += y;
+                        }
+                        const uint32_t hit = __ballot_sync(kAll, want < upto);
+                        if (hit) {
+                            found = __ffs(hit) - 1;
+                            it.row = (want - (upto - mine)) * kItemRows;
+                            it.group = i % P.groups;
+                            break;
+                        }
+                        want -= __shfl_sync(kAll, upto, 31);
                     }
                 }
-                fence_proxy_async();
-                mbar_arrive(bar_v + 8 * (nv++ & 3));
+                if (found < 0) it.row = -1;
+                if (lane == max(found, 0)) {
+                    items[w % kItems] = it;
+                    dirty[w % kItems] = 0;
+                    mbar_arrive(bar_item + 8 * (w % kItems));
+                }
+                __syncwarp();
+                return found >= 0;
+            };
+            // ---- and guard: in tiles that some row does not see all of, a value that is not finite is taken out
+            // (a weight of zero would not stop it in the product), and keys past the sequence are zeroed; the
+            // rows that see such a value get it at the end
+            int n = 0;
+            uint32_t nv = 0;
+            bool ok = true, left = find(0);
+            for (int w = 0; ok; ++w) {
+                if (left) {   // one item ahead
+                    if (w + 1 >= kItems)
+                        ok = __all_sync(kAll, wait(bar_item_free + 8 * ((w + 1) % kItems), ((w + 1) / kItems - 1) & 1));
+                    if (!ok) break;
+                    left = find(w + 1);
+                }
+                Item it = items[w % kItems];
+                if (it.row < 0) break;
+                const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                const Tiles t = tiles_of(u0, u1);
+                for (int b = t.lo; b <= t.hi; ++b, n += 2) {
+                    if (!t.cut(b)) continue;
+                    const int slot = (n + 1) % L::kSlots;
+                    // only once its copy is under way does the slot's phase tell whether it has landed
+                    ok = __all_sync(kAll, wait(bar_cut + 8 * (nv & 3), (nv >> 2) & 1)) &&
+                         __all_sync(kAll, wait(bar_full + 8 * slot, ((n + 1) / L::kSlots) & 1));
+                    if (!ok) break;
+                    uint8_t* tile = smem_raw + (skv - smem_addr(smem_raw)) + slot * L::kTileBytes;
+                    const int keys = it.n_k - b * kTileKeys;
+                    int found = 0;
+#pragma unroll 4
+                    for (int i = lane; i < L::kTileBytes / 16; i += 32) {
+                        uint4* p = reinterpret_cast<uint4*>(tile) + i;
+                        if (i % 1024 / 8 >= keys) {
+                            *p = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint4 v = *p;
+                        // the exponent field's ones carry into the sign's place
+                        auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                        if (odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w)) {
+                            auto fix = [&](uint32_t x) {
+                                const uint32_t m = odd(x);
+                                return x & ~((m & 0x8000u ? 0xffffu : 0u) | (m & 0x80000000u ? 0xffff0000u : 0u));
+                            };
+                            *p = make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
+                            found = 1;
+                        }
+                    }
+                    if (__any_sync(kAll, found)) dirty[w % kItems] = 1;
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_v + 8 * (nv & 3));
+                    ++nv;
+                }
+                if (ok && lane == 0) release(w);
             }
         }
     } else {
-        // ---- softmax: warpgroup s has unit s, a row a thread
+        // ---- softmax and output: warpgroup s has unit s, a row a thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = (warp - 4) / 4, row = tid % 128;
-        const Unit u = s ? u1 : u0;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + kTmS + 128 * s + lanes, to = tmem + kTmO + 128 * s + lanes;
         const float c = P.scale_log2;
-        float m = -INFINITY, l = 0.f;   // m: running maximum, in powers of two
+        uint32_t ns = 0, no = 0;
         bool ok = true;
-        for (int b = u.lo; b <= u.hi; ++b) {
-            if (!(ok = __all_sync(kAll, wait(bar_s + 8 * s, (b - u.lo) & 1)))) break;
-            tc_fence_after();
-            uint32_t r[4][32];
+        Item it;
+        for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
+            const Unit u = unit_of<PAIR>(it, s, P.window);
+            float m = -INFINITY, l = 0.f;   // m: running maximum, in powers of two
+            for (int b = u.lo; b <= u.hi; ++b) {
+                if (!(ok = __all_sync(kAll, wait(bar_s + 8 * s, ns)))) break;
+                ns ^= 1;
+                tc_fence_after();
+                uint32_t r[4][32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, r[i]);
-            tmem_wait_ld();
+                for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, r[i]);
+                tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) loaded(r[i]);
-            if (masked(u, b)) {
-                const int last = u.place + row - b * kTileKeys, first = P.window > 0 ? last - P.window + 1 : 0;
+                for (int i = 0; i < 4; ++i) loaded(r[i]);
+                if (u.masked(b)) {
+                    const int last = u.place + row - b * kTileKeys, first = P.window > 0 ? last - P.window + 1 : 0;
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > last || i < first) r[i / 32][i % 32] = 0xff800000u;
-            }
-            float t0 = -INFINITY, t1 = -INFINITY;
+                    for (int i = 0; i < 128; ++i)
+                        if (i > last || i < first) r[i / 32][i % 32] = 0xff800000u;
+                }
+                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                t0 = fmaxf(t0, fmaxf(__uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1])));
-                t1 = fmaxf(t1, fmaxf(__uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1])));
-            }
-            float t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                t2 = fmaxf(t2, fmaxf(__uint_as_float(r[2][i]), __uint_as_float(r[2][i + 1])));
-                t3 = fmaxf(t3, fmaxf(__uint_as_float(r[3][i]), __uint_as_float(r[3][i + 1])));
-            }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
-            const bool raise = top > m + kLazy;
-            if (__any_sync(kAll, raise)) {
-                const float f = raise ? ex2(m - top) : 1.f;   // (0 from -infinity)
-                if (raise) m = top;
-                l *= f;
-                if (b > u.lo) {
-                    // the scores are complete, so the product before them is: O may be changed
+                for (int i = 0; i < 32; i += 2) {
+                    t0 = fmaxf(t0, fmaxf(__uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1])));
+                    t1 = fmaxf(t1, fmaxf(__uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1])));
+                    t2 = fmaxf(t2, fmaxf(__uint_as_float(r[2][i]), __uint_as_float(r[2][i + 1])));
+                    t3 = fmaxf(t3, fmaxf(__uint_as_float(r[3][i]), __uint_as_float(r[3][i + 1])));
+                }
+                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
+                const bool raise = top > m + kLazy;
+                if (__any_sync(kAll, raise)) {
+                    const float f = raise ? ex2(m - top) : 1.f;   // (0 from -infinity)
+                    if (raise) m = top;
+                    l *= f;
+                    if (b > u.lo) {
+                        // the scores are complete, so the product before them is: O may be changed
 #pragma unroll 1
-                    for (int i = 0; i < D; i += 32) {
-                        uint32_t x[32];
-                        tmem_ld32(to + i, x);
-                        tmem_wait_ld();
-                        loaded(x);
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(to + i, x);
+                            tmem_wait_ld();
+                            loaded(x);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                        tmem_st32(to + i, x);
+                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                            tmem_st32(to + i, x);
+                        }
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : -m;
-            const float2 cc = make_float2(c, c), bb = make_float2(base, base);
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                const float base = m == -INFINITY ? 0.f : -m;
+                const float2 cc = make_float2(c, c), bb = make_float2(base, base);
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int at = 2 * (i % 16);
-                    uint32_t(&x)[32] = r[2 * h + i / 16];
-                    float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, bb);
-                    y.x = ex2(y.x);
-                    y.y = ex2(y.y);
-                    if (i & 1) sum1 = add2(sum1, y);
-                    else sum0 = add2(sum0, y);
-                    p[i] = pack_bf16(y.x, y.y);
+                    for (int i = 0; i < 32; ++i) {
+                        const int at = 2 * (i % 16);
+                        uint32_t(&x)[32] = r[2 * h + i / 16];
+                        float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, bb);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        if (i & 1) sum1 = add2(sum1, y);
+                        else sum0 = add2(sum0, y);
+                        p[i] = pack_bf16(y.x, y.y);
+                    }
+                    tmem_st32(ts + 32 * h, p);
                 }
-                tmem_st32(ts + 32 * h, p);
+                sum0 = add2(sum0, sum1);
+                l += sum0.x + sum0.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_p + 8 * s);
             }
-            sum0 = add2(sum0, sum1);
-            l += sum0.x + sum0.y;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_p + 8 * s);
-        }
-        // ---- output
-        const bool some = u.hi >= u.lo;
-        if (ok && some) ok = __all_sync(kAll, wait(bar_o + 8 * s, 0));
-        if (ok && u.rows > 0) {
-            tc_fence_after();
+            if (!ok) break;
+            if (u.any()) {
+                if (!(ok = __all_sync(kAll, wait(bar_o + 8 * s, no)))) break;
+                no ^= 1;
+                tc_fence_after();
+            }
             const float f = l != 0.f ? 1.f / l : 0.f;
             const bool mine = row < u.rows;
             const long long at = static_cast<long long>(it.q0 + u.row + row) * P.H + u.head;
+            // (set, if at all, before the products that bar_o told of)
+            const bool add = u.any() && *const_cast<volatile int*>(&dirty[w % kItems]);
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
+            for (int i = 0; i < D && u.rows > 0; i += 32) {
                 uint32_t x[32];
                 __syncwarp();
-                if (some) {
+                if (u.any()) {
                     tmem_ld32(to + i, x);
                     tmem_wait_ld();
                     loaded(x);
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = some ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
-                if (dirty && mine) {   // what the guard took out and this row sees
-                    const int last = u.place + row, first = P.window > 0 ? last - P.window + 1 : 0;
-                    for (int b = lo; b <= hi; ++b) {
-                        if (!cut(b)) continue;
-                        for (int k = max(b * kTileKeys, first); k <= min(b * kTileKeys + kTileKeys - 1, last); ++k) {
-                            const __nv_bfloat16* v = P.v + (static_cast<long long>(it.k0) + k) * P.v_row + kvh * P.v_head + i;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float y = __bfloat162float(v[j]);
-                                if ((__float_as_uint(y) & 0x7f800000u) == 0x7f800000u)
-                                    x[j] = __float_as_uint(__uint_as_float(x[j]) + y);
-                            }
-                        }
-                    }
+                if (i == D - 32) {   // the next item may have O
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && u.any()) mbar_arrive(bar_o_free + 8 * s);
                 }
-                if (mine) {
-                    uint4* o = reinterpret_cast<uint4*>(P.o + at * D + i);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 w;
-                        w.x = pack_bf16(__uint_as_float(x[8 * j]), __uint_as_float(x[8 * j + 1]));
-                        w.y = pack_bf16(__uint_as_float(x[8 * j + 2]), __uint_as_float(x[8 * j + 3]));
-                        w.z = pack_bf16(__uint_as_float(x[8 * j + 4]), __uint_as_float(x[8 * j + 5]));
-                        w.w = pack_bf16(__uint_as_float(x[8 * j + 6]), __uint_as_float(x[8 * j + 7]));
-                        o[j] = w;
+                for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
+                if (add && mine) give_back<PAIR>(P, it, u.place + row, u.head, i, x);
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            y[k] = pack_bf16(__uint_as_float(x[16 * j + 2 * k]), __uint_as_float(x[16 * j + 2 * k + 1]));
+                        store32(P.o + at * D + i + 16 * j, y, P.wide);
                     }
                 }
             }
             if (mine) P.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            __syncwarp();
+            if (lane == 0) release(w);
         }
     }
     tc_fence_before();
@@ -600,10 +759,14 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
     P.items = a.total_q / rows + (a.n_seq < a.total_q ? a.n_seq : a.total_q);
     const long long grid = static_cast<long long>(P.items) * P.groups;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    P.counter = a.status + 1;
+    P.wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
+    P.chunk = 32 * ((a.n_seq + 32 * kChunks - 1) / (32 * kChunks));
+    P.chunks = (a.n_seq + P.chunk - 1) / P.chunk;
     const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Layout<D>::kSmem);
     if (e != cudaSuccess) return e;
-    prompt_tc_kernel<D, PAIR><<<static_cast<int>(grid), kThreads, Layout<D>::kSmem, s>>>(P);
+    prompt_tc_kernel<D, PAIR><<<static_cast<int>(grid < kSMs ? grid : kSMs), kThreads, Layout<D>::kSmem, s>>>(P);
     return cudaGetLastError();
 }
 
