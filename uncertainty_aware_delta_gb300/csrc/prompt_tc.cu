@@ -28,10 +28,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
-constexpr int kThreads = 384;                 // loader, products, guard and finder warps; 2 softmax warpgroups
+constexpr int kThreads = 384;                 // loader, two product warps, finder and guard; 2 softmax warpgroups
 constexpr int kItems = 3, kChunks = 128;     // items known ahead; chunks of sequences
-// registers: launched with 168 a thread (3 x 128 x 168); 88 + 2 x 208 = 3 x 168
-constexpr int kAuxRegs = 88, kSoftmaxRegs = 208;
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr int kSMs = 152;                     // GB300
 constexpr float kLazy = 8.0f;                 // powers of two a score may pass the running maximum by
@@ -46,15 +44,16 @@ struct PromptParams {
     __nv_bfloat16* o;
     float* lse;
     uint32_t *status, *counter;   // counter: items taken
-    int n_seq, total_q, total_k, H, H_kv, window, groups, items, chunk, chunks, probe, wide;
+    int n_seq, total_q, total_k, H, H_kv, window, groups, items, chunk, chunks, probe;
     float scale_log2;
 };
 
 template <int D> struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = kHalves * 16384;      // 128 rows of d bf16 in 128-byte-swizzled halves
-    static constexpr int kSlots = D == 128 ? 5 : 8;         // K and V tiles in turn
-    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
+    static constexpr int kSlots = D == 128 ? 4 : 8;         // K and V tiles in turn
+    static constexpr int kStage = 8 * 4096;                 // a box for each softmax warp: outputs of 32 rows, 64 channels
+    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + kStage + 1024;
 };
 
 // TMEM columns: scores (then weights) of the units, their outputs
@@ -170,19 +169,6 @@ __device__ __forceinline__ Tiles tiles_of(const Unit& u0, const Unit& u1) {
     return t;
 }
 
-// 32 bytes, at once (a whole sector) where the output starts on 32 bytes
-__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&x)[8], bool wide) {
-    if (!wide) {
-        uint4* q = reinterpret_cast<uint4*>(p);
-        q[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        q[1] = make_uint4(x[4], x[5], x[6], x[7]);
-        return;
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
-}
-
 // Values that are not finite in the tiles that the guard looked at, added to a row that sees
 // them (channels i .. i + 31; its weights are positive, so they come out as they are).
 template <bool PAIR>
@@ -213,17 +199,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     using L = Layout<D>;
     constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * L::kSlots + 20 + 2 * kItems];
+    __shared__ uint64_t bars[2 * L::kSlots + 22 + 2 * kItems];
     __shared__ Item items[kItems];
     __shared__ int chunk_tiles[kChunks], dirty[kItems];
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes;
+    const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes, stage = skv + L::kSlots * L::kTileBytes;
     const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * L::kSlots, bar_q = bar_empty + 8 * L::kSlots,
                    bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
                    bar_o_free = bar_o + 16, bar_v = bar_o_free + 16, bar_cut = bar_v + 32, bar_item = bar_cut + 32,
-                   bar_item_free = bar_item + 8 * kItems, bar_drain = bar_item_free + 8 * kItems;
+                   bar_item_free = bar_item + 8 * kItems, bar_turn = bar_item_free + 8 * kItems, bar_drain = bar_turn + 16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -237,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_p + 8 * i, 4);
+            mbar_init(bar_turn + 8 * i, 1);
             mbar_init(bar_o + 8 * i, 1);
             mbar_init(bar_o_free + 8 * i, 4);
         }
@@ -266,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     for (int i = warp; i < P.chunks; i += kThreads / 32) {
         int n = 0;
         Item it;
+#pragma unroll 1
         for (int j = lane; j < P.chunk; j += 32)
             if (i * P.chunk + j < P.n_seq) n += tiles_of_sequence(i * P.chunk + j, it);
 #pragma unroll
@@ -284,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (mbar_test(bar, parity)) return true;
+#pragma unroll 1
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
             if (aborted) return false;
@@ -302,7 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     auto release = [&](int n) { mbar_arrive(bar_item_free + 8 * (n % kItems)); };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         if (warp == 0 && lane == 0) {
             // ---- loader: Q, then K and V tiles in turn
             const int rep = P.H / P.H_kv;
@@ -325,7 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                         for (int f = 0; f < L::kHalves; ++f)
                             tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row, bar_q);
                 }
+#pragma unroll 1
                 for (int b = t.lo; ok && b <= t.hi; ++b)
+#pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
                         const int slot = n % L::kSlots;
                         if (n >= L::kSlots && !(ok = wait(bar_empty + 8 * slot, (n / L::kSlots - 1) & 1))) break;
@@ -353,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             }
         } else if (warp == 1 || warp == 2) {
             // ---- products of a unit: P V of a key tile, then Q K^T of the next (of this item or the one after it).
-            // A warp a unit: while one waits for its weights, the other's products run.
+            // A warp a unit, issuing in turn: all that a warp waits for, it waits for during the other's turn, and
+            // one unit's softmax runs beside the other's products (issued as they come, the two units' products
+            // share the tensor cores and both end late, and both softmaxes then run at once).
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0, 0), id_o = idesc_bf16(128, D, 0, 1, 0);
             const uint32_t lead = elect_one();
             auto one = [](int x) { return __shfl_sync(kAll, x, 0); };
@@ -410,49 +402,71 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     phase ^= 1;
                 }
             };
-            uint32_t nq = 0, np = 0, no = 1, nv = 0;
-            // scores of the walk's tile, whose K is the next in the ring
-            auto begin = [&](const Walk& x) {
+            uint32_t nq = 0, np = 0, no = 1, nv = 0, turn = s ^ 1;
+            const uint32_t my_turn = one(bar_turn) + 8 * s, other_turn = one(bar_turn) + 8 * (s ^ 1);
+            // K of the walk's tile, the next in the ring, has landed
+            auto have_keys = [&](const Walk& x) {
                 next();
                 if (!await(fb + 8 * slot, phase)) return false;
                 if (x.b == x.lo) {
                     if (!await(bar_q, nq)) return false;
                     nq ^= 1;
                 }
-                tc_fence_after();
-                if (x.b >= x.mine_lo && x.b <= x.mine_hi) scores(slot);
-                commit(lead, eb + 8 * slot);
-                if (x.b == x.hi) commit(lead, bar_q_free);
                 return true;
             };
-            Walk cur, nxt;
-            bool more = next_item(cur);
-            if (more) ok = begin(cur);
-            while (ok && more) {
+            auto take_turn = [&]() {
+                const bool got = await(my_turn, turn);
+                turn ^= 1;
+                tc_fence_after();
+                return got;
+            };
+            Walk cur = {}, nxt;
+            bool have = false;   // cur is a tile (its scores are under way)
+            while (ok) {
                 nxt = cur;
-                if (cur.b < cur.hi) ++nxt.b;
-                else more = next_item(nxt);
+                const bool fresh = !have || cur.b == cur.hi;
+                bool more = true;
+                if (fresh) more = next_item(nxt);
+                else ++nxt.b;
                 if (!ok) break;
-                next();
-                if (!(ok = await(fb + 8 * slot, phase))) break;
-                if (cur.b >= cur.cut_to || cur.b <= cur.cut_from) {
-                    if (!(ok = await(bar_v + 8 * (nv & 3), (nv >> 2) & 1))) break;
-                    ++nv;
-                }
-                if (cur.b >= cur.mine_lo && cur.b <= cur.mine_hi) {
-                    if (cur.b == cur.mine_lo) {   // the last item's output has been read
-                        if (!(ok = await(bf, no))) break;
-                        no ^= 1;
+                uint32_t vslot = 0;
+                bool mine = false;
+                if (have) {
+                    next();
+                    vslot = slot;
+                    if (!(ok = await(fb + 8 * vslot, phase))) break;
+                    if (cur.b >= cur.cut_to || cur.b <= cur.cut_from) {
+                        if (!(ok = await(bar_v + 8 * (nv & 3), (nv >> 2) & 1))) break;
+                        ++nv;
                     }
-                    if (!(ok = await(bp, np))) break;
-                    np ^= 1;
-                    tc_fence_after();
-                    output(slot, cur.b > cur.mine_lo);
-                    if (cur.b == cur.mine_hi) commit(lead, bo);
+                    mine = cur.b >= cur.mine_lo && cur.b <= cur.mine_hi;
+                    if (mine) {
+                        if (cur.b == cur.mine_lo) {   // the last item's output has been read
+                            if (!(ok = await(bf, no))) break;
+                            no ^= 1;
+                        }
+                        if (!fresh && !(ok = have_keys(nxt))) break;
+                        if (!(ok = await(bp, np))) break;
+                        np ^= 1;
+                    } else if (!fresh && !(ok = have_keys(nxt))) {
+                        break;
+                    }
+                    if (!(ok = take_turn())) break;
+                    if (mine) {
+                        output(vslot, cur.b > cur.mine_lo);
+                        if (cur.b == cur.mine_hi) commit(lead, bo);
+                    }
+                    commit(lead, eb + 8 * vslot);
+                    if (fresh && lead) mbar_arrive(other_turn);   // the next item's queries may be late: a turn of its own
                 }
+                if (!more) break;
+                if (fresh && !(ok = have_keys(nxt) && take_turn())) break;
+                if (nxt.b >= nxt.mine_lo && nxt.b <= nxt.mine_hi) scores(slot);
                 commit(lead, eb + 8 * slot);
-                if (more && !(ok = begin(nxt))) break;
+                if (nxt.b == nxt.hi) commit(lead, bar_q_free);
+                if (lead) mbar_arrive(other_turn);
                 cur = nxt;
+                have = true;
             }
             if (!ok) {   // products already issued end before TMEM goes away
                 commit(lead, bar_drain + 8 * s);
@@ -465,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             auto find = [&](int w) {
                 int found = -1;
                 Item it;
+#pragma unroll 1
                 while (found < 0) {
                     int i = 0;
                     if (lane == 0) i = static_cast<int>(atomicAdd(P.counter, 1u));
@@ -473,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     int want = P.items - 1 - i / P.groups;
                     // its chunk of sequences
                     int c = -1;
+#pragma unroll 1
                     for (int c0 = 0; c0 < P.chunks; c0 += 32) {
                         const int mine = c0 + lane < P.chunks ? chunk_tiles[c0 + lane] : 0;
                         int upto = mine;
@@ -491,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                         want -= __shfl_sync(kAll, upto, 31);
                     }
                     if (c < 0) continue;   // fewer tiles than there could be
+#pragma unroll 1
                     for (int j0 = 0; j0 < P.chunk; j0 += 32) {
                         const int q = c * P.chunk + j0 + lane;
                         const int mine = j0 + lane < P.chunk && q < P.n_seq ? tiles_of_sequence(q, it) : 0;
@@ -524,18 +541,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             // rows that see such a value get it at the end
             int n = 0;
             uint32_t nv = 0;
-            bool ok = true, left = find(0);
-            for (int w = 0; ok; ++w) {
+            bool ok = true, left = true;
+#pragma unroll 1
+            for (int w = -1; ok; ++w) {
                 if (left) {   // one item ahead
                     if (w + 1 >= kItems)
                         ok = __all_sync(kAll, wait(bar_item_free + 8 * ((w + 1) % kItems), ((w + 1) / kItems - 1) & 1));
                     if (!ok) break;
                     left = find(w + 1);
                 }
-                Item it = items[w % kItems];
+                if (w < 0) continue;
+                const Item it = items[w % kItems];
                 if (it.row < 0) break;
                 const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
                 const Tiles t = tiles_of(u0, u1);
+#pragma unroll 1
                 for (int b = t.lo; b <= t.hi; ++b, n += 2) {
                     if (!t.cut(b)) continue;
                     const int slot = (n + 1) % L::kSlots;
@@ -545,27 +565,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     if (!ok) break;
                     uint8_t* tile = smem_raw + (skv - smem_addr(smem_raw)) + slot * L::kTileBytes;
                     const int keys = it.n_k - b * kTileKeys;
-                    int found = 0;
-#pragma unroll 4
-                    for (int i = lane; i < L::kTileBytes / 16; i += 32) {
-                        uint4* p = reinterpret_cast<uint4*>(tile) + i;
-                        if (i % 1024 / 8 >= keys) {
-                            *p = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        const uint4 v = *p;
-                        // the exponent field's ones carry into the sign's place
-                        auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                        if (odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w)) {
-                            auto fix = [&](uint32_t x) {
-                                const uint32_t m = odd(x);
-                                return x & ~((m & 0x8000u ? 0xffffu : 0u) | (m & 0x80000000u ? 0xffff0000u : 0u));
-                            };
-                            *p = make_uint4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
-                            found = 1;
+                    uint4* v = reinterpret_cast<uint4*>(tile) + lane;
+                    constexpr int kPieces = L::kTileBytes / 16 / 32;   // a lane's
+                    if (keys < kTileKeys)
+#pragma unroll 1
+                        for (int i = 0; i < kPieces; ++i)
+                            if ((i * 32 + lane) % 1024 / 8 >= keys) v[i * 32] = make_uint4(0, 0, 0, 0);
+                    // where the exponent field is all ones, its sum with one carries into the sign's place
+                    auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                    uint32_t found = 0;
+#pragma unroll 1
+                    for (int i = 0; i < kPieces; i += 8) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = v[(i + j) * 32];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) found |= odd(x[j].x) | odd(x[j].y) | odd(x[j].z) | odd(x[j].w);
+                    }
+                    if (found) {
+                        uint32_t* word = reinterpret_cast<uint32_t*>(v);
+#pragma unroll 1
+                        for (int i = 0; i < 4 * kPieces; ++i) {
+                            uint32_t& x = word[i / 4 * 128 + i % 4];
+                            const uint32_t bad = odd(x);
+                            x &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
                         }
                     }
-                    if (__any_sync(kAll, found)) dirty[w % kItems] = 1;
+                    if (__any_sync(kAll, found != 0)) dirty[w % kItems] = 1;
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_v + 8 * (nv & 3));
@@ -576,7 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         }
     } else {
         // ---- softmax and output: warpgroup s has unit s, a row a thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = (warp - 4) / 4, row = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + kTmS + 128 * s + lanes, to = tmem + kTmO + 128 * s + lanes;
@@ -587,31 +612,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
             const Unit u = unit_of<PAIR>(it, s, P.window);
             float m = -INFINITY, l = 0.f;   // m: running maximum, in powers of two
+#pragma unroll 1
             for (int b = u.lo; b <= u.hi; ++b) {
                 if (!(ok = __all_sync(kAll, wait(bar_s + 8 * s, ns)))) break;
                 ns ^= 1;
                 tc_fence_after();
-                uint32_t r[4][32];
+                // Scores of keys 64 h .. 64 h + 63, what the row does not see at -infinity.  The second half is read
+                // twice, for the maximum and for the weights: TMEM gives 64 columns in some 60 cycles, and the code
+                // stays short (unrolled over 128 keys the kernel's code was several times the instruction
+                // cache, and every pass through a rarely run part of it cost thousands of cycles).
+                uint32_t x[64];
+                auto load = [&](int h) {
+                    tmem_ld32(ts + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                    tmem_ld32(ts + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                    tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, r[i]);
-                tmem_wait_ld();
+                    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
+                    if (u.masked(b)) {
+                        const int last = u.place + row - b * kTileKeys - 64 * h, first = P.window > 0 ? last - P.window + 1 : -64;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) loaded(r[i]);
-                if (u.masked(b)) {
-                    const int last = u.place + row - b * kTileKeys, first = P.window > 0 ? last - P.window + 1 : 0;
+                        for (int i = 0; i < 64; ++i)
+                            if (i > last || i < first) x[i] = 0xff800000u;
+                    }
+                };
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+                for (int h = 1; h >= 0; --h) {
+                    load(h);
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i > last || i < first) r[i / 32][i % 32] = 0xff800000u;
+                    for (int i = 0; i < 64; i += 4) {
+                        t0 = fmaxf(t0, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                        t1 = fmaxf(t1, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
+                    }
                 }
-                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    t0 = fmaxf(t0, fmaxf(__uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1])));
-                    t1 = fmaxf(t1, fmaxf(__uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1])));
-                    t2 = fmaxf(t2, fmaxf(__uint_as_float(r[2][i]), __uint_as_float(r[2][i + 1])));
-                    t3 = fmaxf(t3, fmaxf(__uint_as_float(r[3][i]), __uint_as_float(r[3][i + 1])));
-                }
-                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
+                const float top = fmaxf(t0, t1) * c;
                 const bool raise = top > m + kLazy;
                 if (__any_sync(kAll, raise)) {
                     const float f = raise ? ex2(m - top) : 1.f;   // (0 from -infinity)
@@ -634,14 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 const float base = m == -INFINITY ? 0.f : -m;
                 const float2 cc = make_float2(c, c), bb = make_float2(base, base);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
+                    if (h) load(1);
                     uint32_t p[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const int at = 2 * (i % 16);
-                        uint32_t(&x)[32] = r[2 * h + i / 16];
-                        float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc, bb);
+                        float2 y = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, bb);
                         y.x = ex2(y.x);
                         y.y = ex2(y.y);
                         if (i & 1) sum1 = add2(sum1, y);
@@ -665,9 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             }
             const float f = l != 0.f ? 1.f / l : 0.f;
             const bool mine = row < u.rows;
-            const long long at = static_cast<long long>(it.q0 + u.row + row) * P.H + u.head;
             // (set, if at all, before the products that bar_o told of)
             const bool add = u.any() && *const_cast<volatile int*>(&dirty[w % kItems]);
+            // 64 channels at a time through shared memory, so that a store instruction writes whole lines
+            const uint32_t box = stage + (warp - 4) * 4096;
+            const int row0 = u.row + (warp & 3) * 32, valid = u.rows - (warp & 3) * 32;
 #pragma unroll 1
             for (int i = 0; i < D && u.rows > 0; i += 32) {
                 uint32_t x[32];
@@ -685,18 +720,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
                 if (add && mine) give_back<PAIR>(P, it, u.place + row, u.head, i, x);
-                if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t y[8];
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t y[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            y[k] = pack_bf16(__uint_as_float(x[16 * j + 2 * k]), __uint_as_float(x[16 * j + 2 * k + 1]));
-                        store32(P.o + at * D + i + 16 * j, y, P.wide);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = pack_bf16(__uint_as_float(x[8 * j + 2 * k]), __uint_as_float(x[8 * j + 2 * k + 1]));
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(box + lane * 128 + (((i / 8 + j) ^ lane) & 7) * 16),
+                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                 : "memory");
+                }
+                if (i % 64 == 0) continue;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + lane / 8, k = lane % 8;
+                    uint4 y;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                 : "r"(box + r * 128 + ((k ^ r) & 7) * 16)
+                                 : "memory");
+                    if (r < valid)
+                        *reinterpret_cast<uint4*>(P.o + (static_cast<long long>(it.q0 + row0 + r) * P.H + u.head) * D + (i - 32) + 8 * k) = y;
                 }
             }
-            if (mine) P.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (mine)
+                P.lse[static_cast<long long>(it.q0 + u.row + row) * P.H + u.head] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             __syncwarp();
             if (lane == 0) release(w);
         }
@@ -760,7 +809,6 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
     const long long grid = static_cast<long long>(P.items) * P.groups;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     P.counter = a.status + 1;
-    P.wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
     P.chunk = 32 * ((a.n_seq + 32 * kChunks - 1) / (32 * kChunks));
     P.chunks = (a.n_seq + P.chunk - 1) / P.chunk;
     const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
