@@ -105,6 +105,8 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lead)
         : "memory");
 }
+// Ones in bits 0 .. n.
+__device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u; }
 // two fp32 operations an instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -445,14 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                             if (!(ok = await(bf, no))) break;
                             no ^= 1;
                         }
-                        if (!fresh && !(ok = have_keys(nxt))) break;
-                        if (!(ok = await(bp, np))) break;
-                        np ^= 1;
-                    } else if (!fresh && !(ok = have_keys(nxt))) {
-                        break;
                     }
+                    if (!fresh && !(ok = have_keys(nxt))) break;
                     if (!(ok = take_turn())) break;
                     if (mine) {
+                        if (!(ok = await(bp, np))) break;
+                        np ^= 1;
+                        tc_fence_after();
                         output(vslot, cur.b > cur.mine_lo);
                         if (cur.b == cur.mine_hi) commit(lead, bo);
                     }
@@ -629,10 +630,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 #pragma unroll
                     for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(x[i]));
                     if (u.masked(b)) {
-                        const int last = u.place + row - b * kTileKeys - 64 * h, first = P.window > 0 ? last - P.window + 1 : -64;
+                        const int last = u.place + row - b * kTileKeys - 64 * h, first = P.window > 0 ? last - P.window + 1 : 0;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i > last || i < first) x[i] = 0xff800000u;
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t seen = bits_to(last - 32 * i) & ~bits_to(first - 32 * i - 1);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(seen >> j & 1u)) x[32 * i + j] = 0xff800000u;
+                        }
                     }
                 };
                 float t0 = -INFINITY, t1 = -INFINITY;
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 }
                 if (i % 64 == 0) continue;
                 __syncwarp();
-#pragma unroll
+#pragma unroll 2
                 for (int j = 0; j < 8; ++j) {
                     const int r = 4 * j + lane / 8, k = lane % 8;
                     uint4 y;
