@@ -93,6 +93,28 @@ def test_longer(tmp_path):
                 ref.check(_np(o[i, h])[None], _np(lse[i, h]).reshape(1), w, "bf16")
 
 
+@pytest.mark.parametrize("d,H,hkv,lens", [(128, 4, 2, [100] * 700 + [300] * 100), (64, 3, 3, [1, 40, 129, 300] * 120),
+                                          (128, 2, 1, [700, 5, 260] * 110), (64, 8, 1, [128, 256, 384] * 60)])
+@pytest.mark.parametrize("window", [0, 90])
+def test_many_prompts(d, H, hkv, lens, window):
+    """Many more row tiles than SMs, of one key tile and of several, against the CUDA-core path."""
+    import torch
+    import uncertainty_aware_delta_gb300 as kdn
+
+    q, k, v, cu, _ = _inputs(lens, lens, H, hkv, d, "bf16", seed=9)
+    ws = torch.empty(kdn.prompt_attention_workspace_size(len(lens), q.shape[0], H, hkv, d), dtype=torch.uint8, device="cuda")
+    o, lse = kdn.kdn_prompt_attention(q, k, v, cu, window=window, workspace=ws)
+    assert kdn.kdn_read_device_status(ws) == 0
+    want, want_lse = kdn.kdn_prompt_attention(q, k, v, cu, window=window, flags=kdn.KDN_FLAG_PORTABLE)
+    # the weights' rounding to bf16 (2^-8 of at most max |v|) and both outputs' own
+    top = float(v.abs().max())
+    assert float((o.float() - want.float()).abs().max()) <= 3 * 2.0 ** -8 * top
+    assert float((o.float() - want.float()).norm() / want.float().norm()) <= 2.0 ** -8
+    assert float((lse - want_lse).abs().max()) <= 1e-4
+    again = kdn.kdn_prompt_attention(q, k, v, cu, window=window)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])

@@ -28,7 +28,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
-constexpr int kThreads = 384;                 // loader, two product warps, finder and guard; 2 softmax warpgroups
+constexpr int kThreads = 512;                 // loader, two product warps, finder and guard; 2 softmax and 1 output warpgroups
+// registers: launched with 128 a thread; 96 + 2 x 168 + 80 = 4 x 128
+constexpr int kAuxRegs = 96, kSoftmaxRegs = 168, kOutputRegs = 80;
 constexpr int kItems = 3, kChunks = 128;     // items known ahead; chunks of sequences
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr int kSMs = 152;                     // GB300
@@ -52,8 +54,9 @@ template <int D> struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = kHalves * 16384;      // 128 rows of d bf16 in 128-byte-swizzled halves
     static constexpr int kSlots = D == 128 ? 4 : 8;         // K and V tiles in turn
-    static constexpr int kStage = 8 * 4096;                 // a box for each softmax warp: outputs of 32 rows, 64 channels
-    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + kStage + 1024;
+    static constexpr int kStage = 4 * 4096;                 // a box for each output warp: 32 rows, 64 channels
+    static constexpr int kSums = 2 * 2 * 128 * 8;           // the rows' maxima and sums, of two items
+    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + kStage + kSums + 1024;
 };
 
 // TMEM columns: scores (then weights) of the units, their outputs
@@ -201,17 +204,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     using L = Layout<D>;
     constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * L::kSlots + 22 + 2 * kItems];
+    __shared__ uint64_t bars[2 * L::kSlots + 26 + 2 * kItems];
     __shared__ Item items[kItems];
     __shared__ int chunk_tiles[kChunks], dirty[kItems];
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes, stage = skv + L::kSlots * L::kTileBytes;
+    const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes, stage = skv + L::kSlots * L::kTileBytes, sums = stage + L::kStage;
     const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * L::kSlots, bar_q = bar_empty + 8 * L::kSlots,
                    bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
                    bar_o_free = bar_o + 16, bar_v = bar_o_free + 16, bar_cut = bar_v + 32, bar_item = bar_cut + 32,
-                   bar_item_free = bar_item + 8 * kItems, bar_turn = bar_item_free + 8 * kItems, bar_drain = bar_turn + 16;
+                   bar_item_free = bar_item + 8 * kItems, bar_turn = bar_item_free + 8 * kItems, bar_l = bar_turn + 16, bar_drain = bar_l + 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -226,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_p + 8 * i, 4);
             mbar_init(bar_turn + 8 * i, 1);
+            mbar_init(bar_l + 16 * i, 4);   // two a unit in turn: of an item of one tile, they may be there before the last
+            mbar_init(bar_l + 16 * i + 8, 4);   // item's have been read
             mbar_init(bar_o + 8 * i, 1);
             mbar_init(bar_o_free + 8 * i, 4);
         }
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(bar_item + 8 * i, 1);
-            mbar_init(bar_item_free + 8 * i, 4 + 8);   // loader, products, guard; softmax warps
+            mbar_init(bar_item_free + 8 * i, 4 + 12);   // loader, products, guard; softmax and output warps
         }
         mbar_init(bar_drain, 1);   // also the probe's: completed by nothing before the end
         mbar_init(bar_drain + 8, 1);
@@ -293,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     auto release = [&](int n) { mbar_arrive(bar_item_free + 8 * (n % kItems)); };
 
     if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         if (warp == 0 && lane == 0) {
             // ---- loader: Q, then K and V tiles in turn
             const int rep = P.H / P.H_kv;
@@ -601,13 +607,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 if (ok && lane == 0) release(w);
             }
         }
-    } else {
-        // ---- softmax and output: warpgroup s has unit s, a row a thread
+    } else if (warp < 12) {
+        // ---- softmax: warpgroup s has unit s, a row a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = (warp - 4) / 4, row = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + kTmS + 128 * s + lanes, to = tmem + kTmO + 128 * s + lanes;
         const float c = P.scale_log2;
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, nl = 0;   // nl: items that the unit was in
         bool ok = true;
         Item it;
         for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
@@ -697,60 +704,88 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             }
             if (!ok) break;
             if (u.any()) {
-                if (!(ok = __all_sync(kAll, wait(bar_o + 8 * s, no)))) break;
-                no ^= 1;
-                tc_fence_after();
+                asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(sums + (((nl & 1) * 2 + s) * 128 + row) * 8), "f"(m), "f"(l)
+                             : "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_l + 16 * s + 8 * (nl & 1));
+                ++nl;
             }
-            const float f = l != 0.f ? 1.f / l : 0.f;
-            const bool mine = row < u.rows;
-            // (set, if at all, before the products that bar_o told of)
-            const bool add = u.any() && *const_cast<volatile int*>(&dirty[w % kItems]);
-            // 64 channels at a time through shared memory, so that a store instruction writes whole lines
-            const uint32_t box = stage + (warp - 4) * 4096;
-            const int row0 = u.row + (warp & 3) * 32, valid = u.rows - (warp & 3) * 32;
+            if (lane == 0) release(w);
+        }
+    } else {
+        // ---- outputs of both units, a row a thread, while the softmax goes on with the next item
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
+        const int row = tid % 128;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, box = stage + (warp - 12) * 4096;
+        uint32_t no[2] = {0, 0};
+        bool ok = true;
+        Item it;
 #pragma unroll 1
-            for (int i = 0; i < D && u.rows > 0; i += 32) {
-                uint32_t x[32];
-                __syncwarp();
+        for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+                const Unit u = unit_of<PAIR>(it, s, P.window);
+                const uint32_t to = tmem + kTmO + 128 * s + lanes;
+                float m = 0.f, l = 0.f;
                 if (u.any()) {
-                    tmem_ld32(to + i, x);
-                    tmem_wait_ld();
-                    loaded(x);
+                    const uint32_t n = s ? no[1]++ : no[0]++;
+                    if (!(ok = __all_sync(kAll, wait(bar_l + 16 * s + 8 * (n & 1), n >> 1 & 1)) &&
+                               __all_sync(kAll, wait(bar_o + 8 * s, n & 1))))
+                        break;
+                    tc_fence_after();
+                    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(m), "=f"(l) : "r"(sums + (((n & 1) * 2 + s) * 128 + row) * 8) : "memory");
                 }
-                if (i == D - 32) {   // the next item may have O
-                    tc_fence_before();
+                const float f = l != 0.f ? 1.f / l : 0.f;
+                const bool mine = row < u.rows;
+                // (set, if at all, before the products that bar_o told of)
+                const bool add = u.any() && *const_cast<volatile int*>(&dirty[w % kItems]);
+                // 64 channels at a time through shared memory, so that a store instruction writes whole lines
+                const int row0 = u.row + (warp & 3) * 32, valid = u.rows - (warp & 3) * 32;
+#pragma unroll 1
+                for (int i = 0; i < D && u.rows > 0; i += 32) {
+                    uint32_t x[32];
                     __syncwarp();
-                    if (lane == 0 && u.any()) mbar_arrive(bar_o_free + 8 * s);
-                }
+                    if (u.any()) {
+                        tmem_ld32(to + i, x);
+                        tmem_wait_ld();
+                        loaded(x);
+                    }
+                    if (i == D - 32) {   // the next item may have O
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && u.any()) mbar_arrive(bar_o_free + 8 * s);
+                    }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
-                if (add && mine) give_back<PAIR>(P, it, u.place + row, u.head, i, x);
+                    for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
+                    if (add && mine) give_back<PAIR>(P, it, u.place + row, u.head, i, x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t y[4];
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t y[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = pack_bf16(__uint_as_float(x[8 * j + 2 * k]), __uint_as_float(x[8 * j + 2 * k + 1]));
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(box + lane * 128 + (((i / 8 + j) ^ lane) & 7) * 16),
-                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                 : "memory");
-                }
-                if (i % 64 == 0) continue;
-                __syncwarp();
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = pack_bf16(__uint_as_float(x[8 * j + 2 * k]), __uint_as_float(x[8 * j + 2 * k + 1]));
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(box + lane * 128 + (((i / 8 + j) ^ lane) & 7) * 16),
+                                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                     : "memory");
+                    }
+                    if (i % 64 == 0) continue;
+                    __syncwarp();
 #pragma unroll 2
-                for (int j = 0; j < 8; ++j) {
-                    const int r = 4 * j + lane / 8, k = lane % 8;
-                    uint4 y;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                                 : "r"(box + r * 128 + ((k ^ r) & 7) * 16)
-                                 : "memory");
-                    if (r < valid)
-                        *reinterpret_cast<uint4*>(P.o + (static_cast<long long>(it.q0 + row0 + r) * P.H + u.head) * D + (i - 32) + 8 * k) = y;
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = 4 * j + lane / 8, k = lane % 8;
+                        uint4 y;
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                     : "r"(box + r * 128 + ((k ^ r) & 7) * 16)
+                                     : "memory");
+                        if (r < valid)
+                            *reinterpret_cast<uint4*>(P.o + (static_cast<long long>(it.q0 + row0 + r) * P.H + u.head) * D + (i - 32) + 8 * k) = y;
+                    }
                 }
+                if (mine)
+                    P.lse[static_cast<long long>(it.q0 + u.row + row) * P.H + u.head] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
-            if (mine)
-                P.lse[static_cast<long long>(it.q0 + u.row + row) * P.H + u.head] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (!ok) break;
             __syncwarp();
             if (lane == 0) release(w);
         }
