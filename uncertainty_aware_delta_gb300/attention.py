@@ -12,7 +12,7 @@ import torch
 from .binding import KDN_BF16, KDN_F32, KDNError, library
 
 _IO = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
-_ITEM = {torch.bfloat16: 2, torch.float32: 4}
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone, without a Stream object
 
 
 class CachePlan(NamedTuple):
@@ -26,7 +26,7 @@ class CachePlan(NamedTuple):
     free_left: torch.Tensor    # [1] int32
 
 
-def _tensor(t, name, dtype, shape, device, dense=True):
+def _refuse(t, name, dtype, shape, device, dense):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.device != device:
@@ -35,12 +35,15 @@ def _tensor(t, name, dtype, shape, device, dense=True):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dense:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous" if dense else f"the last axis of {name} must be contiguous")
+
+
+def _tensor(t, name, dtype, shape, device):
+    """Pointer of a dense tensor of this type and shape.  (Calls take a few microseconds on the GPU: the checks are few.)"""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device, True)
 
 
 def _io(t, name):
@@ -51,19 +54,26 @@ def _io(t, name):
 
 def _rows(t, name, dtype, shape, device):
     """Pointer, row stride and head stride of a [rows, heads, d] operand."""
-    return _tensor(t, name, dtype, shape, device, dense=False), t.stride(0), t.stride(1)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda:
+        row, head, one = t.stride()
+        if one == 1 or shape[2] <= 1 or t.numel() == 0:
+            return t.data_ptr(), row, head
+    _refuse(t, name, dtype, shape, device, False)
 
 
 def _call(fn, device, stream, args, scratch=()):
     """Run an entry point on `stream` (None: the device's current one).  `scratch`: tensors made here."""
-    current = torch.cuda.current_stream(device)
-    if stream is not None and stream != current:
-        # the allocator made them for the current stream: their memory must not be reused before `stream` is done,
-        # and `stream` must not write to it before what used it last
-        stream.wait_stream(current)
-        for t in scratch:
-            t.record_stream(stream)
-    handle = (current if stream is None else stream).cuda_stream
+    if stream is None:
+        handle = _raw_stream(device.index)
+    else:
+        current = torch.cuda.current_stream(device)
+        if stream != current:
+            # the allocator made them for the current stream: their memory must not be reused before `stream` is
+            # done, and `stream` must not write to it before what used it last
+            stream.wait_stream(current)
+            for t in scratch:
+                t.record_stream(stream)
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
         st = fn(*args, handle)
     else:
@@ -113,14 +123,11 @@ def kdn_cache_plan(context_len, new_len, block_table, free_pages, free_count, *,
     width = block_table.shape[1]
     made = []
     if out is None:
-        # one allocation; every part starts on 16 bytes
-        slots = (8 * capacity + 15) // 16 * 4
-        parts = [(k + 3) // 4 * 4 for k in (capacity, n + 1, n, n, 1)]
-        buf = torch.empty(slots + sum(parts), dtype=i32, device=device)
-        made.append(buf)
-        cut = buf.split([slots] + parts)
-        out = CachePlan(cut[0].view(torch.int64)[:capacity], cut[1][:capacity], cut[2][:n + 1], cut[3][:n], cut[4][:n],
-                        cut[5][:1])
+        empty = torch.empty
+        out = CachePlan(empty(capacity, dtype=torch.int64, device=device), empty(capacity, dtype=i32, device=device),
+                        empty(n + 1, dtype=i32, device=device), empty(n, dtype=i32, device=device),
+                        empty(n, dtype=i32, device=device), empty(1, dtype=i32, device=device))
+        made.extend(out)
         outs = [t.data_ptr() for t in out]
     else:
         outs = [_tensor(t, name, dt, shape, device) for t, name, dt, shape in zip(
