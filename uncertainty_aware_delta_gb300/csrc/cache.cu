@@ -150,63 +150,121 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
 
 // ------------------------------------------------------------------ write and read
 
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32, kWriteUnroll = 2;
 
-template <typename T> __device__ __forceinline__ void load4(const T* p, float (&x)[4]);
-template <> __device__ __forceinline__ void load4<float>(const float* p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
-}
-
-// Codes (offset 8) and scale of a 32-value group held by 8 neighbouring lanes, 4 values
-// each.  The largest magnitude is taken on the bit patterns, which order NaN above
-// infinity above every number, so one test afterwards finds a value that is not finite.
-__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], __half& scale) {
-    uint32_t m = 0;
+// 8 neighbouring values as they are stored; as fp32; and the largest bit pattern without sign among
+// them, as fp32 bits (patterns order NaN above infinity above every number).
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const uint4*>(p)[0];
+        b = reinterpret_cast<const uint4*>(p)[1];
+    }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
+    }
+    __device__ __forceinline__ uint32_t largest() const {
+        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t m = 0;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    scale = m >= 0x7f800000u ? __ushort_as_half(0x7fff)
-                             : __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m), 7.0f), 65504.0f));
-    const float s = __half2float(scale);
-    uint32_t code = 0;
+        for (int i = 0; i < 8; ++i) m = max(m, v[i] & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+        const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    }
+    __device__ __forceinline__ uint32_t largest() const {   // two halves at a time
+        uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float q = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.0f), 7.0f) : 0.0f;
-        code |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * i);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
-    return code;
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Places of a lane's pieces within a token's block: 4 values of channel dd (a multiple of 4).
+// Codes (offset 8) and scale of a 32-value group held by 4 neighbouring lanes, 8 values each.
+// x / s, rounded once, without a division a value: the product with the approximate reciprocal
+// is off by at most 2^-22 of it, and its remainder x - q s (one fused operation) times the reciprocal
+// takes that to 2^-44, while x / s, with 24 and 11 bits, is never nearer than 2^-36 to the middle of
+// two fp32 numbers without being there.
+template <typename T> __device__ __forceinline__ uint32_t quantise8(const Eight<T>& v, __half& scale) {
+    const float m = __uint_as_float(v.largest());
+    // m / 7, rounded once: the quotient by the rounded reciprocal, corrected by its remainder
+    constexpr float kSeventh = 1.0f / 7.0f;
+    const float q0 = m * kSeventh, q = fmaf(fmaf(-q0, 7.0f, m), kSeventh, q0);
+    scale = m < INFINITY ? __float2half_rn(fminf(q, 65504.0f)) : __ushort_as_half(0x7fff);
+    const float s = __half2float(scale);
+    if (!(s > 0.0f)) return 0x88888888u;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    constexpr float kRound = 12582912.0f;   // 1.5 2^23: adding and subtracting it rounds to a whole number
+    float x[8], t[8];
+    v.widen(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float y = x[i] * inv, z = fmaf(fmaf(-y, s, x[i]), inv, y);
+        t[i] = __fsub_rn(__fadd_rn(fminf(fmaxf(z, -7.0f), 7.0f), kRound), kRound);
+    }
+    // four codes at a time as one exact fp32 number, whose low bits are read off its sum with 2^23
+    float lo = 8423560.0f, hi = 8423560.0f;   // 2^23 + 8 (1 + 16 + 256 + 4096)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo = fmaf(t[i], static_cast<float>(1 << (4 * i)), lo);
+        hi = fmaf(t[i + 4], static_cast<float>(1 << (4 * i)), hi);
+    }
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+}
+
+// Places of a lane's pieces within a token's block: 8 values of channel dd (a multiple of 8),
+// the n-th eight of their group of 32.
 struct Place {
-    int k_code, k_scale, v_code, v_scale;
+    int k_code, k_scale, v_code, v_scale;   // v_code: of the even one of the lane's two units
 };
 template <int D> __device__ __forceinline__ Place place(int t, int dd) {
     constexpr int G = D / 32;
-    const int m = dd >> 5, c = (dd >> 3) & 3, odd = (dd >> 2) & 1;
-    const int half = t >> 3, pair = (t >> 1) & 3, par = t & 1;
+    const int m = dd >> 5, n = (dd >> 3) & 3, half = t >> 3, pair = (t >> 1) & 3, par = t & 1;
     Place p;
-    p.k_code = t * (D / 2) + (c * G + m) * 4 + odd * 2;
+    p.k_code = t * (D / 2) + (n * G + m) * 4;
     p.k_scale = 8 * D + (t * G + m) * 2;
-    // the 16-bit unit of channels 32 m + 8 n + (4 odd + c), n = 0..3
-    p.v_code = 9 * D + half * 4 * D + (4 * odd + c) * 16 * G + pair * 4 * G + m * 4 + par * 2;
+    // the 16-bit units i of channels 32 m + 8 j + i, j = 0..3; lane n of the group has units 2 n, 2 n + 1
+    p.v_code = 9 * D + half * 4 * D + 2 * n * 16 * G + pair * 4 * G + m * 4 + par * 2;
     p.v_scale = 17 * D + half * (D / 2) + pair * 4 * G + m * 4 + par * 2;
     return p;
+}
+
+// Lanes n = 0..3 of a group hold the codes of channels 8 n + i (i = 0..7) of it; they get the units
+// 2 n (low half) and 2 n + 1 (high half): unit i has the codes of channels 8 j + i in nibbles j.
+__device__ __forceinline__ uint32_t units_of(uint32_t code, int n) {
+    const uint32_t even = code & 0x0f0f0f0fu, odd = (code >> 4) & 0x0f0f0f0fu;
+    uint32_t r[4];   // codes 2 i and 2 i + 1, a half each, in nibble n
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (__byte_perm(even, odd, i | (4 + i) << 8) & 0x000f000fu) << (4 * n);
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, n & 2 ? r[0] : r[2], 2);
+    const uint32_t b = __shfl_xor_sync(0xffffffffu, n & 2 ? r[1] : r[3], 2);
+    const uint32_t k0 = (n & 2 ? r[2] : r[0]) | a, k1 = (n & 2 ? r[3] : r[1]) | b;
+    return (n & 1 ? k1 : k0) | __shfl_xor_sync(0xffffffffu, n & 1 ? k0 : k1, 1);
 }
 
 // Whether the warp's 16 slots are one aligned block of the cache, in order.
@@ -214,65 +272,65 @@ __device__ __forceinline__ bool whole_block(int64_t slot, int n, int64_t n_slots
     const int lane = threadIdx.x & 31;
     const int64_t s0 = __shfl_sync(0xffffffffu, slot, 0);
     const bool fits = lane >= kBlockTokens || slot == s0 + lane;
-    return __all_sync(0xffffffffu, fits) && n == kBlockTokens && s0 >= 0 && s0 % kBlockTokens == 0 && s0 < n_slots;
+    return __all_sync(0xffffffffu, fits) && n == kBlockTokens && s0 >= 0 && (s0 & (kBlockTokens - 1)) == 0 && s0 < n_slots;
 }
 
 template <int D> __device__ __forceinline__ size_t block_offset(const CacheArgs& a, int64_t slot, int h) {
-    const int64_t page = slot / a.page;
+    // a division of 64-bit numbers costs some hundred instructions: only where a slot needs one
+    const int64_t page = slot >> 32 ? slot / a.page : static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page));
     const int blk = static_cast<int>(slot - page * a.page) / kBlockTokens;
     return ((static_cast<size_t>(page) * a.H_kv + h) * (a.page / kBlockTokens) + blk) * cache_block_bytes(D);
 }
 
-// A warp takes TOK consecutive tokens of one key head, 128 / D of them at a time, each
-// lane 4 channels.
+// A warp takes TOK consecutive tokens of one key head, 256 / D of them at a time, each
+// lane 8 channels.
 template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CacheArgs a) {
-    constexpr int kBytes = cache_block_bytes(D), kStep = 128 / D;
+    constexpr int kBytes = cache_block_bytes(D), kStep = 256 / D, G = D / 32;
     __shared__ __align__(16) uint8_t stage[TOK == kBlockTokens ? kRowWarps * kBytes : 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long unit = static_cast<long long>(blockIdx.x) * kRowWarps + warp;
-    const int h = static_cast<int>(unit % a.H_kv);
-    const long long t0 = unit / a.H_kv * TOK;
+    const unsigned unit = blockIdx.x * kRowWarps + warp, tile = unit / static_cast<unsigned>(a.H_kv);   // (below 2^31)
+    const int h = static_cast<int>(unit - tile * a.H_kv);
+    const long long t0 = static_cast<long long>(tile) * TOK;
     if (t0 >= a.n_tok) return;
-    const int n = static_cast<int>(min(static_cast<long long>(TOK), a.n_tok - t0));
+    const int n_here = static_cast<int>(min(static_cast<long long>(TOK), a.n_tok - t0));
     const int64_t n_slots = static_cast<int64_t>(a.n_pages) * a.page;
-    const int64_t mine = lane < n ? a.slots[t0 + lane] : -1;
-    const bool whole = TOK == kBlockTokens && whole_block(mine, n, n_slots);
+    const int64_t mine = lane < n_here ? a.slots[t0 + lane] : -1;
+    const bool whole = TOK == kBlockTokens && whole_block(mine, n_here, n_slots);
     uint8_t* buf = stage + (TOK == kBlockTokens ? warp * kBytes : 0);
-    const T* k = static_cast<const T*>(a.k.p) + t0 * a.k.row + h * a.k.head;
-    const T* v = static_cast<const T*>(a.v.p) + t0 * a.v.row + h * a.v.head;
-    const int dd = (4 * lane) % D;
-#pragma unroll 4
+    const int dd = (8 * lane) % D, n = (dd >> 3) & 3;
+    const T* k = static_cast<const T*>(a.k.p) + t0 * a.k.row + h * a.k.head + dd;
+    const T* v = static_cast<const T*>(a.v.p) + t0 * a.v.row + h * a.v.head + dd;
+#pragma unroll kWriteUnroll
     for (int i = 0; i < (TOK + kStep - 1) / kStep; ++i) {
-        const int t = i * kStep + 4 * lane / D;
+        const int t = i * kStep + 8 * lane / D;
         const int64_t slot = __shfl_sync(0xffffffffu, mine, t & 31);
-        const bool live = t < n && slot >= 0 && slot < n_slots;
-        float xk[4] = {0.f, 0.f, 0.f, 0.f}, xv[4] = {0.f, 0.f, 0.f, 0.f};
+        const bool live = whole || (t < n_here && slot >= 0 && slot < n_slots);
+        Eight<T> kk = {}, vv = {};
         if (live) {
-            load4(k + t * a.k.row + dd, xk);
-            load4(v + t * a.v.row + dd, xv);
+            kk.load(k + t * a.k.row);
+            vv.load(v + t * a.v.row);
         }
         __half sk, sv;
-        const uint32_t ck = quantise4(xk, sk), cv = quantise4(xv, sv);
-        // lanes n = 0..3 of a group half hold nibble n of the half's four 16-bit units:
-        // lane n collects unit n
-        const int nib = (dd >> 3) & 3;
-        uint32_t lo = (cv & 15u) | (((cv >> 4) & 15u) << 16), hi = ((cv >> 8) & 15u) | ((cv >> 12) << 16);
-        lo <<= 4 * nib;
-        hi <<= 4 * nib;
-#pragma unroll
-        for (int o = 2; o <= 4; o <<= 1) {
-            lo |= __shfl_xor_sync(0xffffffffu, lo, o);
-            hi |= __shfl_xor_sync(0xffffffffu, hi, o);
-        }
-        const uint32_t both = nib < 2 ? lo : hi;
-        const uint16_t unit16 = static_cast<uint16_t>((nib & 1) ? both >> 16 : both);
-        if (live) {
-            uint8_t* blk = whole ? buf : a.cache + block_offset<D>(a, slot, h);
-            const Place p = place<D>(static_cast<int>(slot % kBlockTokens), dd);
-            *reinterpret_cast<uint16_t*>(blk + p.k_code) = static_cast<uint16_t>(ck);
-            *reinterpret_cast<uint16_t*>(blk + p.v_code) = unit16;
-            if ((dd & 31) == 0) {
+        const uint32_t ck = quantise8(kk, sk), units = units_of(quantise8(vv, sv), n);
+        if (whole) {
+            // a token's unit and the next's are one word: the even token's lane writes unit 2 n, the odd one's 2 n + 1
+            const uint32_t next = __shfl_xor_sync(0xffffffffu, units, D / 8);
+            const Place p = place<D>(t, dd);
+            *reinterpret_cast<uint32_t*>(buf + p.k_code) = ck;
+            *reinterpret_cast<uint32_t*>(buf + p.v_code + (t & 1) * (16 * G - 2)) =
+                t & 1 ? (next >> 16) | (units & 0xffff0000u) : (units & 0xffffu) | (next << 16);
+            if (n == 0) {
+                *reinterpret_cast<__half*>(buf + p.k_scale) = sk;
+                *reinterpret_cast<__half*>(buf + p.v_scale) = sv;
+            }
+        } else if (live) {
+            uint8_t* blk = a.cache + block_offset<D>(a, slot, h);
+            const Place p = place<D>(static_cast<int>(slot & (kBlockTokens - 1)), dd);
+            *reinterpret_cast<uint32_t*>(blk + p.k_code) = ck;
+            *reinterpret_cast<uint16_t*>(blk + p.v_code) = static_cast<uint16_t>(units);
+            *reinterpret_cast<uint16_t*>(blk + p.v_code + 16 * G) = static_cast<uint16_t>(units >> 16);
+            if (n == 0) {
                 *reinterpret_cast<__half*>(blk + p.k_scale) = sk;
                 *reinterpret_cast<__half*>(blk + p.v_scale) = sv;
             }
@@ -287,17 +345,17 @@ __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(const CacheArg
 
 template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheArgs a) {
-    constexpr int kBytes = cache_block_bytes(D), kStep = 128 / D;
+    constexpr int kBytes = cache_block_bytes(D), kStep = 256 / D, G = D / 32;
     __shared__ __align__(16) uint8_t stage[TOK == kBlockTokens ? kRowWarps * kBytes : 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long unit = static_cast<long long>(blockIdx.x) * kRowWarps + warp;
-    const int h = static_cast<int>(unit % a.H_kv);
-    const long long t0 = unit / a.H_kv * TOK;
+    const unsigned unit = blockIdx.x * kRowWarps + warp, tile = unit / static_cast<unsigned>(a.H_kv);   // (below 2^31)
+    const int h = static_cast<int>(unit - tile * a.H_kv);
+    const long long t0 = static_cast<long long>(tile) * TOK;
     if (t0 >= a.n_tok) return;
-    const int n = static_cast<int>(min(static_cast<long long>(TOK), a.n_tok - t0));
+    const int n_here = static_cast<int>(min(static_cast<long long>(TOK), a.n_tok - t0));
     const int64_t n_slots = static_cast<int64_t>(a.n_pages) * a.page;
-    const int64_t mine = lane < n ? a.slots[t0 + lane] : -1;
-    const bool whole = TOK == kBlockTokens && whole_block(mine, n, n_slots);
+    const int64_t mine = lane < n_here ? a.slots[t0 + lane] : -1;
+    const bool whole = TOK == kBlockTokens && whole_block(mine, n_here, n_slots);
     uint8_t* buf = stage + (TOK == kBlockTokens ? warp * kBytes : 0);
     if (whole) {
         const uint4* src =
@@ -305,35 +363,39 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheArgs
         for (int i = lane; i < kBytes / 16; i += 32) reinterpret_cast<uint4*>(buf)[i] = src[i];
         __syncwarp();
     }
-    T* k = static_cast<T*>(a.k_out) + (t0 * a.H_kv + h) * D;
-    T* v = static_cast<T*>(a.v_out) + (t0 * a.H_kv + h) * D;
-    const int dd = (4 * lane) % D;
+    const int dd = (8 * lane) % D, n = (dd >> 3) & 3;
+    T* k = static_cast<T*>(a.k_out) + (t0 * a.H_kv + h) * D + dd;
+    T* v = static_cast<T*>(a.v_out) + (t0 * a.H_kv + h) * D + dd;
 #pragma unroll 4
     for (int i = 0; i < (TOK + kStep - 1) / kStep; ++i) {
-        const int t = i * kStep + 4 * lane / D;
+        const int t = i * kStep + 8 * lane / D;
         const int64_t slot = __shfl_sync(0xffffffffu, mine, t & 31);
-        const bool live = t < n && slot >= 0 && slot < n_slots;
-        uint32_t ck = 0x8888u, unit16 = 0x8888u;
+        const bool live = whole || (t < n_here && slot >= 0 && slot < n_slots);
+        uint32_t ck = 0x88888888u, units = 0x88888888u;
         float sk = 0.0f, sv = 0.0f;
         if (live) {
             const uint8_t* blk = whole ? buf : a.cache + block_offset<D>(a, slot, h);
-            const Place p = place<D>(static_cast<int>(slot % kBlockTokens), dd);
-            ck = *reinterpret_cast<const uint16_t*>(blk + p.k_code);
-            unit16 = *reinterpret_cast<const uint16_t*>(blk + p.v_code);
+            const Place p = place<D>(whole ? t : static_cast<int>(slot & (kBlockTokens - 1)), dd);
+            ck = *reinterpret_cast<const uint32_t*>(blk + p.k_code);
+            units = *reinterpret_cast<const uint16_t*>(blk + p.v_code) |
+                    static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(blk + p.v_code + 16 * G)) << 16;
             sk = __half2float(*reinterpret_cast<const __half*>(blk + p.k_scale));
             sv = __half2float(*reinterpret_cast<const __half*>(blk + p.v_scale));
         }
-        const int nib = (dd >> 3) & 3;
-        float xk[4], xv[4];
+        // 2^23 + code as fp32 bits, less 2^23 + 8
+        auto value = [](uint32_t code, float s) { return (__uint_as_float((code & 15u) | 0x4b000000u) - 8388616.0f) * s; };
+        float xk[8], xv[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // value j: nibble `nib` of the unit that lane j of the half holds
-            const uint32_t u = __shfl_sync(0xffffffffu, unit16, (lane & ~6) | (j << 1));
-            xk[j] = (static_cast<float>((ck >> (4 * j)) & 15u) - 8.0f) * sk;
-            xv[j] = (static_cast<float>((u >> (4 * nib)) & 15u) - 8.0f) * sv;
+        for (int j = 0; j < 8; ++j) xk[j] = value(ck >> (4 * j), sk);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // units 2 j and 2 j + 1, of lane j of the group; this lane's are nibbles n
+            const uint32_t u = __shfl_sync(0xffffffffu, units, (lane & ~3) | j) >> (4 * n);
+            xv[2 * j] = value(u, sv);
+            xv[2 * j + 1] = value(u >> 16, sv);
         }
-        if (t < n) {
-            store4(k + static_cast<size_t>(t) * a.H_kv * D + dd, xk);
-            store4(v + static_cast<size_t>(t) * a.H_kv * D + dd, xv);
+        if (t < n_here) {
+            store8(k + static_cast<size_t>(t) * a.H_kv * D, xk);
+            store8(v + static_cast<size_t>(t) * a.H_kv * D, xv);
         }
     }
 }
@@ -343,10 +405,10 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheArgs
 template <typename T, int D, bool WRITE> cudaError_t launch_rows(const CacheArgs& a, cudaStream_t s) {
     const long long big = (static_cast<long long>(a.n_tok) + kBlockTokens - 1) / kBlockTokens * a.H_kv;
     const bool few = big < 152ll * kRowWarps;
-    constexpr int kStep = 128 / D;
+    constexpr int kStep = 256 / D;
     const long long units = few ? (static_cast<long long>(a.n_tok) + kStep - 1) / kStep * a.H_kv : big;
     const long long grid = (units + kRowWarps - 1) / kRowWarps;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    if (grid > 0x7fffffffll / kRowWarps) return cudaErrorInvalidValue;
     const int g = static_cast<int>(grid);
     if (WRITE) {
         if (few) cache_write_kernel<T, D, kStep><<<g, kRowThreads, 0, s>>>(a);
