@@ -1,6 +1,17 @@
-// Causal attention over whole prompts, CUDA-core path: fp32 operands (bf16 is widened),
-// products in 3xTF32 on warp-level tensor-core MMAs.  Every size and type; the tcgen05
-// kernel takes bf16 with heads of 64 and 128.
+// Causal attention over whole prompts, CUDA-core path: every size and type (the tcgen05
+// kernel takes bf16 with heads of 64 and 128).  fp32 operands (bf16 is widened) as two TF32
+// parts, products in 3xTF32 on warp-level MMAs (m16n8k8).
+//
+// A block has 128 query rows, a warp 32 of them, and walks the keys in tiles of 32: scores in
+// registers, a running maximum and sum a row, weights used as the next product's left operand
+// where they are (the keys of a step are taken in the order 0, 2, 4, 6, 1, 3, 5, 7, in which the
+// accumulators' columns are that operand's).  Operands are split once, when they are put into
+// shared memory.  What bounds it: the tensor pipe and shared memory, 24 MMAs against 32
+// 4-byte loads a thread for 32 rows, 8 channels and 32 keys; a wider warp tile would not fit
+// its registers.
+//
+// The MMAs cut sums off instead of rounding them, which a long sum would show: products of
+// one tile are summed there, and added to the output in fp32.
 
 #include <cuda_bf16.h>
 
@@ -12,153 +23,262 @@
 namespace kdn {
 namespace {
 
-constexpr int kThreads = 256, kRows = 64, kKeys = 64, kPad = 4;
+constexpr int kThreads = 128, kRows = 128, kKeys = 32;
+constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+// The two TF32 parts of four numbers (an infinity has no second part).
+__device__ __forceinline__ void split4(float4 x, uint4& hi, uint4& lo) {
+    split_tf32(x.x, hi.x, lo.x);
+    split_tf32(x.y, hi.y, lo.y);
+    split_tf32(x.z, hi.z, lo.z);
+    split_tf32(x.w, hi.w, lo.w);
+    if (!finite(x.x)) lo.x = 0;
+    if (!finite(x.y)) lo.y = 0;
+    if (!finite(x.z)) lo.z = 0;
+    if (!finite(x.w)) lo.w = 0;
+}
 
-// One block per (64 query rows of a sequence, head); key tiles of 64 with the running
-// maximum and sum of the softmax.  A masked key has no influence whatever it holds: keys
-// outside the sequence are read as zeros, scores are masked by selection, and a value that
-// is not finite is taken out of the tile and added to the rows that see it.
+// A masked key has no influence whatever it holds: keys outside the sequence are read as
+// zeros, scores are masked by selection, and a value that is not finite is taken out of the
+// tile and added to the rows that see it.
 template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_kernel(const PromptArgs a, int n_items) {
-    constexpr int LD = D + kPad, LS = kKeys + kPad;
-    extern __shared__ float prompt_smem[];
-    float* Q = prompt_smem;
-    float* K = Q + kRows * LD;
-    float* V = K + kKeys * LD;
-    float* O = V + kKeys * LD;
-    float* S = O + kRows * LD;
-    float* row_m = S + kRows * LS;
-    float* row_l = row_m + kRows;
-    float* row_f = row_l + kRows;
-    __shared__ int found[5], odd_value;
-    const int tid = threadIdx.x, h = blockIdx.y, kvh = h / (a.H / a.H_kv);
-    if (tid == 0) {
-        // item -> (sequence, row tile): sequences in order
-        int item = blockIdx.x, s = 0;
-        found[0] = -1;
-        for (; s < a.n_seq; ++s) {
-            const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-            const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
-            if (!ok) {
-                set_status(a.status, kStatusRange);
-                continue;
+    constexpr int LD = D + 4;   // rows 4 banks apart: the fragments' loads are free of conflicts
+    extern __shared__ __align__(16) uint32_t prompt_smem[];
+    uint32_t* qh = prompt_smem;
+    uint32_t* ql = qh + kRows * LD;
+    uint32_t* kh = ql + kRows * LD;
+    uint32_t* kl = kh + kKeys * LD;
+    uint32_t* vh = kl + kKeys * LD;
+    uint32_t* vl = vh + kKeys * LD;
+    __shared__ int found[5];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int h = blockIdx.y, kvh = h / (a.H / a.H_kv);
+    if (warp == 0) {
+        // item -> (sequence, row tile), the last tiles first: they have the most keys
+        int item = n_items - 1 - static_cast<int>(blockIdx.x);
+        bool here = false;
+        if (lane == 0) found[0] = -1;
+        for (int s0 = 0; s0 < a.n_seq && !here; s0 += 32) {
+            const int s = s0 + lane;
+            int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+            if (s < a.n_seq) {
+                q0 = a.cu_q[s]; q1 = a.cu_q[s + 1]; k0 = a.cu_k[s]; k1 = a.cu_k[s + 1];
+                if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
+                    set_status(a.status, kStatusRange);
+                    q0 = q1 = 0;
+                }
             }
             const int tiles = (q1 - q0 + kRows - 1) / kRows;
-            if (item < tiles) {
-                found[0] = q0 + item * kRows;
-                found[1] = min(kRows, q1 - q0 - item * kRows);
+            int upto = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (item < upto && item >= upto - tiles) {
+                const int row = (item - (upto - tiles)) * kRows;
+                found[0] = q0 + row;
+                found[1] = min(kRows, q1 - q0 - row);
                 found[2] = k0;
                 found[3] = k1 - k0;
-                found[4] = (k1 - k0) - (q1 - q0) + item * kRows;   // place of the tile's first row among the keys
-                break;
+                found[4] = (k1 - k0) - (q1 - q0) + row;   // place of the tile's first row among the keys
             }
-            item -= tiles;
+            here = __any_sync(kAll, item < upto);
+            item -= __shfl_sync(kAll, upto, 31);
         }
     }
     __syncthreads();
     const int q0 = found[0], rows = found[1], k0 = found[2], n_keys = found[3], place = found[4];
     if (q0 < 0) return;
-    const T* q = static_cast<const T*>(a.q.p) + q0 * a.q.row + h * a.q.head;
-    for (int i = tid; i < kRows * D; i += kThreads) {
-        const int r = i / D, c = i % D;
-        Q[r * LD + c] = r < rows ? IO<T>::load(q, r * a.q.row + c) : 0.f;
-        O[r * LD + c] = 0.f;
+    const T* qp = static_cast<const T*>(a.q.p) + q0 * a.q.row + h * a.q.head;
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        uint4 hi, lo;
+        split4(r < rows ? load4(qp + r * a.q.row + c) : make_float4(0.f, 0.f, 0.f, 0.f), hi, lo);
+        *reinterpret_cast<uint4*>(qh + r * LD + c) = hi;
+        *reinterpret_cast<uint4*>(ql + r * LD + c) = lo;
     }
-    for (int i = tid; i < kRows; i += kThreads) {
-        row_m[i] = -INFINITY;
-        row_l[i] = 0.f;
+    float o[2][D / 8][4], m[4], l[4];   // rows 16 i + g, + 8 of the warp's 32
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
     }
     const int last = min(place + rows - 1, n_keys - 1);                       // last key any row sees
     const int low = a.window > 0 ? max(place - a.window + 1, 0) : 0;         // first
     const float to_log2 = a.scale * 1.4426950408889634f;
     for (int j0 = low / kKeys * kKeys; j0 <= last; j0 += kKeys) {
-        if (tid == 0) odd_value = 0;
-        __syncthreads();
-        const T* k = static_cast<const T*>(a.k.p) + (static_cast<long long>(k0) + j0) * a.k.row + kvh * a.k.head;
-        const T* v = static_cast<const T*>(a.v.p) + (static_cast<long long>(k0) + j0) * a.v.row + kvh * a.v.head;
-        for (int i = tid; i < kKeys * D; i += kThreads) {
-            const int r = i / D, c = i % D;
+        const T* kp = static_cast<const T*>(a.k.p) + (static_cast<long long>(k0) + j0) * a.k.row + kvh * a.k.head;
+        const T* vp = static_cast<const T*>(a.v.p) + (static_cast<long long>(k0) + j0) * a.v.row + kvh * a.v.head;
+        bool odd = false;
+        for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
             const bool in = j0 + r < n_keys;
-            K[r * LD + c] = in ? IO<T>::load(k, r * a.k.row + c) : 0.f;
-            const float x = in ? IO<T>::load(v, r * a.v.row + c) : 0.f;
-            V[r * LD + c] = finite(x) ? x : 0.f;
-            if (!finite(x)) odd_value = 1;
-        }
-        __syncthreads();
-        smem_gemm<4>(kRows, kKeys, D, Q, LD, 1, K, 1, LD, S, LS, 1.f, false);
-        __syncthreads();
-        {
-            const int r = tid >> 2, c0 = (tid & 3) * (kKeys / 4), at = place + r;
-            float x[kKeys / 4], mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kKeys / 4; ++i) {
-                const int j = j0 + c0 + i;
-                const bool see = r < rows && j <= at && j < n_keys && (a.window <= 0 || j > at - a.window);
-                x[i] = see ? S[r * LS + c0 + i] * to_log2 : -INFINITY;
-                mx = fmaxf(mx, x[i]);
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint4 hi, lo;
+            split4(in ? load4(kp + r * a.k.row + c) : zero, hi, lo);
+            *reinterpret_cast<uint4*>(kh + r * LD + c) = hi;
+            *reinterpret_cast<uint4*>(kl + r * LD + c) = lo;
+            float4 x = in ? load4(vp + r * a.v.row + c) : zero;
+            if (!(finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w))) {
+                odd = true;
+                x = make_float4(finite(x.x) ? x.x : 0.f, finite(x.y) ? x.y : 0.f, finite(x.z) ? x.z : 0.f, finite(x.w) ? x.w : 0.f);
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float old = row_m[r], mn = fmaxf(old, mx), base = mn == -INFINITY ? 0.f : mn;
+            split4(x, hi, lo);
+            *reinterpret_cast<uint4*>(vh + r * LD + c) = hi;
+            *reinterpret_cast<uint4*>(vl + r * LD + c) = lo;
+        }
+        odd = __syncthreads_or(odd);
+        float s[2][kKeys / 8][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < kKeys / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < D; c += 8) {
+            uint32_t ah[2][4], al[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = (32 * warp + 16 * i + g) * LD + c + q;
+                ah[i][0] = qh[at]; ah[i][1] = qh[at + 8 * LD]; ah[i][2] = qh[at + 4]; ah[i][3] = qh[at + 8 * LD + 4];
+                al[i][0] = ql[at]; al[i][1] = ql[at + 8 * LD]; al[i][2] = ql[at + 4]; al[i][3] = ql[at + 8 * LD + 4];
+            }
+#pragma unroll
+            for (int n = 0; n < kKeys / 8; ++n) {
+                const int at = (8 * n + g) * LD + c + q;
+                const uint32_t bh0 = kh[at], bh1 = kh[at + 4], bl0 = kl[at], bl1 = kl[at + 4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mma_m16n8k8_tf32(s[i][n], al[i], bh0, bh1);
+                    mma_m16n8k8_tf32(s[i][n], ah[i], bl0, bl1);
+                    mma_m16n8k8_tf32(s[i][n], ah[i], bh0, bh1);
+                }
+            }
+        }
+        // rows 2 i and 2 i + 1 of the thread: 16 i + g and 16 i + g + 8
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = r / 2, e = r % 2 * 2, at = place + 32 * warp + 16 * i + 8 * (r % 2) + g;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < kKeys / 8; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int j = j0 + 8 * n + 2 * q + k;
+                    const bool see = j <= at && j < n_keys && (a.window <= 0 || j > at - a.window);
+                    s[i][n][e + k] = see ? s[i][n][e + k] * to_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[i][n][e + k]);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+            const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[r] - base);
+            m[r] = mn;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kKeys / 4; ++i) {
-                const float p = exp2f(x[i] - base);
-                S[r * LS + c0 + i] = p;
-                sum += p;
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            __syncwarp();
-            if ((tid & 3) == 0) {
-                const float f = exp2f(old - base);
-                row_f[r] = f;
-                row_m[r] = mn;
-                row_l[r] = row_l[r] * f + sum;
+            for (int n = 0; n < kKeys / 8; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float p = exp2f(s[i][n][e + k] - base);
+                    s[i][n][e + k] = p;
+                    sum += p;
+                }
+            l[r] = l[r] * f + sum;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                o[i][n][e] *= f;
+                o[i][n][e + 1] *= f;
             }
         }
-        __syncthreads();
-        for (int i = tid; i < kRows * D; i += kThreads) O[i / D * LD + i % D] *= row_f[i / D];
-        __syncthreads();
-        smem_gemm<(D >= 32 ? 4 : 2)>(kRows, D, kKeys, S, LS, 1, V, LD, 1, O, LD, 1.f, true);
-        __syncthreads();
-        if (odd_value) {
-            for (int i = tid; i < kRows * D; i += kThreads) {
-                const int r = i / D, c = i % D, at = place + r;
-                float acc = 0.f;
+        // channels in two halves of at most 64, so that a half's sums stay in registers beside o
+        constexpr int kPart = D / 8 < 8 ? D / 8 : 8;
+#pragma unroll
+        for (int n0 = 0; n0 < D / 8; n0 += kPart) {
+#pragma unroll
+            for (int n = n0; n < n0 + kPart; ++n) {
+                float t[2][4] = {};
+#pragma unroll
+                for (int c = 0; c < kKeys / 8; ++c) {
+                    const int at = (8 * c + 2 * q) * LD + 8 * n + g;
+                    const uint32_t bh0 = vh[at], bh1 = vh[at + LD], bl0 = vl[at], bl1 = vl[at + LD];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t ph[4], pl[4];
+                        split_tf32(s[i][c][0], ph[0], pl[0]);
+                        split_tf32(s[i][c][2], ph[1], pl[1]);
+                        split_tf32(s[i][c][1], ph[2], pl[2]);
+                        split_tf32(s[i][c][3], ph[3], pl[3]);
+                        mma_m16n8k8_tf32(t[i], pl, bh0, bh1);
+                        mma_m16n8k8_tf32(t[i], ph, bl0, bl1);
+                        mma_m16n8k8_tf32(t[i], ph, bh0, bh1);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][n][e] += t[i][e];
+            }
+        }
+        if (odd) {   // each row adds what it sees of the values taken out (its weights are positive)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = r / 2, e = r % 2 * 2, at = place + 32 * warp + 16 * i + 8 * (r % 2) + g;
                 for (int jj = 0; jj < kKeys; ++jj) {
                     const int j = j0 + jj;
-                    if (r >= rows || j > at || j >= n_keys || (a.window > 0 && j <= at - a.window)) continue;
-                    const float x = IO<T>::load(v, jj * a.v.row + c);
-                    if (!finite(x)) acc += S[r * LS + jj] * x;
+                    if (j > at || j >= n_keys || (a.window > 0 && j <= at - a.window)) continue;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float x = IO<T>::load(vp, jj * a.v.row + 8 * n + 2 * q + k);
+                            if (!finite(x)) o[i][n][e + k] += x;
+                        }
                 }
-                O[r * LD + c] += acc;
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
-    __syncthreads();
-    T* o = static_cast<T*>(a.o) + (static_cast<size_t>(q0) * a.H + h) * D;
-    for (int i = tid; i < rows * D; i += kThreads) {
-        const int r = i / D, c = i % D;
-        const float l = row_l[r];
-        IO<T>::store(o, static_cast<size_t>(r) * a.H * D + c, l != 0.f ? O[r * LD + c] / l : 0.f);
-        if (c == 0)
-            a.lse[(static_cast<size_t>(q0) + r) * a.H + h] =
-                l != 0.f ? (row_m[r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    T* op = static_cast<T*>(a.o) + (static_cast<size_t>(q0) * a.H + h) * D;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = r / 2, e = r % 2 * 2, row = 32 * warp + 16 * i + 8 * (r % 2) + g;
+        float sum = l[r];
+        sum += __shfl_xor_sync(kAll, sum, 1);
+        sum += __shfl_xor_sync(kAll, sum, 2);
+        if (row >= rows) continue;
+        const float f = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                IO<T>::store(op, static_cast<size_t>(row) * a.H * D + 8 * n + 2 * q + k, o[i][n][e + k] * f);
+        if (q == 0)
+            a.lse[(static_cast<size_t>(q0) + row) * a.H + h] = sum != 0.f ? (m[r] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
 template <typename T, int D> cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
-    const size_t smem = sizeof(float) * (4 * kRows * (D + kPad) + kRows * (kKeys + kPad) + 3 * kRows);
+    const size_t smem = sizeof(float) * 2 * (kRows + 2 * kKeys) * (D + 4);
     const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // no more row tiles than this, whatever the lengths
-    const long long items = a.total_q / kRows + static_cast<long long>(a.n_seq < a.total_q ? a.n_seq : a.total_q);
-    const dim3 grid(static_cast<unsigned>(items), a.H);
-    prompt_kernel<T, D><<<grid, kThreads, smem, s>>>(a, static_cast<int>(items));
+    const int items = a.total_q / kRows + (a.n_seq < a.total_q ? a.n_seq : a.total_q);
+    prompt_kernel<T, D><<<dim3(items, a.H), kThreads, smem, s>>>(a, items);
     return cudaGetLastError();
 }
 
