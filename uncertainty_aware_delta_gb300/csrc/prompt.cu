@@ -45,6 +45,15 @@ __device__ __forceinline__ void split4(float4 x, uint4& hi, uint4& lo) {
     if (!finite(x.w)) lo.w = 0;
 }
 
+// c[i][n] += a[i] b[n]: two 16-row tiles by N 8-column tiles, independent of each other.
+template <int N>
+__device__ __forceinline__ void products(float (&c)[2][N][4], const uint32_t (&a)[2][4], const uint32_t (&b)[N][2]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mma_m16n8k8_tf32(c[i][n], a[i], b[n][0], b[n][1]);
+}
+
 // A masked key has no influence whatever it holds: keys outside the sequence are read as
 // zeros, scores are masked by selection, and a value that is not finite is taken out of the
 // tile and added to the rows that see it.
@@ -59,10 +68,10 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
     uint32_t* vl = vh + kKeys * LD;
     __shared__ int found[5];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int h = blockIdx.y, kvh = h / (a.H / a.H_kv);
+    const int h = blockIdx.x % a.H, kvh = h / (a.H / a.H_kv);
     if (warp == 0) {
         // item -> (sequence, row tile), the last tiles first: they have the most keys
-        int item = n_items - 1 - static_cast<int>(blockIdx.x);
+        int item = n_items - 1 - static_cast<int>(blockIdx.x / a.H);
         bool here = false;
         if (lane == 0) found[0] = -1;
         for (int s0 = 0; s0 < a.n_seq && !here; s0 += 32) {
@@ -158,17 +167,17 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
                 ah[i][0] = qh[at]; ah[i][1] = qh[at + 8 * LD]; ah[i][2] = qh[at + 4]; ah[i][3] = qh[at + 8 * LD + 4];
                 al[i][0] = ql[at]; al[i][1] = ql[at + 8 * LD]; al[i][2] = ql[at + 4]; al[i][3] = ql[at + 8 * LD + 4];
             }
+            uint32_t bh[kKeys / 8][2], bl[kKeys / 8][2];
 #pragma unroll
             for (int n = 0; n < kKeys / 8; ++n) {
                 const int at = (8 * n + g) * LD + c + q;
-                const uint32_t bh0 = kh[at], bh1 = kh[at + 4], bl0 = kl[at], bl1 = kl[at + 4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mma_m16n8k8_tf32(s[i][n], al[i], bh0, bh1);
-                    mma_m16n8k8_tf32(s[i][n], ah[i], bl0, bl1);
-                    mma_m16n8k8_tf32(s[i][n], ah[i], bh0, bh1);
-                }
+                bh[n][0] = kh[at]; bh[n][1] = kh[at + 4];
+                bl[n][0] = kl[at]; bl[n][1] = kl[at + 4];
             }
+            // part by part: the three products of one sum stand apart
+            products(s, al, bh);
+            products(s, ah, bl);
+            products(s, ah, bh);
         }
         // rows 2 i and 2 i + 1 of the thread: 16 i + g and 16 i + g + 8
 #pragma unroll
@@ -204,34 +213,37 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
                 o[i][n][e + 1] *= f;
             }
         }
-        // channels in two halves of at most 64, so that a half's sums stay in registers beside o
-        constexpr int kPart = D / 8 < 8 ? D / 8 : 8;
+        // 32 channels at a time (16 where there are no more): eight sums side by side
+        constexpr int kPart = D / 8 < 4 ? D / 8 : 4;
 #pragma unroll
         for (int n0 = 0; n0 < D / 8; n0 += kPart) {
+            float t[2][kPart][4] = {};
 #pragma unroll
-            for (int n = n0; n < n0 + kPart; ++n) {
-                float t[2][4] = {};
+            for (int c = 0; c < kKeys / 8; ++c) {
+                uint32_t ph[2][4], pl[2][4], bh[kPart][2], bl[kPart][2];
 #pragma unroll
-                for (int c = 0; c < kKeys / 8; ++c) {
-                    const int at = (8 * c + 2 * q) * LD + 8 * n + g;
-                    const uint32_t bh0 = vh[at], bh1 = vh[at + LD], bl0 = vl[at], bl1 = vl[at + LD];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t ph[4], pl[4];
-                        split_tf32(s[i][c][0], ph[0], pl[0]);
-                        split_tf32(s[i][c][2], ph[1], pl[1]);
-                        split_tf32(s[i][c][1], ph[2], pl[2]);
-                        split_tf32(s[i][c][3], ph[3], pl[3]);
-                        mma_m16n8k8_tf32(t[i], pl, bh0, bh1);
-                        mma_m16n8k8_tf32(t[i], ph, bl0, bl1);
-                        mma_m16n8k8_tf32(t[i], ph, bh0, bh1);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    split_tf32(s[i][c][0], ph[i][0], pl[i][0]);
+                    split_tf32(s[i][c][2], ph[i][1], pl[i][1]);
+                    split_tf32(s[i][c][1], ph[i][2], pl[i][2]);
+                    split_tf32(s[i][c][3], ph[i][3], pl[i][3]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[i][n][e] += t[i][e];
+                for (int n = 0; n < kPart; ++n) {
+                    const int at = (8 * c + 2 * q) * LD + 8 * (n0 + n) + g;
+                    bh[n][0] = vh[at]; bh[n][1] = vh[at + LD];
+                    bl[n][0] = vl[at]; bl[n][1] = vl[at + LD];
+                }
+                products(t, pl, bh);
+                products(t, ph, bl);
+                products(t, ph, bh);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < kPart; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][n0 + n][e] += t[i][n][e];
         }
         if (odd) {   // each row adds what it sees of the values taken out (its weights are positive)
 #pragma unroll
@@ -278,7 +290,9 @@ template <typename T, int D> cudaError_t launch(const PromptArgs& a, cudaStream_
     if (e != cudaSuccess) return e;
     // no more row tiles than this, whatever the lengths
     const int items = a.total_q / kRows + (a.n_seq < a.total_q ? a.n_seq : a.total_q);
-    prompt_kernel<T, D><<<dim3(items, a.H), kThreads, smem, s>>>(a, items);
+    const long long grid = static_cast<long long>(items) * a.H;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    prompt_kernel<T, D><<<static_cast<int>(grid), kThreads, smem, s>>>(a, items);
     return cudaGetLastError();
 }
 
