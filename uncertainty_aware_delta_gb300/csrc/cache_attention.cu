@@ -31,6 +31,10 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStepBlocks = 4, kStepTokens = kStepBlocks * kBlockTokens, kStages = 2, kResident = 3;
 constexpr int kUnit = kWarps * kStepTokens;   // a step of every warp
 constexpr int kTile = 8;                      // query heads of one key head a block
+// Blocks an SM.  fp32's two parts need the registers of two (three spilled: 80 us against 73 on 256
+// sequences of up to 1536 tokens, 16/4 heads of 128); bf16 is the faster for a third (101 against 103 on 64 of
+// up to 32768, 32/4 heads).
+template <typename T> constexpr int resident() { return sizeof(T) == 4 ? 2 : kResident; }
 constexpr uint32_t kWaitLimit = 2000000u;     // polls of about a microsecond at most
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kAll = 0xffffffffu;
@@ -197,7 +201,7 @@ struct Header {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : kResident) cache_attention_kernel(const CacheAttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, resident<T>()) cache_attention_kernel(const CacheAttentionArgs a) {
     constexpr int G = D / 32, kBytes = cache_block_bytes(D), kStageBytes = kStepBlocks * kBytes;
     constexpr uint32_t kAllBlocks = (1u << kStepBlocks) - 1;
     // fp32 queries and weights go as two fp16 parts (22 bits), bf16 ones as one (exact, and 11 bits)
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : kResident) cach
 
 // Joins the parts of the row that begins in block x of the first kernel and goes on, for one of
 // its heads: groups of D threads take every kGroups-th part, the groups are added up in order.
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 512;
 template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttentionArgs a, int blocks) {
     constexpr int kGroups = kJoinThreads / D;
     __shared__ float sum[kGroups][D], weight[kMaxParts], top[kMaxParts / 32], den[kMaxParts / 32];
@@ -649,17 +653,17 @@ struct Grid {
     int blocks;
     bool cut;
 };
-constexpr int kMostBlocks = 152 * kResident;   // GB300's SMs
-Grid grid_of(int n_seq, int H, int H_kv, int max_len, int window) {
+constexpr int kSMs = 152;   // GB300's
+Grid grid_of(int n_seq, int H, int H_kv, int max_len, int window, int most_blocks) {
     if (H <= 0 || H_kv <= 0) return {0, false};
     const long long tiles = static_cast<long long>(H_kv) * ((H / H_kv + kTile - 1) / kTile);
     const long long seen = window > 0 && window < max_len ? static_cast<long long>(window) + kBlockTokens - 1 : max_len;
     const long long units = (seen + kUnit - 1) / kUnit, all = (units > 1 ? units : 1) * n_seq * tiles;
-    return {static_cast<int>(all < kMostBlocks ? all : kMostBlocks), units > 1};
+    return {static_cast<int>(all < most_blocks ? all : most_blocks), units > 1};
 }
 
 template <typename T, int D> cudaError_t launch(const CacheAttentionArgs& a, cudaStream_t s) {
-    const Grid g = grid_of(a.n_seq, a.H, a.H_kv, a.max_len, a.window);
+    const Grid g = grid_of(a.n_seq, a.H, a.H_kv, a.max_len, a.window, kSMs * resident<T>());
     constexpr int ring = kWarps * kStages * kStepBlocks * cache_block_bytes(D), joined = kWarps * kTile * D * 4;
     constexpr int smem = ring > joined ? ring : joined;
     cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -691,7 +695,7 @@ template <typename T> cudaError_t by_size(const CacheAttentionArgs& a, cudaStrea
 }  // namespace
 
 size_t cache_attention_scratch(int n_seq, int H, int H_kv, int d, int max_len, int window) {
-    const Grid g = grid_of(n_seq, H, H_kv, max_len, window);
+    const Grid g = grid_of(n_seq, H, H_kv, max_len, window, kSMs * kResident);
     return g.cut ? static_cast<size_t>(g.blocks) * (sizeof(Header) + 2 * sizeof(float) * (kTile * d + 2 * kTile)) : 0;
 }
 
