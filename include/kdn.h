@@ -95,14 +95,15 @@ typedef enum { KDN_DIAG = 0, KDN_ISO = 1, KDN_PKDA = 2 } kdn_variant;
 #define KDN_FLAG_NO_SPLIT 0x2u   /* tensor-core path: never split sequences into segments */
 /*
  * Test facility for the bounded-wait path; never set it in production.  The
- * kernels that wait on asynchronous copies (the tensor-core forward and the
- * d_k = d_v = 128 decode kernel) first wait, with a short bound (a few
- * milliseconds), on a barrier that nothing completes, while their first
- * copies are in flight.  The wait gives up, the status word records
+ * kernels that wait on asynchronous copies (the tensor-core forward, the
+ * d_k = d_v = 128 decode kernel and the tensor-core prompt attention) first
+ * wait, with a short bound (a few milliseconds), on a barrier that nothing
+ * completes, while their first copies are in flight.  The wait gives up, the status word records
  * KDN_ERR_TIMEOUT, and each CTA takes its abort path: it issues no further
  * work, lets the copies already issued land and exits.  The outputs of such
  * a call are undefined; the stream and the device stay usable.  Other paths
- * (CUDA-core forward, other decode shapes, the dense filter) ignore the flag.
+ * (CUDA-core forward and prompt attention, other decode shapes, the dense filter)
+ * ignore the flag.
  */
 #define KDN_FLAG_TIMEOUT_PROBE 0x100u
 

@@ -639,7 +639,7 @@ const char* kdn_status_string(int status) {
         case KDN_ERR_UNSUPPORTED: return "d_k, d_v or chunk outside the supported set";
         case KDN_ERR_CUDA: return "a CUDA call or kernel launch failed";
         case KDN_ERR_TIMEOUT: return "a bounded device wait gave up";
-        case KDN_ERR_RANGE: return "a chunk's cumulative log-decay is outside the supported range";
+        case KDN_ERR_RANGE: return "a chunk's cumulative log-decay, a length or a table entry is outside the supported range";
         case KDN_ERR_ALIAS: return "an output overlaps an input";
         default: return "unknown status";
     }
