@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     using L = Layout<D>;
     constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * L::kSlots + 26 + 2 * kItems];
+    __shared__ uint64_t bars[2 * L::kSlots + 28 + 2 * kItems];
     __shared__ Item items[kItems];
     __shared__ int chunk_tiles[kChunks], dirty[kItems];
     __shared__ volatile int aborted;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t sq = sb, skv = sb + 2 * L::kTileBytes, stage = skv + L::kSlots * L::kTileBytes, sums = stage + L::kStage;
     const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * L::kSlots, bar_q = bar_empty + 8 * L::kSlots,
-                   bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
+                   bar_q_free = bar_q + 16, bar_s = bar_q_free + 16, bar_p = bar_s + 16, bar_o = bar_p + 16,
                    bar_o_free = bar_o + 16, bar_v = bar_o_free + 16, bar_cut = bar_v + 32, bar_item = bar_cut + 32,
                    bar_item_free = bar_item + 8 * kItems, bar_turn = bar_item_free + 8 * kItems, bar_l = bar_turn + 16, bar_drain = bar_l + 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             mbar_init(bar_full + 8 * i, 1);
             mbar_init(bar_empty + 8 * i, 2);   // both units' products
         }
-        mbar_init(bar_q, 1);
-        mbar_init(bar_q_free, 2);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_q + 8 * i, 1);
+            mbar_init(bar_q_free + 8 * i, 1);
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_p + 8 * i, 4);
             mbar_init(bar_turn + 8 * i, 1);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         if (warp == 0 && lane == 0) {
             // ---- loader: Q, then K and V tiles in turn
             const int rep = P.H / P.H_kv;
-            int n = 0, nq = 0;
+            int n = 0, nq = 0, nq_sent[2] = {0, 0};
             uint32_t nc = 0;
             bool ok = true;
             Item it;
@@ -312,15 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 const Tiles t = tiles_of(u0, u1);
                 if (t.hi < t.lo) continue;
                 const int kvh = u0.head / rep;
-                if (nq > 0 && !(ok = wait(bar_q_free, (nq - 1) & 1))) break;
-                mbar_expect_tx(bar_q, (u0.any() ? L::kTileBytes : 0) + (u1.any() ? L::kTileBytes : 0));
-                ++nq;
-                for (int s = 0; s < 2; ++s) {
-                    const Unit& u = s ? u1 : u0;
-                    if (u.any())
-                        for (int f = 0; f < L::kHalves; ++f)
-                            tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row, bar_q);
-                }
 #pragma unroll 1
                 for (int b = t.lo; ok && b <= t.hi; ++b)
 #pragma unroll 1
@@ -332,6 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                             tma_load_3d(skv + slot * L::kTileBytes + f * 16384, i ? &P.tv : &P.tk, 64 * f, kvh,
                                         it.k0 + b * kTileKeys, bar_full + 8 * slot);
                         ++n;
+                        // the first keys are asked for before the queries: these wait for the last products of the
+                        // item before, each unit's for its own
+                        if (i == 0 && b == t.lo) {
+                            for (int s = 0; s < 2; ++s) {
+                                const Unit& u = s ? u1 : u0;
+                                if (nq > 0 && !(ok = wait(bar_q_free + 8 * s, (nq - 1) & 1))) break;
+                                mbar_expect_tx(bar_q + 8 * s, u.any() ? L::kTileBytes : 0);
+                                nq_sent[s] = nq + 1;
+                                if (u.any())
+                                    for (int f = 0; f < L::kHalves; ++f)
+                                        tma_load_3d(sq + s * L::kTileBytes + f * 16384, &P.tq, 64 * f, u.head, it.q0 + u.row,
+                                                    bar_q + 8 * s);
+                            }
+                            if (!ok) break;
+                            ++nq;
+                        }
                         if (i && t.cut(b)) mbar_arrive(bar_cut + 8 * (nc++ & 3));
                         if (P.probe && n == 1 && !mbar_wait(bar_drain, 0, kProbeLimit)) {
                             aborted = 1;
@@ -345,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 if (!ok) break;
             }
             if (aborted) {   // copies already issued land before the block's shared memory goes away
-                if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, kWaitLimit);
+                for (int s = 0; s < 2; ++s)
+                    if (nq_sent[s] > 0) mbar_wait(bar_q + 8 * s, (nq_sent[s] - 1) & 1, kWaitLimit);
                 for (int j = max(n - L::kSlots, 0); j < n; ++j)
                     mbar_wait(bar_full + 8 * (j % L::kSlots), (j / L::kSlots) & 1, kWaitLimit);
             }
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 next();
                 if (!await(fb + 8 * slot, phase)) return false;
                 if (x.b == x.lo) {
-                    if (!await(bar_q, nq)) return false;
+                    if (!await(one(bar_q) + 8 * s, nq)) return false;
                     nq ^= 1;
                 }
                 return true;
@@ -454,8 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                             no ^= 1;
                         }
                     }
-                    if (!fresh && !(ok = have_keys(nxt))) break;
-                    if (!(ok = take_turn())) break;
+                }
+                // (a new item's queries, too: they are asked for when this unit's last scores are done)
+                if (more && !(ok = have_keys(nxt))) break;
+                if (!(ok = take_turn())) break;
+                if (have) {
                     if (mine) {
                         if (!(ok = await(bp, np))) break;
                         np ^= 1;
@@ -464,13 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                         if (cur.b == cur.mine_hi) commit(lead, bo);
                     }
                     commit(lead, eb + 8 * vslot);
-                    if (fresh && lead) mbar_arrive(other_turn);   // the next item's queries may be late: a turn of its own
                 }
-                if (!more) break;
-                if (fresh && !(ok = have_keys(nxt) && take_turn())) break;
+                if (!more) {
+                    if (lead) mbar_arrive(other_turn);
+                    break;
+                }
                 if (nxt.b >= nxt.mine_lo && nxt.b <= nxt.mine_hi) scores(slot);
                 commit(lead, eb + 8 * slot);
-                if (nxt.b == nxt.hi) commit(lead, bar_q_free);
+                if (nxt.b == nxt.hi) commit(lead, bar_q_free + 8 * s);
                 if (lead) mbar_arrive(other_turn);
                 cur = nxt;
                 have = true;
