@@ -227,3 +227,18 @@ def test_refusals():
         with pytest.raises(kdn.KDNError) as e:
             kdn.kdn_prompt_attention(q, k, v, cu, **kw)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("d,io", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+def test_outputs_aligned_to_16_bytes(d, io):
+    import torch
+    import uncertainty_aware_delta_gb300 as kdn
+
+    q, k, v, cu_q, cu_k = _inputs([130, 3], [130, 3], 2, 1, d, io)
+    want = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k)
+    spare, off = torch.zeros(q.numel() + 64, dtype=q.dtype, device="cuda"), 16 // q.element_size()
+    o, lse = spare[off:off + q.numel()].view(q.shape), torch.empty_like(want[1])
+    assert o.data_ptr() % 32 == 16
+    kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, out=(o, lse))
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert not bool(spare[:off].any()) and not bool(spare[off + q.numel():].any())
