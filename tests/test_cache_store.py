@@ -137,3 +137,10 @@ def test_refusals():
         kdn.cache_alloc(3, 17, 2, 64)
     with pytest.raises(kdn.KDNError):
         kdn.cache_alloc(3, 16, 2, 96)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n,hkv,d,page,order", [(70001, 1, 128, 64, "pages"), (70000, 1, 128, 32, "shifted"),
+                                                (46000, 3, 64, 128, "pages"), (131077, 2, 32, 16, "scattered")])
+def test_large_write_and_read(n, hkv, d, page, order, io):
+    test_write_and_read(n, hkv, page, order, io, d)

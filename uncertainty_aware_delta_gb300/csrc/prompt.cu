@@ -10,6 +10,11 @@
 // 4-byte loads a thread for 32 rows, 8 channels and 32 keys; a wider warp tile would not fit
 // its registers.
 //
+// Measured: 4 prompts of 700 to 1024 tokens in fp32 (16/4 heads of 64, causal) 230 us, 31 TFLOP/s (92 of
+// TF32 products); bf16 prompts of 128 tokens (16 of them, 16/4 heads of 128) 84 us against the tcgen05
+// kernel's 14, one of 77 tokens 33 against 14.  Calls of a few rows tie (heads of 64, 1 x 16 tokens: 10.6
+// against 12.1), so the path goes by type and head size alone.
+//
 // The MMAs cut sums off instead of rounding them, which a long sum would show: products of
 // one tile are summed there, and added to the output in fp32.
 
