@@ -15,9 +15,9 @@
 // constants.  Scales multiply the scores per group (fp32), and the softmax weights per
 // group (values).
 //
-// Measured: 64 sequences of 1000 to 32768 tokens (bf16, 32/4 heads of 128) 101 us, 3.6 TB/s of cache,
+// Measured: 64 sequences of 1000 to 32768 tokens (bf16, 32/4 heads of 128) 90 us, 4.0 TB/s of cache,
 // where the unpacking and the MMAs of 8 heads are the bound (see above); 256 of 512 to 1536 tokens (fp32, 16/4
-// heads of 128) 73 us, 1.95 TB/s: two fp16 parts double the MMAs, and 4 of their 8 columns are heads;
+// heads of 128) 72 us, 1.97 TB/s: two fp16 parts double the MMAs, and 4 of their 8 columns are heads;
 // one of 4096 tokens (bf16, 16/4) 14.3 us, the latency of two kernels.
 
 #include <cuda_bf16.h>
@@ -124,49 +124,60 @@ __device__ __forceinline__ Span span_of(const CacheAttentionArgs& a, int r) {
 }
 
 // The work in a row: sequence after sequence, its tiles of heads one after another, each
-// `units` long.  Block b of the grid takes units b share .. (b + 1) share - 1, so every block
-// has the same work whatever the lengths; a share is no less than 1 / kMaxParts of a row, so that
-// no row is in more parts than the join can take.
-constexpr int kMaxParts = 128;
-__device__ __forceinline__ void work_of(const CacheAttentionArgs& a, int tiles, long long& total, long long& share) {
+// `cost` + `units` long, as a row's start and end take about as long as `cost` of its units.  Block b of
+// the grid takes places b share .. (b + 1) share - 1, so every block has the same work whatever the
+// lengths; a share is no less than 1 / kMaxParts of a row, so that no row is in more parts than the
+// join can take.  Small shares leave the cost out: a block more counts for more there.
+// (64 rows of 1000 to 32768 tokens, 32/4 heads of 128, at a cost of 0, 1, 2, 3, 4 and 6 units: 101, 94, 90, 91, 91
+// and 95 us; 256 of 512 to 1536 in fp32, 16/4 heads: 73, 72, 72, 74, 75 and 76.)
+constexpr int kMaxParts = 128, kRowCost = 2, kCostedShare = 8;
+__device__ __forceinline__ void work_of(const CacheAttentionArgs& a, int tiles, long long& total, long long& share, int& cost) {
     __shared__ long long part_sum[kWarps];
-    __shared__ int part_max[kWarps];
+    __shared__ int part_max[kWarps], part_rows[kWarps];
     long long sum = 0;
-    int top = 0;
+    int top = 0, rows = 0;
     for (int i = threadIdx.x; i < a.n_seq; i += kThreads) {
         const int u = span_of(a, i).units;
         sum += u;
         top = max(top, u);
+        rows += u > 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(kAll, sum, o);
         top = max(top, __shfl_xor_sync(kAll, top, o));
+        rows += __shfl_xor_sync(kAll, rows, o);
     }
     if (threadIdx.x % 32 == 0) {
         part_sum[threadIdx.x / 32] = sum;
         part_max[threadIdx.x / 32] = top;
+        part_rows[threadIdx.x / 32] = rows;
     }
     __syncthreads();
     sum = 0;
-    top = 0;
+    top = rows = 0;
     for (int w = 0; w < kWarps; ++w) {
         sum += part_sum[w];
         top = max(top, part_max[w]);
+        rows += part_rows[w];
     }
-    total = sum * tiles;
+    cost = sum * tiles >= static_cast<long long>(kCostedShare) * gridDim.x ? kRowCost : 0;
+    total = (sum + static_cast<long long>(rows) * cost) * tiles;
     // (a row of top units that starts inside a share spans at most kMaxParts of this length)
     share = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>((top + kMaxParts - 2) / (kMaxParts - 1)));
 }
 
-// The sequence that holds unit `at` of the work, and the units before it; n_seq past the end.
-__device__ __forceinline__ void find_sequence(const CacheAttentionArgs& a, long long at, int tiles, int& r, long long& before) {
+// Places of one tile of a sequence's heads.
+__device__ __forceinline__ int places_of(const Span& s, int cost) { return s.units ? cost + s.units : 0; }
+
+// The sequence that holds place `at` of the work, and the places before it; n_seq past the end.
+__device__ __forceinline__ void find_sequence(const CacheAttentionArgs& a, long long at, int tiles, int cost, int& r, long long& before) {
     __shared__ long long part[kWarps], found_before;
     __shared__ int found;
     const int per = (a.n_seq + kThreads - 1) / kThreads, r0 = min(static_cast<int>(threadIdx.x) * per, a.n_seq),
               r1 = min(r0 + per, a.n_seq);
     long long mine = 0;
-    for (int i = r0; i < r1; ++i) mine += static_cast<long long>(span_of(a, i).units) * tiles;
+    for (int i = r0; i < r1; ++i) mine += static_cast<long long>(places_of(span_of(a, i), cost)) * tiles;
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,7 +191,7 @@ __device__ __forceinline__ void find_sequence(const CacheAttentionArgs& a, long 
     if (at < upto && at >= upto - mine) {
         long long x = upto - mine;
         for (int i = r0; i < r1; ++i) {
-            const long long u = static_cast<long long>(span_of(a, i).units) * tiles;
+            const long long u = static_cast<long long>(places_of(span_of(a, i), cost)) * tiles;
             if (at < x + u) {
                 found = i;
                 found_before = x;
@@ -226,26 +237,29 @@ __global__ void __launch_bounds__(kThreads, resident<T>()) cache_attention_kerne
         for (int j = tid; j < a.H * D; j += kThreads) IO<T>::store(static_cast<T*>(a.o), static_cast<size_t>(i) * a.H * D + j, 0.f);
         for (int j = tid; j < a.H; j += kThreads) a.lse[static_cast<size_t>(i) * a.H + j] = -INFINITY;
     }
-    long long unit, end, row_units, total, share;   // this block's share of the work; units before sequence r
+    long long place, end, row_place, total, share;   // this block's share of the work; places before sequence r
     Header* headers = static_cast<Header*>(a.scratch);
     float* records = reinterpret_cast<float*>(headers + gridDim.x);
-    int r;
+    int r, cost;
     {
-        work_of(a, tiles, total, share);
-        unit = share * blockIdx.x;
-        end = min(unit + share, total);
+        work_of(a, tiles, total, share, cost);
+        place = share * blockIdx.x;
+        end = min(place + share, total);
         if (tid == 0 && a.scratch) headers[blockIdx.x] = Header{0, 0, 0, 0};
-        if (unit >= end) return;
-        find_sequence(a, unit, tiles, r, row_units);
+        if (place >= end) return;
+        find_sequence(a, place, tiles, cost, r, row_place);
     }
     const uint32_t ring = smem_addr(cache_smem) + warp * kStages * kStageBytes;
     const int per_page = a.page / kBlockTokens, ahead = kUnit / a.page, ahead_off = kUnit - ahead * a.page;
     int used = 0;   // stages filled so far
     Span sp = span_of(a, r);
 
-    while (unit < end) {
-    const int at = static_cast<int>(unit - row_units), tile = at / sp.units, u0 = at - tile * sp.units;
-    const int n_units = static_cast<int>(min(static_cast<long long>(sp.units - u0), end - unit));
+    while (place < end) {
+    const int at = static_cast<int>(place - row_place), tile = at / (cost + sp.units), at0 = at - tile * (cost + sp.units);
+    const int n_places = static_cast<int>(min(static_cast<long long>(cost + sp.units - at0), end - place));
+    // the cost stands before the row's first unit; a row of which a block has no more than that begins in the next
+    const int u0 = max(at0 - cost, 0), n_units = at0 + n_places - cost - u0;
+    if (n_units <= 0) break;
     const int kvh = tile / ht, h0 = kvh * rep + tile % ht * kTile, heads = min(kTile, rep - tile % ht * kTile);
     const int t_begin = sp.first + u0 * kUnit, t_end = min(sp.n, t_begin + n_units * kUnit);
     const int32_t* table = a.block_table + static_cast<size_t>(r) * a.table_width;
@@ -560,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, resident<T>()) cache_attention_kerne
     const bool whole_row = n_units == sp.units;
     float* rec = records + (2 * static_cast<size_t>(blockIdx.x) + (u0 == 0)) * Record<D>::kFloats;
     if (tid == 0 && !whole_row && u0 == 0)
-        headers[blockIdx.x] = Header{r, tile, static_cast<int>((unit + sp.units - 1) / share) - static_cast<int>(blockIdx.x) + 1, 0};
+        headers[blockIdx.x] = Header{r, tile, static_cast<int>((place - at0 + cost + sp.units - 1) / share) - static_cast<int>(blockIdx.x) + 1, 0};
     for (int i = tid; i < heads * D; i += kThreads) {
         const int h = i / D, d = i % D;
         float m = join_m[0][h];
@@ -586,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, resident<T>()) cache_attention_kerne
             if (d == 0) a.lse[row] = l != 0.f ? (base + log2f(l)) * kLn2 : -INFINITY;
         }
     }
-    unit += n_units;
-    if (unit - row_units >= static_cast<long long>(sp.units) * tiles) {
-        row_units = unit;
+    place += n_places;
+    if (place - row_place >= static_cast<long long>(cost + sp.units) * tiles) {
+        row_place = place;
         do {
             if (++r >= a.n_seq) return;
             sp = span_of(a, r);
