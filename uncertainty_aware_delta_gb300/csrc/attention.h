@@ -67,6 +67,7 @@ struct PromptArgs {
 size_t prompt_scratch(int n_seq, int total_q, int H, int H_kv, int d, int io, uint32_t flags);
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s);
 bool prompt_tc_supported(int io, int d);   // prompt_tc.cu
+size_t prompt_tc_scratch(int n_seq, int total_q, int H, int H_kv, int d);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
 }  // namespace kdn

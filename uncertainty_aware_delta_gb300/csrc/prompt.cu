@@ -327,7 +327,9 @@ template <typename T> cudaError_t by_size(const PromptArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t prompt_scratch(int, int, int, int, int, int, uint32_t) { return 0; }
+size_t prompt_scratch(int n_seq, int total_q, int H, int H_kv, int d, int io, uint32_t flags) {
+    return !(flags & KDN_FLAG_PORTABLE) && prompt_tc_supported(io, d) ? prompt_tc_scratch(n_seq, total_q, H, H_kv, d) : 0;
+}
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s) {
     if (!(a.flags & KDN_FLAG_PORTABLE) && prompt_tc_supported(a.io, a.d)) return launch_prompt_tc(a, s);

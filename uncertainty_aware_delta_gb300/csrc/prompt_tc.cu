@@ -54,6 +54,10 @@ struct PromptParams {
     float* lse;
     uint32_t *status, *counter;   // counter: items taken
     int n_seq, total_q, total_k, H, H_kv, window, groups, items, chunk, chunks, probe, wide;
+    struct SplitPlan* plan;
+    struct SplitHead* heads;
+    float* records;
+    int n_records;
     float scale_log2;
 };
 
@@ -139,10 +143,25 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 }
 
 // What a block works on: a row tile of one sequence and a group of heads.
+// Few items, some of them long: the keys of a long one are split over several, whose sums a second kernel joins.
+// A record has both units' outputs [2][128][d] (as far as they go) and their rows' maxima and sums [2][128][2].
+constexpr int kMaxParts = 16, kMinPart = 6;   // of a row; key tiles of a part
+constexpr int kSplitItems = 3 * kSMs;         // more items than this fill the SMs
+struct SplitPlan {
+    int items, unused[15];    // items that are split, the first so many by their length
+    int base[kMaxParts];      // record of the first one's part p
+    int unused_too[32];
+};
+struct SplitHead {
+    int q0, rows, group, parts, unused[4];   // first query, queries
+};
+template <int D> constexpr int kRecord = 2 * kTileRows * (D + 2);
+
 struct Item {
     int q0, n_q, k0, n_k;    // the sequence's rows
     int row;                 // first row of the item in its sequence; negative: no more items
     int group;
+    int from, to, slot;      // where rows may be split: key tiles that the item has, its record (negative: all of the row)
 };
 struct Unit {
     int head, row, rows;     // rows: valid ones
@@ -152,7 +171,7 @@ struct Unit {
     __device__ __forceinline__ bool any() const { return hi >= lo; }
     __device__ __forceinline__ bool masked(int b) const { return b >= all_to || b <= all_from; }
 };
-template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int window) {
+template <bool PAIR, bool SPLIT> __device__ __forceinline__ Unit unit_of(const Item& it, int s, int window) {
     Unit u;
     u.head = PAIR ? 2 * it.group + s : it.group;
     u.row = it.row + (PAIR ? 0 : s * kTileRows);
@@ -161,6 +180,10 @@ template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Item& it, int
     const int last = u.place + u.rows - 1, first = window > 0 ? max(u.place - window + 1, 0) : 0;
     u.lo = first / kTileKeys;
     u.hi = u.rows > 0 && last >= 0 ? last / kTileKeys : u.lo - 1;
+    if (SPLIT) {
+        u.lo = max(u.lo, it.from);
+        u.hi = min(u.hi, it.to);
+    }
     u.all_to = max(u.place + 1, 0) / kTileKeys;
     u.all_from = window > 0 && last >= window ? (last - window) / kTileKeys : -1;
     return u;
@@ -182,9 +205,9 @@ __device__ __forceinline__ Tiles tiles_of(const Unit& u0, const Unit& u1) {
 
 // Values that are not finite in the tiles that the guard looked at, added to a row that sees
 // them (channels i .. i + 31; its weights are positive, so they come out as they are).
-template <bool PAIR>
+template <bool PAIR, bool SPLIT>
 __device__ __forceinline__ void give_back(const PromptParams& P, const Item& it, int last, int head, int i, uint32_t (&x)[32]) {
-    const Tiles t = tiles_of(unit_of<PAIR>(it, 0, P.window), unit_of<PAIR>(it, 1, P.window));
+    const Tiles t = tiles_of(unit_of<PAIR, SPLIT>(it, 0, P.window), unit_of<PAIR, SPLIT>(it, 1, P.window));
     const int first = P.window > 0 ? last - P.window + 1 : 0, kvh = head / (P.H / P.H_kv);
 #pragma unroll 1
     for (int b = t.lo; b <= t.hi; ++b) {
@@ -221,7 +244,7 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&y)[16
 // the units' products, warp 3 finds the items and guards, warps 4 .. 11 are the units' softmax, 12 .. 15
 // write the outputs of both.  Everything is counted on from item to item, so the next item's first products run
 // while the last one's outputs are written.
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptParams P) {
     using L = Layout<D>;
     constexpr int kItemRows = PAIR ? kTileRows : 2 * kTileRows;
@@ -330,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             Item it;
             for (int w = 0; take(w, it, ok); ++w) {
                 release(w);
-                const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                const Unit u0 = unit_of<PAIR, SPLIT>(it, 0, P.window), u1 = unit_of<PAIR, SPLIT>(it, 1, P.window);
                 const Tiles t = tiles_of(u0, u1);
                 if (t.hi < t.lo) continue;
                 const int kvh = u0.head / rep;
@@ -425,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     if (!one(got)) return false;
                     if (lead) release(w);
                     ++w;
-                    const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                    const Unit u0 = unit_of<PAIR, SPLIT>(it, 0, P.window), u1 = unit_of<PAIR, SPLIT>(it, 1, P.window);
                     const Unit& u = s ? u1 : u0;
                     const Tiles t = tiles_of(u0, u1);
                     x = Walk{one(t.lo), one(t.lo), one(t.hi), one(u.any() ? u.lo : 0x7ffffff0), one(u.any() ? u.hi : -1),
@@ -517,6 +540,105 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             // ---- finder: the next item, the longest rows first (a sequence's last tiles have the most keys); false
             // when there is none
             const int all = P.items * P.groups;
+            // with splits: a sequence a lane, its row tiles with the length first .. first + tiles - 1 (in row tiles)
+            constexpr int kRatio = kItemRows / kTileKeys;
+            Item own;
+            int tiles = 0, first = 0, part_len = 1, n_part = 0, base = 0, n_parts = 1, seen = 0x7fffffff;
+            auto from = [&](int x) {   // row tiles at least x + 1 long
+                int n = max(first + tiles - max(x, first), 0);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+                return n;
+            };
+            if (SPLIT) {
+                if (lane < P.n_seq) tiles = tiles_of_sequence(lane, own);
+                if (tiles) first = max(own.n_k - own.n_q, 0) / kItemRows;
+                if (P.window > 0) seen = (P.window + kItemRows) / kTileKeys + 2;   // key tiles at most
+                const int k = min(max(seen / kRatio - first, 0), tiles);
+                float work = kRatio * (static_cast<float>(k) * first + 0.5f * k * (k + 1)) + (tiles - k) * static_cast<float>(tiles > k ? seen : 0);
+                int top = tiles ? first + tiles : 0;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    work += __shfl_xor_sync(kAll, work, o);
+                    top = max(top, __shfl_xor_sync(kAll, top, o));
+                }
+                const int longest = min(top > seen / kRatio ? seen : top * kRatio, seen);
+                // a part is no longer than an SM's share of the work
+                part_len = max(max(kMinPart, static_cast<int>(work * P.groups / kSMs) + 1), (longest + kMaxParts - 1) / kMaxParts);
+                n_parts = max((longest + part_len - 1) / part_len, 1);
+                int records = 0;
+#pragma unroll 1
+                for (int q = 0; q < n_parts; ++q) {   // lane q: items with more than q parts
+                    const int n = P.groups * from(q * part_len / kRatio);
+                    if (lane == q) {
+                        n_part = n;
+                        base = records;
+                    }
+                    if (q == 1) records = n;
+                    if (q == 1 && lane == 1) base = n;
+                    if (q) records += n;
+                }
+                if (records > P.n_records) n_parts = 1;
+                const int split = __shfl_sync(kAll, n_part, 1);
+                if (blockIdx.x == 0) {
+                    if (lane == 0) P.plan->items = n_parts > 1 ? split : 0;
+                    if (lane < kMaxParts) P.plan->base[lane] = base;
+                }
+            }
+            // a part of the longest rows first
+            auto find_part = [&](int i, Item& it) {
+                int q = n_parts - 1;
+#pragma unroll 1
+                for (; q >= 0; --q) {
+                    const int n = __shfl_sync(kAll, n_part, q);
+                    if (i < n) break;
+                    i -= n;
+                }
+                if (q < 0) return -1;
+                const int want = i / P.groups, record = __shfl_sync(kAll, base, q) + i;
+                int lo = 0, hi = 0, before = 0;
+                hi = first + tiles;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(kAll, hi, o));
+#pragma unroll 1
+                while (hi - lo > 1) {   // from(lo) > want >= from(hi) = before
+                    const int m = (lo + hi) / 2, n = from(m);
+                    if (n > want) {
+                        lo = m;
+                    } else {
+                        hi = m;
+                        before = n;
+                    }
+                }
+                const bool has = lo >= first && lo < first + tiles;
+                const uint32_t there = __ballot_sync(kAll, has);
+                const bool me = has && __popc(there & ((1u << lane) - 1)) == want - before;
+                if (me) {
+                    it = own;
+                    it.row = (lo - first) * kItemRows;
+                    it.group = i % P.groups;
+                    it.from = 0;
+                    it.to = 0x7fffffff;
+                    it.slot = -1;
+                    const int parts = n_parts > 1 ? min((min(lo >= seen / kRatio ? seen : (lo + 1) * kRatio, seen) + part_len - 1) / part_len, n_parts) : 1;
+                    if (parts > 1) {
+                        const Tiles t = tiles_of(unit_of<PAIR, SPLIT>(it, 0, P.window), unit_of<PAIR, SPLIT>(it, 1, P.window));
+                        const int len = (max(t.hi - t.lo + 1, 0) + parts - 1) / parts;
+                        if (len > 0) {
+                            it.from = t.lo + q * len;
+                            it.to = it.from + len - 1;
+                        }
+                        it.slot = record;
+                        if (q == 0) {
+                            P.heads[i].q0 = it.q0 + it.row;
+                            P.heads[i].rows = it.n_q - it.row;
+                            P.heads[i].group = it.group;
+                            P.heads[i].parts = parts;
+                        }
+                    }
+                }
+                return __ffs(__ballot_sync(kAll, me)) - 1;
+            };
             auto find = [&](int w) {
                 int found = -1;
                 Item it;
@@ -525,6 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     int i = 0;
                     if (lane == 0) i = static_cast<int>(atomicAdd(P.counter, 1u));
                     i = __shfl_sync(kAll, i, 0);
+                    if (SPLIT) {
+                        found = find_part(i, it);
+                        break;
+                    }
                     if (i >= all) break;
                     int want = P.items - 1 - i / P.groups;
                     // its chunk of sequences
@@ -594,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 if (w < 0) continue;
                 const Item it = items[w % kItems];
                 if (it.row < 0) break;
-                const Unit u0 = unit_of<PAIR>(it, 0, P.window), u1 = unit_of<PAIR>(it, 1, P.window);
+                const Unit u0 = unit_of<PAIR, SPLIT>(it, 0, P.window), u1 = unit_of<PAIR, SPLIT>(it, 1, P.window);
                 const Tiles t = tiles_of(u0, u1);
 #pragma unroll 1
                 for (int b = t.lo; b <= t.hi; ++b, n += 2) {
@@ -652,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         bool ok = true;
         Item it;
         for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
-            const Unit u = unit_of<PAIR>(it, s, P.window);
+            const Unit u = unit_of<PAIR, SPLIT>(it, s, P.window);
             float m = -INFINITY, l = 0.f;   // m: running maximum, in powers of two
 #pragma unroll 1
             for (int b = u.lo; b <= u.hi; ++b) {
@@ -758,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         for (int w = 0; __all_sync(kAll, take(w, it, ok)); ++w) {
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                const Unit u = unit_of<PAIR>(it, s, P.window);
+                const Unit u = unit_of<PAIR, SPLIT>(it, s, P.window);
                 const uint32_t to = tmem + kTmO + 128 * s + lanes;
                 float m = 0.f, l = 0.f;
                 if (u.any()) {
@@ -769,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     tc_fence_after();
                     asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(m), "=f"(l) : "r"(sums + (((n & 1) * 2 + s) * 128 + row) * 8) : "memory");
                 }
-                const float f = l != 0.f ? 1.f / l : 0.f;
+                const bool part = SPLIT && it.slot >= 0;
+                const float f = part ? 1.f : l != 0.f ? 1.f / l : 0.f;
                 const bool mine = row < u.rows;
                 // (set, if at all, before the products that bar_o told of)
                 const bool add = u.any() && *const_cast<volatile int*>(&dirty[w % kItems]);
@@ -789,8 +916,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
-                    if (add && mine) give_back<PAIR>(P, it, u.place + row, u.head, i, x);
-                    if (mine) {
+                    if (add && mine) give_back<PAIR, SPLIT>(P, it, u.place + row, u.head, i, x);
+                    if (part) {
+                        float4* p = reinterpret_cast<float4*>(P.records + static_cast<size_t>(it.slot) * kRecord<D> + (s * kTileRows + row) * D + i);
+                        if (mine && u.any())
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                p[j] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]), __uint_as_float(x[4 * j + 2]),
+                                                   __uint_as_float(x[4 * j + 3]));
+                    } else if (mine) {
                         uint32_t y[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) y[j] = pack_bf16(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
@@ -798,7 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     }
                     __syncwarp();
                 }
-                if (mine)
+                if (part) {
+                    if (mine)
+                        reinterpret_cast<float2*>(P.records + static_cast<size_t>(it.slot) * kRecord<D> + 2 * kTileRows * D)[s * kTileRows + row] =
+                            make_float2(m, l);
+                } else if (mine)
                     P.lse[static_cast<long long>(it.q0 + u.row + row) * P.H + u.head] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
             if (!ok) break;
@@ -812,6 +950,60 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmCols);
+    }
+}
+
+// Joins the records of a split item: 32 rows of a unit a block, a row a warp at a time.  After a timeout,
+// whose results are invalid, plan and heads may hold anything: it is checked before it is followed.
+constexpr int kJoinThreads = 256;
+template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
+    constexpr int C = D / 32;   // channels a lane
+    const int s = blockIdx.y / 4, lane = threadIdx.x % 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (static_cast<int>(blockIdx.x) >= P.plan->items || *P.status == kStatusTimeout) return;
+    const SplitHead head = P.heads[blockIdx.x];
+    const int h = PAIR ? 2 * head.group + s : head.group, unit_row = PAIR ? 0 : s * kTileRows, rows = min(head.rows - unit_row, kTileRows);
+    if (head.parts < 1 || head.parts > kMaxParts || head.q0 < 0 || head.q0 >= P.total_q || rows > P.total_q - head.q0 - unit_row ||
+        h < 0 || h >= P.H)
+        return;
+    for (int p = 0; p < head.parts; ++p)
+        if (P.plan->base[p] < 0 || P.plan->base[p] >= P.n_records - static_cast<int>(blockIdx.x)) return;
+    auto record = [&](int p) { return P.records + (static_cast<size_t>(P.plan->base[p]) + blockIdx.x) * kRecord<D>; };
+#pragma unroll 1
+    for (int row = blockIdx.y % 4 * 32 + threadIdx.x / 32; row < min(rows, static_cast<int>(blockIdx.y) % 4 * 32 + 32); row += kJoinThreads / 32) {
+        const int at = s * kTileRows + row;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < head.parts) ml = reinterpret_cast<const float2*>(record(lane) + 2 * kTileRows * D)[at];
+        float m = ml.y != 0.f ? ml.x : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        const float base = m == -INFINITY ? 0.f : m, k = ml.y != 0.f ? ex2(ml.x - base) : 0.f;
+        float l = ml.y != 0.f ? k * ml.y : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+        const uint32_t some = __ballot_sync(kAll, ml.y != 0.f);
+        float x[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = 0.f;
+        for (int p = 0; p < head.parts; ++p) {
+            const float kp = __shfl_sync(kAll, k, p);
+            if (!(some >> p & 1u)) continue;   // (its outputs may not be there)
+            const float* y = record(p) + at * D + C * lane;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                // a value that is not finite counts whatever the weight has become
+                const float v = y[c];
+                x[c] += fabsf(v) < INFINITY ? kp * v : v;
+            }
+        }
+        const float f = l != 0.f ? 1.f / l : 0.f;
+        const long long out = (static_cast<long long>(head.q0 + unit_row) + row) * P.H + h;
+        uint32_t w[C / 2];
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) w[c] = pack_bf16(x[2 * c] * f, x[2 * c + 1] * f);
+        if constexpr (C == 4) *reinterpret_cast<uint2*>(P.o + out * D + C * lane) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(P.o + out * D + C * lane) = w[0];
+        if (lane == 0) P.lse[out] = l != 0.f ? (base + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -844,6 +1036,16 @@ bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool can_split(int n_seq, long long items) { return n_seq <= 32 && items <= kSplitItems; }
+
+template <int D, bool PAIR, bool SPLIT> cudaError_t start(const PromptParams& P, int blocks, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Layout<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    prompt_tc_kernel<D, PAIR, SPLIT><<<blocks, kThreads, Layout<D>::kSmem, s>>>(P);
+    return cudaGetLastError();
+}
+
 template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
     PromptParams P;
     // without keys nothing is loaded; the maps then describe the queries
@@ -868,16 +1070,43 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
     P.counter = a.status + 1;
     P.chunk = 32 * ((a.n_seq + 32 * kChunks - 1) / (32 * kChunks));
     P.chunks = (a.n_seq + P.chunk - 1) / P.chunk;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Layout<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    prompt_tc_kernel<D, PAIR><<<static_cast<int>(grid < kSMs ? grid : kSMs), kThreads, Layout<D>::kSmem, s>>>(P);
-    return cudaGetLastError();
+    // long rows and few of them (a window's rows are no longer than it)
+    const bool split = can_split(a.n_seq, grid) && a.total_k > 2 * kMinPart * kTileKeys &&
+                       (a.window == 0 || a.window > 2 * kMinPart * kTileKeys);
+    if (split) {
+        P.plan = static_cast<SplitPlan*>(a.scratch);
+        P.heads = reinterpret_cast<SplitHead*>(P.plan + 1);
+        P.records = reinterpret_cast<float*>(P.heads + grid);
+        P.n_records = static_cast<int>(grid) + kSMs;
+        cudaError_t e = start<D, PAIR, true>(P, kSMs, s);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), 8);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.stream = s;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, PAIR>, P);
+    }
+    return start<D, PAIR, false>(P, static_cast<int>(grid < kSMs ? grid : kSMs), s);
 }
 
 }  // namespace
 
 bool prompt_tc_supported(int io, int d) { return io == 1 && (d == 64 || d == 128); }
+
+size_t prompt_tc_scratch(int n_seq, int total_q, int H, int H_kv, int d) {
+    if (n_seq <= 0 || total_q <= 0 || H <= 0 || H_kv <= 0) return 0;
+    const bool pair = (H / H_kv) % 2 == 0;
+    const long long tiles = total_q / (pair ? kTileRows : 2 * kTileRows) + (n_seq < total_q ? n_seq : total_q),
+                    items = tiles * (pair ? H / 2 : H);
+    if (!can_split(n_seq, items)) return 0;
+    return sizeof(SplitPlan) + items * sizeof(SplitHead) +
+           (items + kSMs) * sizeof(float) * (d == 128 ? kRecord<128> : kRecord<64>);
+}
 
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s) {
     const bool pair = (a.H / a.H_kv) % 2 == 0;
