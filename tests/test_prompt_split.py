@@ -52,3 +52,49 @@ def test_workspace_reused_and_invalid_bounds():
     o = torch.full_like(q, 3.0)
     kdn.kdn_prompt_attention(q, k, v, cu_q, bad, workspace=ws, out=(o, torch.empty_like(a[1])))
     assert kdn.kdn_read_device_status(ws) == 9 and bool((o == 3).all())
+
+
+@pytest.mark.parametrize("lq,lk,H,hkv,d", [([130, 1, 300, 0, 77], [6130, 9000, 300, 40, 7500], 2, 1, 64), ([1], [9001], 2, 2, 128),
+                                           ([257, 2], [7000, 6700], 3, 1, 128), ([3, 140], [100, 20000], 2, 1, 128)])
+@pytest.mark.parametrize("window", [0, 6000])
+def test_longer_keys(lq, lk, H, hkv, d, window):
+    _run(lq, lk, H, hkv, d, "bf16", window)
+
+
+@pytest.mark.parametrize("d,hkv", [(128, 1), (64, 2)])
+def test_special_values_in_parts(d, hkv):
+    import uncertainty_aware_delta_gb300 as kdn
+
+    q, k, v, cu_q, cu_k = _inputs([140, 9], [9000, 7600], 2, hkv, d, "bf16", seed=4)
+    k *= (1 + 3 * torch.arange(k.shape[0], device="cuda") / k.shape[0]).to(k.dtype)[:, None, None]
+    v[8950, :, 5] = float("inf")      # in the masked tiles, seen by the last rows
+    v[8940, :, 6] = float("nan")
+    v[9000 + 7598, :, 7] = -float("inf")
+    v[8999, :, 8] = float("inf")
+    want = _expect(q, k, v, cu_q, cu_k, 0)
+    o, lse = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k)
+    got = _np(o)
+    for c in (5, 6, 7, 8):
+        a, b = got[..., c], want[0][..., c]
+        odd = ~(abs(b) < float("inf"))
+        assert odd.any() and ((a == b) | (a != a) & (b != b))[odd].all()
+    keep = [i for i in range(d) if i not in (5, 6, 7, 8)]
+    ref.check(got[..., keep], _np(lse), (want[0][..., keep], want[1], want[2][..., keep], want[3]), "bf16")
+    ws = torch.randint(0, 256, (kdn.prompt_attention_workspace_size(2, 149, 2, hkv, d),), dtype=torch.uint8, device="cuda")
+    again = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws)
+    assert torch.equal(again[0].nan_to_num(), o.nan_to_num()) and torch.equal(again[1], lse)
+    with pytest.raises(ValueError):
+        kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws[:-1])
+
+
+def test_timeout_of_parts():
+    import uncertainty_aware_delta_gb300 as kdn
+
+    q, k, v, cu_q, cu_k = _inputs([3], [9000], 4, 2, 128, "bf16")
+    ws = torch.empty(kdn.prompt_attention_workspace_size(1, 3, 4, 2, 128), dtype=torch.uint8, device="cuda")
+    want = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k)
+    kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws, flags=kdn.KDN_FLAG_TIMEOUT_PROBE)
+    assert kdn.kdn_read_device_status(ws) == 8
+    got = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws)
+    assert kdn.kdn_read_device_status(ws) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -22,6 +22,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <mutex>
 
 #include "attention.h"
@@ -36,8 +37,10 @@ using namespace sm100;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr int kThreads = 512;                 // loader, two product warps, finder and guard; 2 softmax and 1 output warpgroups
-// registers: launched with 128 a thread; 96 + 2 x 168 + 80 = 4 x 128
-constexpr int kAuxRegs = 96, kSoftmaxRegs = 168, kOutputRegs = 80;
+// registers: launched with 128 a thread; 96 + 2 x 168 + 80 = 4 x 128, and 96 + 2 x 152 + 112 where outputs may be parts
+constexpr int kAuxRegs = 96;
+template <bool SPLIT> constexpr int kSoftmaxRegs = SPLIT ? 152 : 168;
+template <bool SPLIT> constexpr int kOutputRegs = SPLIT ? 112 : 80;
 constexpr int kItems = 3, kChunks = 128;     // items known ahead; chunks of sequences
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr int kSMs = 152;                     // GB300
@@ -144,8 +147,12 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 
 // What a block works on: a row tile of one sequence and a group of heads.
 // Few items, some of them long: the keys of a long one are split over several, whose sums a second kernel joins.
+// Measured (us, split against whole, 16/2 heads of 128 unless stated): one token over 32768 47 / 384, 128 over 32768
+// 54 / 385, 4 x 64 over 16384 (8/1 heads of 64) 51 / 176, 8192 alone (2/1 heads) 71 / 105, 16384 alone (2/1) 171 / 199,
+// but 8192 alone (4/1 heads of 64) 91 / 93, 16 x 256 over up to 3840 63 / 60, 8 x 64 over 4096 (16/4) 73 / 61: the
+// longest item has to be longer than an SM's share of all by some 40 tiles.
 // A record has both units' outputs [2][128][d] (as far as they go) and their rows' maxima and sums [2][128][2].
-constexpr int kMaxParts = 16, kMinPart = 6;   // of a row; key tiles of a part
+constexpr int kMaxParts = 16, kMinPart = 6, kWorthParts = 40;   // of a row; key tiles of a part; see above
 constexpr int kSplitItems = 3 * kSMs;         // more items than this fill the SMs
 struct SplitPlan {
     int items, unused[15];    // items that are split, the first so many by their length
@@ -261,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                    bar_o_free = bar_o + 16, bar_v = bar_o_free + 16, bar_cut = bar_v + 32, bar_item = bar_cut + 32,
                    bar_item_free = bar_item + 8 * kItems, bar_turn = bar_item_free + 8 * kItems, bar_l = bar_turn + 16, bar_drain = bar_l + 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (SPLIT) asm volatile("griddepcontrol.launch_dependents;");
 
     if (tid == 0) {
         aborted = 0;
@@ -564,8 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 }
                 const int longest = min(top > seen / kRatio ? seen : top * kRatio, seen);
                 // a part is no longer than an SM's share of the work
-                part_len = max(max(kMinPart, static_cast<int>(work * P.groups / kSMs) + 1), (longest + kMaxParts - 1) / kMaxParts);
-                n_parts = max((longest + part_len - 1) / part_len, 1);
+                const int share = static_cast<int>(work * P.groups / kSMs) + 1;
+                part_len = max(max(kMinPart, share), (longest + kMaxParts - 1) / kMaxParts);
+                n_parts = longest - share > kWorthParts ? (longest + part_len - 1) / part_len : 1;
                 int records = 0;
 #pragma unroll 1
                 for (int q = 0; q < n_parts; ++q) {   // lane q: items with more than q parts
@@ -769,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         }
     } else if (warp < 12) {
         // ---- softmax: warpgroup s has unit s, a row a thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<SPLIT>));
         const int s = (warp - 4) / 4, row = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + kTmS + 128 * s + lanes, to = tmem + kTmO + 128 * s + lanes;
@@ -874,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         }
     } else {
         // ---- outputs of both units, a row a thread, while the softmax goes on with the next item
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs<SPLIT>));
         const int row = tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t no[2] = {0, 0};
@@ -918,12 +927,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
                     if (add && mine) give_back<PAIR, SPLIT>(P, it, u.place + row, u.head, i, x);
                     if (part) {
-                        float4* p = reinterpret_cast<float4*>(P.records + static_cast<size_t>(it.slot) * kRecord<D> + (s * kTileRows + row) * D + i);
+                        float* p = P.records + static_cast<size_t>(it.slot) * kRecord<D> + (s * kTileRows + row) * D + i;
                         if (mine && u.any())
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                p[j] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]), __uint_as_float(x[4 * j + 2]),
-                                                   __uint_as_float(x[4 * j + 3]));
+                            for (int j = 0; j < 32; j += 8)
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + j), "r"(x[j]), "r"(x[j + 1]),
+                                             "r"(x[j + 2]), "r"(x[j + 3]), "r"(x[j + 4]), "r"(x[j + 5]), "r"(x[j + 6]), "r"(x[j + 7])
+                                             : "memory");
                     } else if (mine) {
                         uint32_t y[16];
 #pragma unroll
@@ -953,27 +963,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     }
 }
 
-// Joins the records of a split item: 32 rows of a unit a block, a row a warp at a time.  After a timeout,
-// whose results are invalid, plan and heads may hold anything: it is checked before it is followed.
-constexpr int kJoinThreads = 256;
+// Joins the records of the split items, a row a warp.  After a timeout, whose results are invalid, plan and heads
+// may hold anything: they are checked before they are followed.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32, kJoinSteps = 2 * kTileRows / kJoinRows;
 template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
     constexpr int C = D / 32;   // channels a lane
-    const int s = blockIdx.y / 4, lane = threadIdx.x % 32;
+    const int lane = threadIdx.x % 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (static_cast<int>(blockIdx.x) >= P.plan->items || *P.status == kStatusTimeout) return;
-    const SplitHead head = P.heads[blockIdx.x];
-    const int h = PAIR ? 2 * head.group + s : head.group, unit_row = PAIR ? 0 : s * kTileRows, rows = min(head.rows - unit_row, kTileRows);
-    if (head.parts < 1 || head.parts > kMaxParts || head.q0 < 0 || head.q0 >= P.total_q || rows > P.total_q - head.q0 - unit_row ||
-        h < 0 || h >= P.H)
-        return;
-    for (int p = 0; p < head.parts; ++p)
-        if (P.plan->base[p] < 0 || P.plan->base[p] >= P.n_records - static_cast<int>(blockIdx.x)) return;
-    auto record = [&](int p) { return P.records + (static_cast<size_t>(P.plan->base[p]) + blockIdx.x) * kRecord<D>; };
+    if (*P.status == kStatusTimeout) return;
+    const long long steps = static_cast<long long>(min(max(P.plan->items, 0), P.n_records)) * kJoinSteps;
 #pragma unroll 1
-    for (int row = blockIdx.y % 4 * 32 + threadIdx.x / 32; row < min(rows, static_cast<int>(blockIdx.y) % 4 * 32 + 32); row += kJoinThreads / 32) {
-        const int at = s * kTileRows + row;
+    for (long long step = blockIdx.x; step < steps; step += gridDim.x) {
+        const int item = static_cast<int>(step / kJoinSteps), at = static_cast<int>(step % kJoinSteps) * kJoinRows + threadIdx.x / 32,
+                  s = at / kTileRows;
+        const SplitHead head = P.heads[item];
+        const int h = PAIR ? 2 * head.group + s : head.group, row = PAIR ? at % kTileRows : at;   // the item's row
+        if (row >= head.rows || head.q0 < 0 || head.q0 >= P.total_q - row || h < 0 || h >= P.H) continue;
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < head.parts) ml = reinterpret_cast<const float2*>(record(lane) + 2 * kTileRows * D)[at];
+        const float* y = nullptr;
+        if (lane < min(head.parts, kMaxParts)) {
+            const int base = P.plan->base[lane];
+            if (base >= 0 && base < P.n_records - item) {
+                y = P.records + static_cast<size_t>(base + item) * kRecord<D>;
+                ml = reinterpret_cast<const float2*>(y + 2 * kTileRows * D)[at];
+            }
+        }
         float m = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
@@ -981,23 +995,30 @@ template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prom
         float l = ml.y != 0.f ? k * ml.y : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-        const uint32_t some = __ballot_sync(kAll, ml.y != 0.f);
+        uint32_t some = __ballot_sync(kAll, ml.y != 0.f);   // (the others' outputs may not be there)
         float x[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) x[c] = 0.f;
-        for (int p = 0; p < head.parts; ++p) {
-            const float kp = __shfl_sync(kAll, k, p);
-            if (!(some >> p & 1u)) continue;   // (its outputs may not be there)
-            const float* y = record(p) + at * D + C * lane;
+#pragma unroll 1
+        while (some) {   // four at a time, in order
+            float v[4][C], kp[4];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                // a value that is not finite counts whatever the weight has become
-                const float v = y[c];
-                x[c] += fabsf(v) < INFINITY ? kp * v : v;
+            for (int i = 0; i < 4; ++i) {
+                const int p = some ? __ffs(some) - 1 : -1;
+                kp[i] = __shfl_sync(kAll, k, max(p, 0));
+                const float* z = reinterpret_cast<const float*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(y), max(p, 0)));
+                some &= some - 1;
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[i][c] = p >= 0 ? z[at * D + C * lane + c] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < C; ++c)   // a value that is not finite counts whatever the weight has become
+                    x[c] += fabsf(v[i][c]) < INFINITY ? kp[i] * v[i][c] : v[i][c];
         }
         const float f = l != 0.f ? 1.f / l : 0.f;
-        const long long out = (static_cast<long long>(head.q0 + unit_row) + row) * P.H + h;
+        const long long out = (static_cast<long long>(head.q0) + row) * P.H + h;
         uint32_t w[C / 2];
 #pragma unroll
         for (int c = 0; c < C / 2; ++c) w[c] = pack_bf16(x[2 * c] * f, x[2 * c + 1] * f);
@@ -1038,6 +1059,17 @@ bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d) {
 
 bool can_split(int n_seq, long long items) { return n_seq <= 32 && items <= kSplitItems; }
 
+// Whether an item is longer than an SM's share of all by more than parts cost, as far as the host can tell: with the
+// prefixes spread evenly, or, by far, with one sequence having them all.  (Where the kernel then finds rows that are
+// not worth it, being ready for it has cost some 5 us.)
+bool worth_splitting(const PromptArgs& a, long long items) {
+    const double prefix = a.total_k > a.total_q ? static_cast<double>(a.total_k) - a.total_q : 0.0,
+                 rows = static_cast<double>(a.total_q) / a.n_seq, seen = a.window > 0 ? a.window : 2147483648.0;
+    const double even = std::min(prefix / a.n_seq + rows, seen), most = std::min(prefix + rows, seen),
+                 share = items * std::min(prefix / a.n_seq + rows / 2, seen) / kSMs;
+    return even - share > kWorthParts * kTileKeys || most - share > 3.0 * kWorthParts * kTileKeys;
+}
+
 template <int D, bool PAIR, bool SPLIT> cudaError_t start(const PromptParams& P, int blocks, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, PAIR, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Layout<D>::kSmem);
@@ -1070,11 +1102,10 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
     P.counter = a.status + 1;
     P.chunk = 32 * ((a.n_seq + 32 * kChunks - 1) / (32 * kChunks));
     P.chunks = (a.n_seq + P.chunk - 1) / P.chunk;
-    // long rows and few of them (a window's rows are no longer than it)
-    const bool split = can_split(a.n_seq, grid) && a.total_k > 2 * kMinPart * kTileKeys &&
-                       (a.window == 0 || a.window > 2 * kMinPart * kTileKeys);
+    const bool split = can_split(a.n_seq, grid) && worth_splitting(a, grid);
     if (split) {
-        P.plan = static_cast<SplitPlan*>(a.scratch);
+        // (records are written in pieces of 32 bytes)
+        P.plan = reinterpret_cast<SplitPlan*>((reinterpret_cast<uintptr_t>(a.scratch) + 31) / 32 * 32);
         P.heads = reinterpret_cast<SplitHead*>(P.plan + 1);
         P.records = reinterpret_cast<float*>(P.heads + grid);
         P.n_records = static_cast<int>(grid) + kSMs;
@@ -1084,7 +1115,7 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
         at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at.val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(grid), 8);
+        cfg.gridDim = dim3(4 * kSMs);
         cfg.blockDim = dim3(kJoinThreads);
         cfg.stream = s;
         cfg.attrs = &at;
@@ -1104,7 +1135,7 @@ size_t prompt_tc_scratch(int n_seq, int total_q, int H, int H_kv, int d) {
     const long long tiles = total_q / (pair ? kTileRows : 2 * kTileRows) + (n_seq < total_q ? n_seq : total_q),
                     items = tiles * (pair ? H / 2 : H);
     if (!can_split(n_seq, items)) return 0;
-    return sizeof(SplitPlan) + items * sizeof(SplitHead) +
+    return 32 + sizeof(SplitPlan) + items * sizeof(SplitHead) +
            (items + kSMs) * sizeof(float) * (d == 128 ? kRecord<128> : kRecord<64>);
 }
 
