@@ -92,12 +92,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
             }
             const int tiles = (q1 - q0 + kRows - 1) / kRows;
             // items from row tile t of their sequence on
-            auto from = [&](int t) {
-                int n = max(tiles - t, 0);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
-                return n;
-            };
+            auto from = [&](int t) { return __reduce_add_sync(kAll, max(tiles - t, 0)); };
             const int all = from(0);
             here = item < all;
             if (!here) {

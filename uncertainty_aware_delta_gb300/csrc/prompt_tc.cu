@@ -553,23 +553,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             Item own;
             int tiles = 0, first = 0, part_len = 1, n_part = 0, base = 0, n_parts = 1, seen = 0x7fffffff;
             auto from = [&](int x) {   // row tiles at least x + 1 long
-                int n = max(first + tiles - max(x, first), 0);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
-                return n;
+                return __reduce_add_sync(kAll, max(first + tiles - max(x, first), 0));
             };
-            if (SPLIT) {
+            const bool ordered = SPLIT || P.n_seq <= 32;
+            if (ordered) {
                 if (lane < P.n_seq) tiles = tiles_of_sequence(lane, own);
                 if (tiles) first = max(own.n_k - own.n_q, 0) / kItemRows;
+                const int n = P.groups * from(0);
+                if (lane == 0) n_part = n;
+            }
+            if (SPLIT) {
                 if (P.window > 0) seen = (P.window + kItemRows) / kTileKeys + 2;   // key tiles at most
                 const int k = min(max(seen / kRatio - first, 0), tiles);
                 float work = kRatio * (static_cast<float>(k) * first + 0.5f * k * (k + 1)) + (tiles - k) * static_cast<float>(tiles > k ? seen : 0);
-                int top = tiles ? first + tiles : 0;
+                const int top = __reduce_max_sync(kAll, first + tiles);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    work += __shfl_xor_sync(kAll, work, o);
-                    top = max(top, __shfl_xor_sync(kAll, top, o));
-                }
+                for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
                 const int longest = min(top > seen / kRatio ? seen : top * kRatio, seen);
                 // a part is no longer than an SM's share of the work
                 const int share = static_cast<int>(work * P.groups / kSMs) + 1;
@@ -605,10 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 }
                 if (q < 0) return -1;
                 const int want = i / P.groups, record = __shfl_sync(kAll, base, q) + i;
-                int lo = 0, hi = 0, before = 0;
-                hi = first + tiles;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(kAll, hi, o));
+                int lo = 0, hi = __reduce_max_sync(kAll, first + tiles), before = 0;
 #pragma unroll 1
                 while (hi - lo > 1) {   // from(lo) > want >= from(hi) = before
                     const int m = (lo + hi) / 2, n = from(m);
@@ -629,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     it.from = 0;
                     it.to = 0x7fffffff;
                     it.slot = -1;
-                    const int parts = n_parts > 1 ? min((min(lo >= seen / kRatio ? seen : (lo + 1) * kRatio, seen) + part_len - 1) / part_len, n_parts) : 1;
+                    const int parts = SPLIT && n_parts > 1 ? min((min(lo >= seen / kRatio ? seen : (lo + 1) * kRatio, seen) + part_len - 1) / part_len, n_parts) : 1;
                     if (parts > 1) {
                         const Tiles t = tiles_of(unit_of<PAIR, SPLIT>(it, 0, P.window), unit_of<PAIR, SPLIT>(it, 1, P.window));
                         const int len = (max(t.hi - t.lo + 1, 0) + parts - 1) / parts;
@@ -656,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     int i = 0;
                     if (lane == 0) i = static_cast<int>(atomicAdd(P.counter, 1u));
                     i = __shfl_sync(kAll, i, 0);
-                    if (SPLIT) {
+                    if (ordered) {
                         found = find_part(i, it);
                         break;
                     }
