@@ -10,10 +10,10 @@
 // as many maxima, sums and roundings) where d = 64, and on short rows what lies between items: the
 // masked last tile, an item's outputs, code that has left the instruction cache.
 //
-// Measured: 8 prompts of 4096 tokens (16/4 heads of 128, causal) 404 us, 1360 TFLOP/s, 72% of the
+// Measured: 8 prompts of 4096 tokens (16/4 heads of 128, causal) 397 us, 1385 TFLOP/s, 73% of the
 // cuBLAS rate, and a pair of tiles in 2900 cycles; 24 prompts of up to 4095 through a window of
-// 1024 (16 heads of 64) 106 us, 475 TFLOP/s; 16 x up to 256 tokens over prefixes of up to 3840 (16/2 heads of
-// 128) 68 us, 325 TFLOP/s; one of 77 tokens 14.4 us.
+// 1024 (16 heads of 64) 102 us, 495 TFLOP/s; 16 x up to 256 tokens over prefixes of up to 3840 (16/2 heads of
+// 128) 57 us, 390 TFLOP/s; one of 77 tokens 14.4 us.
 //
 // The running maximum is raised only when a row's score passes it by 2^8: fp32 sums and
 // accumulators and bf16 weights have the range, and O (in TMEM) is then hardly ever rescaled.
@@ -147,12 +147,12 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 
 // What a block works on: a row tile of one sequence and a group of heads.
 // Few items, some of them long: the keys of a long one are split over several, whose sums a second kernel joins.
-// Measured (us, split against whole, 16/2 heads of 128 unless stated): one token over 32768 47 / 384, 128 over 32768
-// 54 / 385, 4 x 64 over 16384 (8/1 heads of 64) 51 / 176, 8192 alone (2/1 heads) 71 / 105, 16384 alone (2/1) 171 / 199,
-// but 8192 alone (4/1 heads of 64) 91 / 93, 16 x 256 over up to 3840 63 / 60, 8 x 64 over 4096 (16/4) 73 / 61: the
-// longest item has to be longer than an SM's share of all by some 40 tiles.
+// Measured (us, split against whole, 16/2 heads of 128 unless stated): one token over 32768 46 / 384, 128 over 32768
+// 53 / 385, 4 x 64 over 16384 (8/1 heads of 64) 51 / 176, 8192 alone (2/1 heads) 71 / 105, 16384 alone (2/1) 172 / 199,
+// 16 x 256 over up to 3840 57 / 66, 8192 alone (4/1 heads of 64) 89 / 93, 8 x 64 over 4096 (16/4) 63 / 61: the
+// longest item has to be longer than an SM's share of all by some 16 tiles.
 // A record has both units' outputs [2][128][d] (as far as they go) and their rows' maxima and sums [2][128][2].
-constexpr int kMaxParts = 16, kMinPart = 6, kWorthParts = 40;   // of a row; key tiles of a part; see above
+constexpr int kMaxParts = 16, kMinPart = 6, kWorthParts = 16;   // of a row; key tiles of a part; see above
 constexpr int kSplitItems = 3 * kSMs;         // more items than this fill the SMs
 struct SplitPlan {
     int items, unused[15];    // items that are split, the first so many by their length
@@ -545,10 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                 mbar_wait(bar_drain + 8 * s, 0, kWaitLimit);
             }
         } else if (warp == 3) {
-            // ---- finder: the next item, the longest rows first (a sequence's last tiles have the most keys); false
-            // when there is none
+            // ---- finder: the next item, the longest rows first: of up to 32 sequences by their length (24 ragged prompts
+            // 102 us against 107.5 sequence by sequence), of more by sequence, its last tiles first; false when there is none
             const int all = P.items * P.groups;
-            // with splits: a sequence a lane, its row tiles with the length first .. first + tiles - 1 (in row tiles)
+            // up to 32: a sequence a lane, its row tiles first + 1 .. first + tiles row tiles long
             constexpr int kRatio = kItemRows / kTileKeys;
             Item own;
             int tiles = 0, first = 0, part_len = 1, n_part = 0, base = 0, n_parts = 1, seen = 0x7fffffff;
@@ -1057,7 +1057,7 @@ bool can_split(int n_seq, long long items) { return n_seq <= 32 && items <= kSpl
 
 // Whether an item is longer than an SM's share of all by more than parts cost, as far as the host can tell: with the
 // prefixes spread evenly, or, by far, with one sequence having them all.  (Where the kernel then finds rows that are
-// not worth it, being ready for it has cost some 5 us.)
+// not worth it, being ready for it has cost some 4 us: 16 x 256 over 740 each, 43 against 39.)
 bool worth_splitting(const PromptArgs& a, long long items) {
     const double prefix = a.total_k > a.total_q ? static_cast<double>(a.total_k) - a.total_q : 0.0,
                  rows = static_cast<double>(a.total_q) / a.n_seq, seen = a.window > 0 ? a.window : 2147483648.0;
