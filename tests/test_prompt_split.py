@@ -98,3 +98,19 @@ def test_timeout_of_parts():
     got = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws)
     assert kdn.kdn_read_device_status(ws) == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_overlapping_bounds():
+    """Bounds out of order: more row tiles than queries; what the calls leave unwritten stays so, and nothing else is written."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    n, T, C = 31, 512, 9000
+    cu_q = torch.tensor([0, T] * 16, dtype=torch.int32, device="cuda")       # 0 .. T and, backwards, T .. 0
+    cu_k = torch.tensor([0, C] * 16, dtype=torch.int32, device="cuda")
+    q, k, v, _, _ = _inputs([T], [C], 4, 2, 64, "bf16")
+    need = kdn.prompt_attention_workspace_size(n, T, 4, 2, 64)
+    ws = torch.full((need + 4096,), 7, dtype=torch.uint8, device="cuda")
+    o, lse = kdn.kdn_prompt_attention(q, k, v, cu_q, cu_k, workspace=ws[:need])
+    assert kdn.kdn_read_device_status(ws) == 9 and bool((ws[need:] == 7).all())
+    one, lse_one = kdn.kdn_prompt_attention(q, k, v, cu_q[:2], cu_k[:2])
+    assert bool(((o.float() - one.float()).abs() <= 0.02).all()) and bool(((lse - lse_one).abs() < 1e-4).all())

@@ -59,8 +59,9 @@ struct PromptParams {
     int n_seq, total_q, total_k, H, H_kv, window, groups, items, chunk, chunks, probe, wide;
     struct SplitPlan* plan;
     struct SplitHead* heads;
-    float* records;
-    int n_records;
+    float* rows;         // [n_rows][d]
+    float2* sums;        // [n_rows]: maximum and sum
+    int n_rows, dense, row_step, unit_step;   // dense: rows by part, row and head, else by record
     float scale_log2;
 };
 
@@ -151,24 +152,25 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 // 53 / 385, 4 x 64 over 16384 (8/1 heads of 64) 51 / 176, 8192 alone (2/1 heads) 71 / 105, 16384 alone (2/1) 172 / 199,
 // 16 x 256 over up to 3840 57 / 66, 8192 alone (4/1 heads of 64) 89 / 93, 8 x 64 over 4096 (16/4) 63 / 61: the
 // longest item has to be longer than an SM's share of all by some 16 tiles.
-// A record has both units' outputs [2][128][d] (as far as they go) and their rows' maxima and sums [2][128][2].
+// A part's outputs stand in rows of d, with the rows' maxima and sums beside them: a record of 2 x 128 rows for every
+// part, or, where that is less, kMaxParts rows for every row that there is.
 constexpr int kMaxParts = 16, kMinPart = 6, kWorthParts = 16;   // of a row; key tiles of a part; see above
 constexpr int kSplitItems = 3 * kSMs;         // more items than this fill the SMs
 struct SplitPlan {
     int items, unused[15];    // items that are split, the first so many by their length
-    int base[kMaxParts];      // record of the first one's part p
+    int base[kMaxParts];      // record of the first one's part p (where there are records)
     int unused_too[32];
 };
 struct SplitHead {
     int q0, rows, group, parts, unused[4];   // first query, queries
 };
-template <int D> constexpr int kRecord = 2 * kTileRows * (D + 2);
+constexpr int kRecord = 2 * kTileRows;
 
 struct Item {
     int q0, n_q, k0, n_k;    // the sequence's rows
     int row;                 // first row of the item in its sequence; negative: no more items
     int group;
-    int from, to, slot;      // where rows may be split: key tiles that the item has, its record (negative: all of the row)
+    int from, to, slot;      // where rows may be split: key tiles that the item has, the first row of its part (negative: not a part)
 };
 struct Unit {
     int head, row, rows;     // rows: valid ones
@@ -586,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     if (q == 1 && lane == 1) base = n;
                     if (q) records += n;
                 }
-                if (records > P.n_records) n_parts = 1;
+                // (sequences may overlap where bounds are out of order: then there may be more items than room)
+                if (__shfl_sync(kAll, n_part, 0) > all || (!P.dense && records > P.n_rows / kRecord)) n_parts = 1;
                 const int split = __shfl_sync(kAll, n_part, 1);
                 if (blockIdx.x == 0) {
                     if (lane == 0) P.plan->items = n_parts > 1 ? split : 0;
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                             it.from = t.lo + q * len;
                             it.to = it.from + len - 1;
                         }
-                        it.slot = record;
+                        it.slot = P.dense ? (q * P.total_q + it.q0 + it.row) * P.H + (PAIR ? 2 : 1) * it.group : record * kRecord;
                         if (q == 0) {
                             P.heads[i].q0 = it.q0 + it.row;
                             P.heads[i].rows = it.n_q - it.row;
@@ -923,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     for (int j = 0; j < 32; ++j) x[j] = u.any() ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
                     if (add && mine) give_back<PAIR, SPLIT>(P, it, u.place + row, u.head, i, x);
                     if (part) {
-                        float* p = P.records + static_cast<size_t>(it.slot) * kRecord<D> + (s * kTileRows + row) * D + i;
+                        float* p = P.rows + static_cast<size_t>(it.slot + s * P.unit_step + row * P.row_step) * D + i;
                         if (mine && u.any())
 #pragma unroll
                             for (int j = 0; j < 32; j += 8)
@@ -939,9 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
                     __syncwarp();
                 }
                 if (part) {
-                    if (mine)
-                        reinterpret_cast<float2*>(P.records + static_cast<size_t>(it.slot) * kRecord<D> + 2 * kTileRows * D)[s * kTileRows + row] =
-                            make_float2(m, l);
+                    if (mine) P.sums[it.slot + s * P.unit_step + row * P.row_step] = make_float2(m, l);
                 } else if (mine)
                     P.lse[static_cast<long long>(it.q0 + u.row + row) * P.H + u.head] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
@@ -967,7 +968,7 @@ template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prom
     const int lane = threadIdx.x % 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (*P.status == kStatusTimeout) return;
-    const long long steps = static_cast<long long>(min(max(P.plan->items, 0), P.n_records)) * kJoinSteps;
+    const long long steps = static_cast<long long>(min(max(P.plan->items, 0), P.items * P.groups)) * kJoinSteps;
 #pragma unroll 1
     for (long long step = blockIdx.x; step < steps; step += gridDim.x) {
         const int item = static_cast<int>(step / kJoinSteps), at = static_cast<int>(step % kJoinSteps) * kJoinRows + threadIdx.x / 32,
@@ -978,10 +979,12 @@ template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prom
         float2 ml = make_float2(-INFINITY, 0.f);
         const float* y = nullptr;
         if (lane < min(head.parts, kMaxParts)) {
-            const int base = P.plan->base[lane];
-            if (base >= 0 && base < P.n_records - item) {
-                y = P.records + static_cast<size_t>(base + item) * kRecord<D>;
-                ml = reinterpret_cast<const float2*>(y + 2 * kTileRows * D)[at];
+            const long long id = (P.dense ? (static_cast<long long>(lane) * P.total_q + head.q0) * P.H + (PAIR ? 2 : 1) * head.group
+                                          : (static_cast<long long>(P.plan->base[lane]) + item) * kRecord) +
+                                 s * P.unit_step + at % kTileRows * P.row_step;
+            if (id >= 0 && id < P.n_rows) {
+                y = P.rows + id * D;
+                ml = P.sums[id];
             }
         }
         float m = ml.y != 0.f ? ml.x : -INFINITY;
@@ -1005,7 +1008,7 @@ template <int D, bool PAIR> __global__ void __launch_bounds__(kJoinThreads) prom
                 const float* z = reinterpret_cast<const float*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(y), max(p, 0)));
                 some &= some - 1;
 #pragma unroll
-                for (int c = 0; c < C; ++c) v[i][c] = p >= 0 ? z[at * D + C * lane + c] : 0.f;
+                for (int c = 0; c < C; ++c) v[i][c] = p >= 0 ? z[C * lane + c] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -1051,6 +1054,11 @@ bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d) {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows for parts, of at most kSplitItems items.
+int part_rows(int total_q, int H, long long items) {
+    return static_cast<int>(std::min((items + kSMs) * kRecord, static_cast<long long>(kMaxParts) * total_q * H));
 }
 
 bool can_split(int n_seq, long long items) { return n_seq <= 32 && items <= kSplitItems; }
@@ -1103,8 +1111,12 @@ template <int D, bool PAIR> cudaError_t launch(const PromptArgs& a, cudaStream_t
         // (records are written in pieces of 32 bytes)
         P.plan = reinterpret_cast<SplitPlan*>((reinterpret_cast<uintptr_t>(a.scratch) + 31) / 32 * 32);
         P.heads = reinterpret_cast<SplitHead*>(P.plan + 1);
-        P.records = reinterpret_cast<float*>(P.heads + grid);
-        P.n_records = static_cast<int>(grid) + kSMs;
+        P.rows = reinterpret_cast<float*>(P.heads + grid);
+        P.n_rows = part_rows(a.total_q, a.H, grid);
+        P.sums = reinterpret_cast<float2*>(P.rows + static_cast<size_t>(P.n_rows) * D);
+        P.dense = P.n_rows < (grid + kSMs) * kRecord ? 1 : 0;
+        P.row_step = P.dense ? a.H : 1;
+        P.unit_step = P.dense && PAIR ? 1 : kTileRows * P.row_step;
         cudaError_t e = start<D, PAIR, true>(P, kSMs, s);
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute at;
@@ -1131,8 +1143,7 @@ size_t prompt_tc_scratch(int n_seq, int total_q, int H, int H_kv, int d) {
     const long long tiles = total_q / (pair ? kTileRows : 2 * kTileRows) + (n_seq < total_q ? n_seq : total_q),
                     items = tiles * (pair ? H / 2 : H);
     if (!can_split(n_seq, items)) return 0;
-    return 32 + sizeof(SplitPlan) + items * sizeof(SplitHead) +
-           (items + kSMs) * sizeof(float) * (d == 128 ? kRecord<128> : kRecord<64>);
+    return 32 + sizeof(SplitPlan) + items * sizeof(SplitHead) + part_rows(total_q, H, items) * sizeof(float) * (d + 2);
 }
 
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s) {
