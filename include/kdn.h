@@ -585,8 +585,8 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
  * Status : KDN_ERR_RANGE when the bounds of a sequence run backwards or outside
  *          the totals (its rows are left unwritten); KDN_ERR_TIMEOUT.
  * Workspace: kdn_prompt_attention_workspace_size() bytes.  On the tensor-core path
- *          that is up to 85 MB where n_seq <= 32 and the queries are few (some 58,000
- *          rows of heads at most): long rows may then be split over their keys.
+ *          that is up to 81 MB where n_seq <= 32 and queries x H are some 117,000 at
+ *          most: rows with many keys may then be split over them.
  */
 size_t kdn_prompt_attention_workspace_size(int n_seq, int total_q, int H, int H_kv, int d, int io_dtype,
                                            uint32_t flags);

@@ -10,13 +10,15 @@
 // 4-byte loads a thread for 32 rows, 8 channels and 32 keys; a wider warp tile would not fit
 // its registers.
 //
-// Measured: 4 prompts of 700 to 1024 tokens in fp32 (16/4 heads of 64, causal) 200 us, 35 TFLOP/s (106 of
+// Measured: 4 prompts of 700 to 1024 tokens in fp32 (16/4 heads of 64, causal) 202 us, 35 TFLOP/s (105 of
 // TF32 products); bf16 prompts of 128 tokens (16 of them, 16/4 heads of 128) 84 us against the tcgen05
 // kernel's 14, one of 77 tokens 33 against 14.  Calls of a few rows tie (heads of 64, 1 x 16 tokens: 10.6
 // against 12.1), so the path goes by type and head size alone.
 //
-// The MMAs cut sums off instead of rounding them, which a long sum would show: products of
-// one tile are summed there, and added to the output in fp32.
+// The MMAs cut sums off instead of rounding them, which a long sum would show: they sum the products of
+// 32 channels, or of one tile's keys, and those are added up in fp32 (2000 tokens, heads of 128: an error of
+// 3.8e-7 of the outputs' norm, 4.5e-7 with products in fp32; with scores summed over all 128 channels, for 2% less
+// time, 1.1e-6).
 
 #include <cuda_bf16.h>
 
@@ -175,26 +177,37 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
             for (int n = 0; n < kKeys / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+        constexpr int kSum = D < 32 ? D : 32;   // channels summed by the MMAs; added up in fp32
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += kSum) {
+            float t[2][kKeys / 8][4] = {};
 #pragma unroll 2
-        for (int c = 0; c < D; c += 8) {
-            uint32_t ah[2][4], al[2][4];
+            for (int c = c0; c < c0 + kSum; c += 8) {
+                uint32_t ah[2][4], al[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = (32 * warp + 16 * i + g) * LD + c + q;
-                ah[i][0] = qh[at]; ah[i][1] = qh[at + 8 * LD]; ah[i][2] = qh[at + 4]; ah[i][3] = qh[at + 8 * LD + 4];
-                al[i][0] = ql[at]; al[i][1] = ql[at + 8 * LD]; al[i][2] = ql[at + 4]; al[i][3] = ql[at + 8 * LD + 4];
-            }
-            uint32_t bh[kKeys / 8][2], bl[kKeys / 8][2];
+                for (int i = 0; i < 2; ++i) {
+                    const int at = (32 * warp + 16 * i + g) * LD + c + q;
+                    ah[i][0] = qh[at]; ah[i][1] = qh[at + 8 * LD]; ah[i][2] = qh[at + 4]; ah[i][3] = qh[at + 8 * LD + 4];
+                    al[i][0] = ql[at]; al[i][1] = ql[at + 8 * LD]; al[i][2] = ql[at + 4]; al[i][3] = ql[at + 8 * LD + 4];
+                }
+                uint32_t bh[kKeys / 8][2], bl[kKeys / 8][2];
 #pragma unroll
-            for (int n = 0; n < kKeys / 8; ++n) {
-                const int at = (8 * n + g) * LD + c + q;
-                bh[n][0] = kh[at]; bh[n][1] = kh[at + 4];
-                bl[n][0] = kl[at]; bl[n][1] = kl[at + 4];
+                for (int n = 0; n < kKeys / 8; ++n) {
+                    const int at = (8 * n + g) * LD + c + q;
+                    bh[n][0] = kh[at]; bh[n][1] = kh[at + 4];
+                    bl[n][0] = kl[at]; bl[n][1] = kl[at + 4];
+                }
+                // part by part: the three products of one sum stand apart
+                products(t, al, bh);
+                products(t, ah, bl);
+                products(t, ah, bh);
             }
-            // part by part: the three products of one sum stand apart
-            products(s, al, bh);
-            products(s, ah, bl);
-            products(s, ah, bh);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < kKeys / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][n][e] += t[i][n][e];
         }
         // rows 2 i and 2 i + 1 of the thread: 16 i + g and 16 i + g + 8
 #pragma unroll
