@@ -250,7 +250,9 @@ kdn_status kdn_prompt_attention(int n_seq, int total_q, int total_k, int H, int 
                         {cu_k, 4 * ((size_t)n_seq + 1)}};
     if ((st = check_alias(out, in)) != KDN_OK) return st;
     a.n_seq = n_seq; a.total_q = total_q; a.total_k = total_k; a.H = H; a.H_kv = H_kv; a.d = d;
-    a.window = window; a.io = io_dtype; a.flags = flags;
+    // a window of all keys or more masks nothing: the kernels' sums with it stay in 32 bits
+    a.window = window < total_k ? window : 0;
+    a.io = io_dtype; a.flags = flags;
     a.scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)d);
     a.cu_q = cu_q; a.cu_k = cu_k; a.o = o; a.lse = lse;
     a.status = static_cast<uint32_t*>(workspace);

@@ -146,7 +146,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
         l[i] = 0.f;
     }
     const int last = min(place + rows - 1, n_keys - 1);                       // last key any row sees
-    const int low = a.window > 0 ? max(place - a.window + 1, 0) : 0;         // first
+    const int low = a.window > 0 && place >= a.window ? place - a.window + 1 : 0;   // first (place may be far below 0)
     const float to_log2 = a.scale * 1.4426950408889634f;
     for (int j0 = low / kKeys * kKeys; j0 <= last; j0 += kKeys) {
         const T* kp = static_cast<const T*>(a.k.p) + (static_cast<long long>(k0) + j0) * a.k.row + kvh * a.k.head;

@@ -186,7 +186,8 @@ template <bool PAIR, bool SPLIT> __device__ __forceinline__ Unit unit_of(const I
     u.row = it.row + (PAIR ? 0 : s * kTileRows);
     u.rows = min(kTileRows, it.n_q - u.row);
     u.place = it.n_k - it.n_q + u.row;
-    const int last = u.place + u.rows - 1, first = window > 0 ? max(u.place - window + 1, 0) : 0;
+    // (place may be far below 0)
+    const int last = u.place + u.rows - 1, first = window > 0 && u.place >= window ? u.place - window + 1 : 0;
     u.lo = first / kTileKeys;
     u.hi = u.rows > 0 && last >= 0 ? last / kTileKeys : u.lo - 1;
     if (SPLIT) {
