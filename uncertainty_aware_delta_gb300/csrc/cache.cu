@@ -446,9 +446,11 @@ template <bool WRITE> cudaError_t dispatch_rows(const CacheArgs& a, cudaStream_t
 }  // namespace
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s) {
-    const size_t smem = sizeof(int) * 2 * (static_cast<size_t>(a.n_req) + 1);
+    auto bytes = [](int n_req) { return static_cast<int>(sizeof(int)) * 2 * (n_req + 1); };
+    // the limit is the kernel's, shared by all host threads: always the same one, whatever this call needs
+    const int smem = bytes(a.n_req);
     const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+                                               bytes(kPlanMaxRequests));
     if (e != cudaSuccess) return e;
     const long long items = a.capacity > a.n_req ? a.capacity : a.n_req + 1;
     const long long want = (items + kPlanThreads - 1) / kPlanThreads;
