@@ -40,16 +40,36 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                        __uint_as_float(v.y & 0xffff0000u));
 }
-// The two TF32 parts of four numbers (an infinity has no second part).
-__device__ __forceinline__ void split4(float4 x, uint4& hi, uint4& lo) {
+// Puts four numbers in two TF32 parts at `at`; whether a first part is not finite.
+__device__ __forceinline__ bool put4(uint32_t* h, uint32_t* l, int at, float4 x) {
+    uint4 hi, lo;
     split_tf32(x.x, hi.x, lo.x);
     split_tf32(x.y, hi.y, lo.y);
     split_tf32(x.z, hi.z, lo.z);
     split_tf32(x.w, hi.w, lo.w);
-    if (!finite(x.x)) lo.x = 0;
-    if (!finite(x.y)) lo.y = 0;
-    if (!finite(x.z)) lo.z = 0;
-    if (!finite(x.w)) lo.w = 0;
+    *reinterpret_cast<uint4*>(h + at) = hi;
+    *reinterpret_cast<uint4*>(l + at) = lo;
+    // zero times a number that is not finite is NaN: one test for the four
+    const float none = fmaf(__uint_as_float(hi.x), 0.f, fmaf(__uint_as_float(hi.y), 0.f,
+                            fmaf(__uint_as_float(hi.z), 0.f, __uint_as_float(hi.w) * 0.f)));
+    return !(none == 0.f);
+}
+// The same where one is not.  An infinity has no second part (or, with `drop`, becomes a zero), and what would round up to one
+// (the largest numbers of fp32, such as a mask's lowest value) is cut off instead, in both parts, so that their sum is
+// no larger.
+__device__ void put4_odd(uint32_t* h, uint32_t* l, int at, float4 v, bool drop) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t hi, lo;
+        split_tf32(x[i], hi, lo);
+        if (!finite(__uint_as_float(hi))) {
+            hi = finite(x[i]) ? __float_as_uint(x[i]) & 0xffffe000u : drop ? 0u : hi;
+            lo = finite(x[i]) ? __float_as_uint(x[i] - __uint_as_float(hi)) & 0xffffe000u : 0u;
+        }
+        h[at + i] = hi;
+        l[at + i] = lo;
+    }
 }
 
 // c[i][n] += a[i] b[n]: two 16-row tiles by N 8-column tiles, independent of each other.
@@ -126,13 +146,16 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
     const int q0 = found[0], rows = found[1], k0 = found[2], n_keys = found[3], place = found[4];
     if (q0 < 0) return;
     const T* qp = static_cast<const T*>(a.q.p) + q0 * a.q.row + h * a.q.head;
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+    auto queries = [&](int i, auto put) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
-        uint4 hi, lo;
-        split4(r < rows ? load4(qp + r * a.q.row + c) : make_float4(0.f, 0.f, 0.f, 0.f), hi, lo);
-        *reinterpret_cast<uint4*>(qh + r * LD + c) = hi;
-        *reinterpret_cast<uint4*>(ql + r * LD + c) = lo;
-    }
+        return put(qh, ql, r * LD + c, r < rows ? load4(qp + r * a.q.row + c) : make_float4(0.f, 0.f, 0.f, 0.f));
+    };
+    bool odd_q = false;
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) odd_q |= queries(i, put4);
+    if (odd_q)   // rare, and every thread has its own: the loads above stay together
+#pragma unroll 1
+        for (int i = tid; i < kRows * (D / 4); i += kThreads)
+            queries(i, [](uint32_t* h, uint32_t* l, int at, float4 x) { put4_odd(h, l, at, x, false); });
     float o[2][D / 8][4], m[4], l[4];   // rows 16 i + g, + 8 of the warp's 32
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -151,24 +174,21 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
     for (int j0 = low / kKeys * kKeys; j0 <= last; j0 += kKeys) {
         const T* kp = static_cast<const T*>(a.k.p) + (static_cast<long long>(k0) + j0) * a.k.row + kvh * a.k.head;
         const T* vp = static_cast<const T*>(a.v.p) + (static_cast<long long>(k0) + j0) * a.v.row + kvh * a.v.head;
+        auto keys = [&](const T* p, long long step, int i, auto put) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            return put(r * LD + c, j0 + r < n_keys ? load4(p + r * step + c) : make_float4(0.f, 0.f, 0.f, 0.f));
+        };
         bool odd = false;
         for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4;
-            const bool in = j0 + r < n_keys;
-            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            uint4 hi, lo;
-            split4(in ? load4(kp + r * a.k.row + c) : zero, hi, lo);
-            *reinterpret_cast<uint4*>(kh + r * LD + c) = hi;
-            *reinterpret_cast<uint4*>(kl + r * LD + c) = lo;
-            float4 x = in ? load4(vp + r * a.v.row + c) : zero;
-            if (!(finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w))) {
-                odd = true;
-                x = make_float4(finite(x.x) ? x.x : 0.f, finite(x.y) ? x.y : 0.f, finite(x.z) ? x.z : 0.f, finite(x.w) ? x.w : 0.f);
-            }
-            split4(x, hi, lo);
-            *reinterpret_cast<uint4*>(vh + r * LD + c) = hi;
-            *reinterpret_cast<uint4*>(vl + r * LD + c) = lo;
+            odd |= keys(kp, a.k.row, i, [&](int at, float4 x) { return put4(kh, kl, at, x); });
+            odd |= keys(vp, a.v.row, i, [&](int at, float4 x) { return put4(vh, vl, at, x); });
         }
+        if (odd)
+#pragma unroll 1
+            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+                keys(kp, a.k.row, i, [&](int at, float4 x) { put4_odd(kh, kl, at, x, false); });
+                keys(vp, a.v.row, i, [&](int at, float4 x) { put4_odd(vh, vl, at, x, true); });
+            }
         odd = __syncthreads_or(odd);
         float s[2][kKeys / 8][4];
 #pragma unroll
