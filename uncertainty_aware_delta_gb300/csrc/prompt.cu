@@ -83,7 +83,7 @@ __device__ __forceinline__ void products(float (&c)[2][N][4], const uint32_t (&a
 
 // A masked key has no influence whatever it holds: keys outside the sequence are read as
 // zeros, scores are masked by selection, and a value that is not finite is taken out of the
-// tile and added to the rows that see it.
+// tile and added to the rows that see it.  A score with an infinity in it is what its products add up to.
 template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_kernel(const PromptArgs a) {
     constexpr int LD = D + 4;   // rows 4 banks apart: the fragments' loads are free of conflicts
     extern __shared__ __align__(16) uint32_t prompt_smem[];
@@ -189,7 +189,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
                 keys(kp, a.k.row, i, [&](int at, float4 x) { put4_odd(kh, kl, at, x, false); });
                 keys(vp, a.v.row, i, [&](int at, float4 x) { put4_odd(vh, vl, at, x, true); });
             }
-        odd = __syncthreads_or(odd);
+        odd = __syncthreads_or(odd || odd_q);
         float s[2][kKeys / 8][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -228,6 +228,33 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
                 for (int n = 0; n < kKeys / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[i][n][e] += t[i][n][e];
+        }
+        if (odd) {
+            // an infinity times the other operand's second part, zero or of the other sign, is not the product's: such
+            // scores are formed anew, from the products that are not finite (bit 8 r + 2 n + k: row r, key 8 n + 2 q + k)
+            uint32_t above = 0, below = 0;
+#pragma unroll 1
+            for (int b = 0; b < 32; ++b) {
+                const int row = 32 * warp + 8 * (b / 8) + g, j = b % 8 / 2 * 8 + 2 * q + b % 2;
+                if (row >= rows || j0 + j >= n_keys) continue;
+                float t = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 4) {
+                    const float4 x = load4(qp + row * a.q.row + c), y = load4(kp + j * a.k.row + c);
+                    if (!(finite(x.x) && finite(y.x))) t += x.x * y.x;
+                    if (!(finite(x.y) && finite(y.y))) t += x.y * y.y;
+                    if (!(finite(x.z) && finite(y.z))) t += x.z * y.z;
+                    if (!(finite(x.w) && finite(y.w))) t += x.w * y.w;
+                }
+                above |= static_cast<uint32_t>(!(t <= 0.f)) << b;   // (both where it is NaN)
+                below |= static_cast<uint32_t>(!(t >= 0.f)) << b;
+            }
+#pragma unroll
+            for (int b = 0; b < 32; ++b) {
+                float& x = s[b / 16][b % 8 / 2][b / 8 % 2 * 2 + b % 2];
+                if (above >> b & 1u) x = below >> b & 1u ? NAN : INFINITY;
+                else if (below >> b & 1u) x = -INFINITY;
+            }
         }
         // rows 2 i and 2 i + 1 of the thread: 16 i + g and 16 i + g + 8
 #pragma unroll
