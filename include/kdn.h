@@ -583,7 +583,8 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
  *          tensor cores, everything else on the CUDA-core path (fp32 products in
  *          3xTF32).
  * Status : KDN_ERR_RANGE when the bounds of a sequence run backwards or outside
- *          the totals (its rows are left unwritten); KDN_ERR_TIMEOUT.
+ *          the totals (its rows are left unwritten; a call without queries looks
+ *          at no bounds); KDN_ERR_TIMEOUT.
  * Workspace: kdn_prompt_attention_workspace_size() bytes.  On the tensor-core path
  *          that is up to 81 MB where n_seq <= 32 and queries x H are some 117,000 at
  *          most: rows with many keys may then be split over them.

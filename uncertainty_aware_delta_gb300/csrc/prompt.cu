@@ -72,6 +72,11 @@ __device__ void put4_odd(uint32_t* h, uint32_t* l, int at, float4 v, bool drop) 
     }
 }
 
+// Bounds of a sequence's queries and keys.
+__device__ __forceinline__ bool in_range(const PromptArgs& a, int q0, int q1, int k0, int k1) {
+    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
+}
+
 // c[i][n] += a[i] b[n]: two 16-row tiles by N 8-column tiles, independent of each other.
 template <int N>
 __device__ __forceinline__ void products(float (&c)[2][N][4], const uint32_t (&a)[2][4], const uint32_t (&b)[N][2]) {
@@ -107,10 +112,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
             int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
             if (s < a.n_seq) {
                 q0 = a.cu_q[s]; q1 = a.cu_q[s + 1]; k0 = a.cu_k[s]; k1 = a.cu_k[s + 1];
-                if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
-                    set_status(a.status, kStatusRange);
-                    q0 = q1 = 0;
-                }
+                if (!in_range(a, q0, q1, k0, k1)) q0 = q1 = 0;
             }
             const int tiles = (q1 - q0 + kRows - 1) / kRows;
             // items from row tile t of their sequence on
@@ -141,6 +143,10 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) prompt_
                 found[4] = (k1 - k0) - (q1 - q0) + row;   // place of the tile's first row among the keys
             }
         }
+    } else {   // the search ends where its item is: the blocks' other warps look at all bounds together
+        for (long long s = static_cast<long long>(blockIdx.x) * (kThreads - 32) + tid - 32; s < a.n_seq;
+             s += static_cast<long long>(gridDim.x) * (kThreads - 32))
+            if (!in_range(a, a.cu_q[s], a.cu_q[s + 1], a.cu_k[s], a.cu_k[s + 1])) set_status(a.status, kStatusRange);
     }
     __syncthreads();
     const int q0 = found[0], rows = found[1], k0 = found[2], n_keys = found[3], place = found[4];
