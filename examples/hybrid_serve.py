@@ -47,9 +47,11 @@ class Server:
         self.device = self.table.device
 
     def _plan(self, new, capacity):
-        plan = kdn.kdn_cache_plan(self.context, new, self.table, self.free, self.n_free, page=self.page, capacity=capacity)
+        # (table entries past a request's length mean nothing: until a plan is taken, another may be made in its place)
+        return kdn.kdn_cache_plan(self.context, new, self.table, self.free, self.n_free, page=self.page, capacity=capacity)
+
+    def _take(self, plan):
         self.n_free, self.context = plan.free_left, plan.seq_len
-        return plan
 
     def _mixer_inputs(self, layer, x):
         """q, k, v, log_alpha, omega, r of tokens x [n, dim]."""
@@ -74,6 +76,7 @@ class Server:
             cu.append(cu[-1] + n)
         plan = self._plan(torch.tensor(new, dtype=torch.int32, device=self.device), cu[-1])
         granted = plan.granted.tolist()
+        self._take(plan)
         # every request's tokens, cached and new, in one row each; the new ones are not read back from the cache
         seq = [c + n for c, n in zip(ctx, new)]
         request = torch.repeat_interleave(torch.tensor(seq)).to(self.device)
@@ -102,10 +105,12 @@ class Server:
         return x, granted
 
     def decode(self, x):
-        """One token x [requests, dim] for every request.  Returns its output."""
+        """One token x [requests, dim] for every request.  Returns its output.  Where pages run out nothing changes:
+        the call may be repeated once a request has been released."""
         plan = self._plan(torch.ones_like(self.context), self.R)
         if not bool(plan.granted.all()):
-            raise RuntimeError("the cache is out of pages: release a request")
+            raise RuntimeError("the cache is out of pages, or a request's row of the block table is full: release a request")
+        self._take(plan)
         for layer in self.layers:
             o = kdn.kdn_step("diag", *self._mixer_inputs(layer, x), layer["S"], layer["p"])
             x = x + o.view_as(x) @ layer["mix_out"]
