@@ -37,6 +37,11 @@ struct Request {
     bool ok;   // lengths in range
 };
 
+// Pages that n tokens take (n plus a page may pass 2^31 where page is no power of two).
+__device__ __forceinline__ int pages_of(int n, int page) {
+    return static_cast<int>((static_cast<uint32_t>(n) + static_cast<uint32_t>(page) - 1u) / static_cast<uint32_t>(page));
+}
+
 __device__ __forceinline__ Request request(const PlanArgs& a, int r) {
     Request q;
     q.ctx = a.context_len[r];
@@ -44,8 +49,8 @@ __device__ __forceinline__ Request request(const PlanArgs& a, int r) {
     const long long total = static_cast<long long>(q.ctx) + q.add;
     q.ok = q.ctx >= 0 && q.add >= 0 && total <= static_cast<long long>(a.table_width) * a.page;
     q.add = max(q.add, 0);
-    q.held = q.ok ? (q.ctx + a.page - 1) / a.page : 0;
-    q.need = q.ok ? static_cast<int>((total + a.page - 1) / a.page) - q.held : 0;
+    q.held = q.ok ? pages_of(q.ctx, a.page) : 0;
+    q.need = q.ok ? pages_of(static_cast<int>(total), a.page) - q.held : 0;
     return q;
 }
 
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
     for (int i = first; i < n_new; i += stride) {
         const int r = find(wanted, i);
         if (wanted[r + 1] > free_n) continue;
-        const int held = (a.context_len[r] + a.page - 1) / a.page;
+        const int held = pages_of(a.context_len[r], a.page);
         a.block_table[static_cast<size_t>(r) * a.table_width + held + i - wanted[r]] = a.free_pages[free_n - 1 - i];
     }
     for (int i = first; i < a.capacity; i += stride) {
