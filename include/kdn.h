@@ -581,7 +581,8 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
  *          others: KDN_ERR_UNSUPPORTED.
  * Sizes  : d in {16, 32, 64, 128}.  bf16 io with d = 64 or 128 runs on tcgen05
  *          tensor cores, everything else on the CUDA-core path (fp32 products in
- *          3xTF32).
+ *          3xTF32).  n_seq, total_q and total_k are below 2^31 - 2^25 (else
+ *          KDN_ERR_SHAPE).
  * Status : KDN_ERR_RANGE when the bounds of a sequence run backwards or outside
  *          the totals (its rows are left unwritten; a call without queries looks
  *          at no bounds); KDN_ERR_TIMEOUT.

@@ -201,11 +201,15 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
     return done(kdn::launch_cache_attention(a, s));
 }
 
+// Counts up to here: what loops and grids add to them (steps of a block's or a grid's threads, row tiles) stays in 32 bits.
+constexpr int kMostRows = 0x7fffffff - (1 << 25);
+
 static kdn_status check_prompt(int n_seq, int total_q, int total_k, int H, int H_kv, int d, int window, int io) {
     if (io != KDN_F32 && io != KDN_BF16) return KDN_ERR_DTYPE;
     if (n_seq < 0 || total_q < 0 || total_k < 0 || H < 0 || H_kv < 0 || window < 0) return KDN_ERR_SHAPE;
     if (H > 0 && (H_kv == 0 || H % H_kv)) return KDN_ERR_SHAPE;
     if (!prompt_dim(d)) return KDN_ERR_UNSUPPORTED;
+    if (n_seq > kMostRows || total_q > kMostRows || total_k > kMostRows) return KDN_ERR_SHAPE;
     if (H > 65535 || (double)total_q * H * d > 1.0e12 || (double)total_k * H_kv * d > 1.0e12) return KDN_ERR_SHAPE;
     return KDN_OK;
 }
