@@ -513,7 +513,8 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *          (that request is not granted; a negative new_len counts as 0), when
  *          free_count is outside [0, n_free] (cut off), or when the tokens exceed
  *          capacity.
- * Sizes  : n_req <= 16384 (else KDN_ERR_UNSUPPORTED), table_width * page < 2^31.
+ * Sizes  : n_req <= 16384 (else KDN_ERR_UNSUPPORTED); table_width * page < 2^31,
+ *          n_free and capacity below 2^31 - 2^25 (else KDN_ERR_SHAPE).
  * Workspace: 256 bytes, the device status word.
  */
 kdn_status kdn_cache_plan(int n_req, int page, int table_width, int n_free, int capacity,

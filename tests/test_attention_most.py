@@ -17,3 +17,11 @@ def test_prompt_counts(lib, what):  # noqa: F811
 
     assert call(**{what: MOST}) == 5 and call(**{what: MOST + 1}) == 2 and call(**{what: 2 ** 31 - 1}) == 2
     assert size(**{what: MOST}) > 0 and (size(**{what: MOST + 1}) == 0 or what == "nk")
+
+
+@pytest.mark.parametrize("what", ["n_free", "cap"])
+def test_plan_counts(lib, what):  # noqa: F811
+    def call(n_free=20, cap=64):
+        return lib.kdn_cache_plan(4, 16, 8, n_free, cap, *[vp(MB)] * 12, 0, None)
+
+    assert call(**{what: MOST}) == 5 and call(**{what: MOST + 1}) == 2 and call(**{what: 2 ** 31 - 1}) == 2

@@ -11,6 +11,9 @@
 
 namespace {
 
+// Counts up to here: what loops and grids add to them (steps of a block's or a grid's threads, row tiles) stays in 32 bits.
+constexpr int kMostRows = 0x7fffffff - (1 << 25);
+
 bool cache_dim(int d) { return d == 32 || d == 64 || d == 128; }
 bool prompt_dim(int d) { return d == 16 || cache_dim(d); }
 bool cache_page(int page) { return page >= kdn::kBlockTokens && page <= 1024 && page % kdn::kBlockTokens == 0; }
@@ -69,6 +72,7 @@ kdn_status kdn_cache_plan(int n_req, int page, int table_width, int n_free, int 
                           size_t workspace_bytes, kdn_stream_t stream) {
     if (n_req < 0 || table_width < 0 || n_free < 0 || capacity < 0) return KDN_ERR_SHAPE;
     if (!cache_page(page) || n_req > kdn::kPlanMaxRequests) return KDN_ERR_UNSUPPORTED;
+    if (n_free > kMostRows || capacity > kMostRows) return KDN_ERR_SHAPE;
     if ((long long)table_width * page > 0x7fffffffll) return KDN_ERR_SHAPE;
     if (!workspace || workspace_bytes < kStatusBytes) return KDN_ERR_WORKSPACE;
     if (!free_count || !free_left || !cu_new) return KDN_ERR_NULL;
@@ -200,9 +204,6 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
     if (!any) return KDN_OK;
     return done(kdn::launch_cache_attention(a, s));
 }
-
-// Counts up to here: what loops and grids add to them (steps of a block's or a grid's threads, row tiles) stays in 32 bits.
-constexpr int kMostRows = 0x7fffffff - (1 << 25);
 
 static kdn_status check_prompt(int n_seq, int total_q, int total_k, int H, int H_kv, int d, int window, int io) {
     if (io != KDN_F32 && io != KDN_BF16) return KDN_ERR_DTYPE;
