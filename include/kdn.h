@@ -555,8 +555,8 @@ kdn_status kdn_cache_read(int n_tok, int n_pages, int page, int H_kv, int d, int
  *          seq_len [n_seq] int32; max_len: a bound on seq_len that the host knows
  *          (it sets how many parts a long sequence is split into).
  * Outputs: o [n_seq, H, d] io_dtype; lse [n_seq, H] fp32.
- * Status : KDN_ERR_RANGE when a seq_len is negative or above max_len or
- *          table_width * page (cut off), or a table entry in use is outside the
+ * Status : KDN_ERR_RANGE when a seq_len is negative or above max_len,
+ *          table_width * page or 2^31 - 1024 (cut off), or a table entry in use is outside the
  *          cache (its keys count as not visible).
  * Workspace: kdn_cache_attention_workspace_size() bytes.
  */

@@ -13,6 +13,7 @@ namespace {
 
 // Counts up to here: what loops and grids add to them (steps of a block's or a grid's threads, row tiles) stays in 32 bits.
 constexpr int kMostRows = 0x7fffffff - (1 << 25);
+constexpr int kMostTokens = 0x7ffffc00;   // of a cached sequence
 
 bool cache_dim(int d) { return d == 32 || d == 64 || d == 128; }
 bool prompt_dim(int d) { return d == 16 || cache_dim(d); }
@@ -193,7 +194,10 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
                         {block_table, 4 * (size_t)n_seq * table_width}, {seq_len, 4 * (size_t)n_seq}};
     if ((st = check_alias(out, in)) != KDN_OK) return st;
     a.n_seq = n_seq; a.H = H; a.H_kv = H_kv; a.d = d; a.page = page; a.n_pages = n_pages;
-    a.table_width = table_width; a.max_len = max_len; a.window = window; a.io = io_dtype;
+    a.table_width = table_width;
+    // the kernel's places run up to a thousand past the last token
+    a.max_len = max_len < kMostTokens ? max_len : kMostTokens;
+    a.window = window; a.io = io_dtype;
     a.scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)d);
     a.cache = static_cast<const uint8_t*>(cache); a.block_table = block_table; a.seq_len = seq_len;
     a.o = o; a.lse = lse;
