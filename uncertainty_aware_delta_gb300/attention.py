@@ -46,6 +46,13 @@ def _tensor(t, name, dtype, shape, device):
     _refuse(t, name, dtype, shape, device, True)
 
 
+def _int(x, name):
+    """A number for a 32-bit argument (ctypes would cut it off; negative ones are the library's to refuse)."""
+    if -0x80000000 <= x <= 0x7fffffff:
+        return x
+    raise ValueError(f"{name} = {x} does not fit 32 bits")
+
+
 def _io(t, name):
     if not isinstance(t, torch.Tensor) or t.dtype not in _IO:
         raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
@@ -96,7 +103,7 @@ def _workspace(given, need, device, made):
 
 def cache_alloc(n_pages, page, H_kv, d, device="cuda"):
     """A zeroed cache: uint8 [n_pages, H_kv, page / 16, 18 d] (its pages' blocks of 16 tokens)."""
-    if library().kdn_cache_size(1, page, 1, d) == 0:
+    if library().kdn_cache_size(1, _int(page, "page"), 1, _int(d, "d")) == 0:
         raise KDNError(6, "kdn_cache_size rejected the arguments")
     return torch.zeros((n_pages, H_kv, page // 16, 18 * d), dtype=torch.uint8, device=device)
 
@@ -120,7 +127,8 @@ def kdn_cache_plan(context_len, new_len, block_table, free_pages, free_count, *,
     """
     device = context_len.device
     n, i32 = context_len.shape[0], torch.int32
-    width = block_table.shape[1]
+    width, page, capacity = _int(block_table.shape[1], "table_width"), _int(page, "page"), _int(capacity, "capacity")
+    n_free = _int(free_pages.shape[0], "n_free")
     made = []
     if out is None:
         empty = torch.empty
@@ -135,10 +143,10 @@ def kdn_cache_plan(context_len, new_len, block_table, free_pages, free_count, *,
             ((capacity,), (capacity,), (n + 1,), (n,), (n,), (1,)))]
     ws, ws_bytes = _workspace(workspace, 256, device, made)
     _call(library().kdn_cache_plan, device, stream,
-          (n, page, width, free_pages.shape[0], capacity,
+          (n, page, width, n_free, capacity,
            _tensor(context_len, "context_len", i32, (n,), device), _tensor(new_len, "new_len", i32, (n,), device),
            _tensor(block_table, "block_table", i32, (n, width), device),
-           _tensor(free_pages, "free_pages", i32, (free_pages.shape[0],), device),
+           _tensor(free_pages, "free_pages", i32, (n_free,), device),
            _tensor(free_count, "free_count", i32, (1,), device), *outs, ws, ws_bytes), made)
     return out
 
@@ -147,7 +155,7 @@ def kdn_cache_write(k, v, slot_map, cache, *, stream=None):
     """Quantise k, v [n, H_kv, d] (fp32 or bf16) into the cache's slots slot_map [n] (int64; negative: skipped)."""
     device, io = k.device, _io(k, "k")
     ptr, pages, page, heads, d = _cache(cache, device)
-    shape = (k.shape[0], heads, d)
+    shape = (_int(k.shape[0], "n"), heads, d)
     _call(library().kdn_cache_write, device, stream,
           (shape[0], pages, page, heads, d, io, *_rows(k, "k", k.dtype, shape, device),
            *_rows(v, "v", k.dtype, shape, device), _tensor(slot_map, "slot_map", torch.int64, shape[:1], device), ptr))
@@ -158,7 +166,7 @@ def kdn_cache_read(cache, slot_map, *, dtype=torch.bfloat16, out=None, stream=No
     """The values that slots hold: (k, v) [n, H_kv, d]; zeros for negative slots.  ``out=(k, v)`` writes into tensors."""
     device = cache.device
     ptr, pages, page, heads, d = _cache(cache, device)
-    shape = (slot_map.shape[0], heads, d)
+    shape = (_int(slot_map.shape[0], "n"), heads, d)
     made = []
     if out is None:
         made = [torch.empty(shape, dtype=dtype, device=device) for _ in range(2)]
@@ -172,7 +180,8 @@ def kdn_cache_read(cache, slot_map, *, dtype=torch.bfloat16, out=None, stream=No
 
 
 def cache_attention_workspace_size(n_seq, H, H_kv, d, max_len, window=0) -> int:
-    return int(library().kdn_cache_attention_workspace_size(n_seq, H, H_kv, d, max_len, window))
+    names = ("n_seq", "H", "H_kv", "d", "max_len", "window")
+    return int(library().kdn_cache_attention_workspace_size(*map(_int, (n_seq, H, H_kv, d, max_len, window), names)))
 
 
 def kdn_cache_attention(q, cache, block_table, seq_len, *, max_len=None, window=0, scale=None, out=None, workspace=None,
@@ -185,9 +194,11 @@ def kdn_cache_attention(q, cache, block_table, seq_len, *, max_len=None, window=
     """
     lib = library()
     device, io = q.device, _io(q, "q")
+    width, window = _int(block_table.shape[1], "table_width"), _int(window, "window")
+    if max_len is not None:
+        _int(max_len, "max_len")
     ptr, pages, page, heads, d = _cache(cache, device)
     n, H = q.shape[0], q.shape[1]
-    width = block_table.shape[1]
     if max_len is None:
         max_len = min(width * page, 0x7fffffff)
     made = []
@@ -207,7 +218,8 @@ def kdn_cache_attention(q, cache, block_table, seq_len, *, max_len=None, window=
 
 
 def prompt_attention_workspace_size(n_seq, total_q, H, H_kv, d, io=KDN_BF16, flags=0) -> int:
-    return int(library().kdn_prompt_attention_workspace_size(n_seq, total_q, H, H_kv, d, io, flags))
+    names = ("n_seq", "total_q", "H", "H_kv", "d", "io", "flags")
+    return int(library().kdn_prompt_attention_workspace_size(*map(_int, (n_seq, total_q, H, H_kv, d, io, flags), names)))
 
 
 def kdn_prompt_attention(q, k, v, cu_q, cu_k=None, *, window=0, scale=None, flags=0, out=None, workspace=None,
@@ -221,8 +233,8 @@ def kdn_prompt_attention(q, k, v, cu_q, cu_k=None, *, window=0, scale=None, flag
     lib = library()
     device, io = q.device, _io(q, "q")
     nq, H, d = q.shape
-    nk, heads = k.shape[0], k.shape[1]
-    n = cu_q.shape[0] - 1
+    nq, nk, heads = _int(nq, "total_q"), _int(k.shape[0], "total_k"), k.shape[1]
+    n, window, flags = cu_q.shape[0] - 1, _int(window, "window"), _int(flags, "flags")
     made = []
     if out is None:
         made = [torch.empty((nq, H, d), dtype=q.dtype, device=device), torch.empty((nq, H), dtype=torch.float32, device=device)]
