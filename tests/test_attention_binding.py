@@ -34,3 +34,17 @@ def test_numbers_past_32_bits(lib, name):  # noqa: F811
         for n in BIG:
             with pytest.raises(ValueError, match=name):
                 call(n)
+
+
+def test_workspace_that_is_not_dense():
+    """A view with strides covers less memory, or other memory, than its count of elements says."""
+    from uncertainty_aware_delta_gb300 import attention
+
+    cpu, made = torch.device("cpu"), []
+    buffer = torch.zeros(4096, dtype=torch.uint8)
+    assert attention._workspace(buffer, 4096, cpu, made) == (buffer.data_ptr(), 4096)
+    assert attention._workspace(buffer.view(torch.int32)[16:], 4000, cpu, made) == (buffer.data_ptr() + 64, 4032)
+    for bad in (buffer[:1].expand(4096), buffer[::2], buffer.view(64, 64)[:, :32], buffer.view(64, 64).t()[:32]):
+        with pytest.raises(ValueError, match="contiguous"):
+            attention._workspace(bad, 512, cpu, made)
+    assert not made

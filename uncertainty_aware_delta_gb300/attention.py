@@ -96,6 +96,8 @@ def _workspace(given, need, device, made):
         made.append(given)
     elif given.device != device:
         raise ValueError(f"workspace is on {given.device}, expected {device}")
+    elif not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     elif given.numel() * given.element_size() < need:
         raise ValueError(f"workspace holds {given.numel() * given.element_size()} bytes, {need} needed")
     return given.data_ptr(), given.numel() * given.element_size()
