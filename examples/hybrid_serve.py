@@ -44,11 +44,17 @@ class Server:
         self.free = torch.arange(pages - 1, -1, -1, **ints)     # a stack: the next page is its last
         self.n_free = torch.tensor([pages], **ints)
         self.context = torch.zeros(requests, **ints)
+        self.plan_ws = torch.empty(256, dtype=torch.uint8, device=device)   # its status word
         self.device = self.table.device
 
     def _plan(self, new, capacity):
         # (table entries past a request's length mean nothing: until a plan is taken, another may be made in its place)
-        return kdn.kdn_cache_plan(self.context, new, self.table, self.free, self.n_free, page=self.page, capacity=capacity)
+        plan = kdn.kdn_cache_plan(self.context, new, self.table, self.free, self.n_free, page=self.page, capacity=capacity,
+                                  workspace=self.plan_ws)
+        status = kdn.kdn_read_device_status(self.plan_ws)   # (waits, as reading what was granted would)
+        if status:
+            raise RuntimeError(f"the requests' lengths or the free pages: {kdn.status_string(status)}")
+        return plan
 
     def _take(self, plan):
         self.n_free, self.context = plan.free_left, plan.seq_len
@@ -109,7 +115,7 @@ class Server:
         the call may be repeated once a request has been released."""
         plan = self._plan(torch.ones_like(self.context), self.R)
         if not bool(plan.granted.all()):
-            raise RuntimeError("the cache is out of pages, or a request's row of the block table is full: release a request")
+            raise RuntimeError("the cache is out of pages: release a request")
         self._take(plan)
         for layer in self.layers:
             o = kdn.kdn_step("diag", *self._mixer_inputs(layer, x), layer["S"], layer["p"])
