@@ -463,7 +463,8 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *   - lse [rows, H] fp32 is log(sum over the visible keys of exp(scale q.k)).
  *     A row that sees no key gives o = 0 and lse = -infinity.
  *   - What a query does not see has no influence on its row, infinities and NaN
- *     included.
+ *     included.  A visible key whose score is -infinity has a weight of 0.
+ *   - Forward only.
  *   - Lengths, tables and slots are device data.  What lies outside its range is
  *     never followed: it is skipped or cut off, and KDN_ERR_RANGE is recorded in
  *     the status word of the calls that have a workspace.
@@ -582,11 +583,14 @@ kdn_status kdn_cache_attention(int n_seq, int H, int H_kv, int d, int page, int 
  *          others: KDN_ERR_UNSUPPORTED.
  * Sizes  : d in {16, 32, 64, 128}.  bf16 io with d = 64 or 128 runs on tcgen05
  *          tensor cores, everything else on the CUDA-core path (fp32 products in
- *          3xTF32).  n_seq, total_q and total_k are below 2^31 - 2^25 (else
+ *          3xTF32).  On tcgen05 the softmax weights are rounded to bf16 for their
+ *          product with v (their sum is fp32); KDN_FLAG_PORTABLE keeps them in
+ *          fp32.  n_seq, total_q and total_k are below 2^31 - 2^25 (else
  *          KDN_ERR_SHAPE).
  * Status : KDN_ERR_RANGE when the bounds of a sequence run backwards or outside
- *          the totals (its rows are left unwritten; a call without queries looks
- *          at no bounds); KDN_ERR_TIMEOUT.
+ *          the totals (its rows are left unwritten, and rows of others may be
+ *          where sequences then overlap; a call without queries looks at no
+ *          bounds); KDN_ERR_TIMEOUT.
  * Workspace: kdn_prompt_attention_workspace_size() bytes.  On the tensor-core path
  *          that is up to 81 MB where n_seq <= 32 and queries x H are some 117,000 at
  *          most: rows with many keys may then be split over them.

@@ -1,6 +1,9 @@
 """Binding of the attention layers beside the mixer (include/kdn.h): attention over whole
 prompts, the paged 4-bit key/value cache, and attention of one new token per sequence
-over it.  Argument marshalling only, as in :mod:`.binding`.
+over it.  Argument marshalling only, as in :mod:`.binding`; forward only, outputs carry no
+history.  What a call records on the GPU (a length or table entry out of range, a timeout) stands
+in the status word of its workspace: pass ``workspace`` and read it with
+``kdn_read_device_status``; one that the call makes for itself goes away with its status.
 """
 from __future__ import annotations
 
@@ -192,7 +195,7 @@ def kdn_cache_attention(q, cache, block_table, seq_len, *, max_len=None, window=
 
     q [n_seq, H, d] fp32 or bf16; block_table [n_seq, table_width], seq_len [n_seq] int32.
     ``max_len``: a bound on seq_len (None: what the table holds); ``window``: 0 or the number of
-    last tokens that are seen; ``scale``: None selects d^-1/2.  ``out=(o, lse)`` writes into tensors.
+    last tokens that are seen; ``scale``: None (or 0) selects d^-1/2.  ``out=(o, lse)`` writes into tensors.
     """
     lib = library()
     device, io = q.device, _io(q, "q")

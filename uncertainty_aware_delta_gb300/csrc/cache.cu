@@ -3,12 +3,14 @@
 // kdn_cache_read).  The cache's layout and the arithmetic are stated in include/kdn.h.
 //
 // Plan: two prefix sums over the requests (new tokens, new pages).  A few KB move, so what bounds it is the
-// launch and one block's chain of scans: 7.5 us for 256 requests of one token, 16.4 us for 1000 prompts
-// of 540,000 tokens (6.5 MB of slots and positions).
+// launch and one block's chain of scans: 7.5 us for 256 requests of one token, 16.3 us for 1000 prompts
+// of 540,000 tokens (6.5 MB of slots and positions), where every token also takes a search, its request's lengths
+// again and three divisions.
 // Write: per group of 32 values the scale max |x| / 7 and the codes rint(x / s); read: (code - 8) s.  Bytes bound
 // them: 2 d values in, 1.125 d bytes out of a token and head, and back.  65536 tokens of 4 heads of 128 in bf16, both
-// ways 345 MB: 90 us, 3.8 TB/s; what is left to the copy rate is the arithmetic of the codes (some 15 instructions
-// a value written) and the strided 2-byte places of the value codes.
+// ways 345 MB: 89 us, 3.9 TB/s (54 and 37; in fp32 63 and 64).  What is left to the copy rate: some 15 instructions a
+// value written, which keep 71% of the issue slots busy (64% where they are read), and in the rest of the time loads
+// are waited for.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

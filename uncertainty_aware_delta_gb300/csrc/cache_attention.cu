@@ -15,10 +15,12 @@
 // constants.  Scales multiply the scores per group (fp32), and the softmax weights per
 // group (values).
 //
-// Measured: 64 sequences of 1000 to 32768 tokens (bf16, 32/4 heads of 128) 90 us, 4.0 TB/s of cache,
-// where the unpacking and the MMAs of 8 heads are the bound (see above); 256 of 512 to 1536 tokens (fp32, 16/4
-// heads of 128) 72 us, 1.97 TB/s: two fp16 parts double the MMAs, and 4 of their 8 columns are heads;
-// one of 4096 tokens (bf16, 16/4) 14.3 us, the latency of two kernels.
+// Measured: 64 sequences of 1000 to 32768 tokens (bf16, 32/4 heads of 128) 89 us, 4.1 TB/s of cache.  The bytes do not
+// bound it there, nor does a pipe (issue slots 55% busy, ALU 45%, tensor 24%): registers leave three warps a
+// scheduler, and each mostly waits for its own last instruction.  256 of 512 to 1536 tokens (fp32, 16/4
+// heads of 128) 72 us, 1.97 TB/s: two warps a scheduler, two fp16 parts double the MMAs, and 4 of their 8 columns are
+// heads.  One of 4096 tokens (bf16, 16/4) 14.4 us, the latency of a memset and two kernels.  256 sequences through a
+// window of 1024 (16/4 heads of 128) 57 us in bf16, 76 in fp32.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -6,12 +6,12 @@
 // registers, a running maximum and sum a row, weights used as the next product's left operand
 // where they are (the keys of a step are taken in the order 0, 2, 4, 6, 1, 3, 5, 7, in which the
 // accumulators' columns are that operand's).  Operands are split once, when they are put into
-// shared memory.  What bounds it: the tensor pipe and shared memory, 24 MMAs against 32
-// 4-byte loads a thread for 32 rows, 8 channels and 32 keys; a wider warp tile would not fit
-// its registers.
+// shared memory.  What bounds it: two warps a scheduler (255 registers) that load, split and
+// multiply in turn, 24 MMAs against 32 4-byte loads a thread for 32 rows, 8 channels and 32 keys (the
+// tensor pipe is busy for 47% of the time, issue slots for 35%); a wider warp tile would not fit its registers.
 //
 // Measured: 4 prompts of 700 to 1024 tokens in fp32 (16/4 heads of 64, causal) 202 us, 35 TFLOP/s (105 of
-// TF32 products); bf16 prompts of 128 tokens (16 of them, 16/4 heads of 128) 84 us against the tcgen05
+// TF32 products), with heads of 128 381; bf16 prompts of 128 tokens (16 of them, 16/4 heads of 128) 84 us against the tcgen05
 // kernel's 14, one of 77 tokens 33 against 14.  Calls of a few rows tie (heads of 64, 1 x 16 tokens: 10.6
 // against 12.1), so the path goes by type and head size alone.
 //

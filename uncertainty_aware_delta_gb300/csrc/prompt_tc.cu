@@ -10,10 +10,10 @@
 // as many maxima, sums and roundings) where d = 64, and on short rows what lies between items: the
 // masked last tile, an item's outputs, code that has left the instruction cache.
 //
-// Measured: 8 prompts of 4096 tokens (16/4 heads of 128, causal) 397 us, 1385 TFLOP/s, 73% of the
+// Measured: 8 prompts of 4096 tokens (16/4 heads of 128, causal) 391 to 409 us, 1344 to 1406 TFLOP/s, 70 to 73% of the
 // cuBLAS rate, and a pair of tiles in 2900 cycles; 24 prompts of up to 4095 through a window of
 // 1024 (16 heads of 64) 102 us, 495 TFLOP/s; 16 x up to 256 tokens over prefixes of up to 3840 (16/2 heads of
-// 128) 57 us, 390 TFLOP/s; one of 77 tokens 14.4 us.
+// 128) 57 us, 390 TFLOP/s (42 of it this kernel, in which an SM is active for 62 to 92% of the time); one of 77 tokens 14.4 us.
 //
 // The running maximum is raised only when a row's score passes it by 2^8: fp32 sums and
 // accumulators and bf16 weights have the range, and O (in TMEM) is then hardly ever rescaled.
