@@ -83,7 +83,8 @@ typedef enum {
     KDN_ERR_TIMEOUT = 8,      /* device: a bounded wait gave up (results invalid)    */
     KDN_ERR_RANGE = 9,        /* device: a chunk's cumulative log-decay left the
                                  range the factored decay supports (results invalid);
-                                 attention calls: a length or table entry out of range */
+                                 attention and decay calls: a length, bound or table entry
+                                 out of range                                        */
     KDN_ERR_ALIAS = 10        /* an output overlaps an input (other than S/p resume) */
 } kdn_status;
 
@@ -443,6 +444,119 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
                                const float *S0, const float *p0,
                                void *o, float *S_T, float *p_T, uint32_t *status_out,
                                kdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A retention layer beside the mixer: linear attention with a fixed decay for each
+ * head (the memory of the mixer without its gain and innovation), and the norm and
+ * gate that a memory's outputs go through head by head.
+ *
+ * Conventions, besides the ones at the top
+ *   - q, k, v, x, gate and the upstream gradients are [rows, heads, d] with row and head
+ *     strides, as the attention calls below take them; outputs are dense.
+ *   - Sequences are dense (cu NULL: n_tok / n_seq tokens each, one after another, which is
+ *     [B, T, H, d]) or packed: sequence s has the rows cu[s] .. cu[s + 1].  cu [n_seq + 1] is
+ *     device data: a sequence whose bounds run backwards or outside n_tok is taken as empty, and
+ *     KDN_ERR_RANGE is recorded.  Rows of no sequence are left unwritten.
+ *   - States are [n_seq, H, dk, dv] fp32.
+ *   - A value that is not finite makes the outputs that depend on it not finite (infinities
+ *     may become NaN) and no others: not those of earlier tokens, of other heads or sequences.
+ *     Finite fp32 values above 3.4e38 (within 2^-12 of the type's largest) count as infinite.
+ */
+
+/*
+ * Linear attention with a decay for each head: with g = exp(log_decay[h]),
+ *
+ *   S_t = g S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t          (after the write)
+ *
+ * Inputs : q, k [n_tok, H, dk], v [n_tok, H, dv] io_dtype; log_decay [H] fp32, <= 0
+ *          (-infinity: g = 0); S0 or NULL (zero).
+ * Outputs: o [n_tok, H, dv] io_dtype; S_T: the states after the sequences' last tokens, the
+ *          resume points of kdn_decay_step or of a later call (S_T == S0 is allowed; that of
+ *          an empty sequence is its S0).
+ * Sizes  : dk, dv in {16, 32, 64, 128}; n_tok below 2^31 - 2^25.
+ * flags  : 0, KDN_FLAG_PORTABLE, KDN_FLAG_NO_SPLIT, KDN_FLAG_TIMEOUT_PROBE.
+ * Paths  : bf16 with dk and dv 64 or 128 on tcgen05 tensor cores, everything else on CUDA cores
+ *          (products in 3xTF32).  On tcgen05 the weights g^(i-j) (q_i k_j) and the state that a chunk
+ *          begins with are rounded to bf16 for their products with v and q; what is added to the
+ *          state is not (g^(m-1-j) v_j goes in as three bf16 parts), and the state itself is fp32.
+ *          Few sequences' heads are cut into segments that run side by side, as those of the mixer's
+ *          forward (KDN_FLAG_NO_SPLIT: they are not).
+ * Workspace: kdn_decay_workspace_size() bytes; its first 256 hold the status word.
+ */
+size_t kdn_decay_workspace_size(int n_seq, int n_tok, int H, int dk, int dv, int io_dtype, uint32_t flags);
+kdn_status kdn_decay_forward(int n_seq, int n_tok, int H, int dk, int dv, int io_dtype, uint32_t flags,
+                             const void *q, int64_t q_row, int64_t q_head,
+                             const void *k, int64_t k_row, int64_t k_head,
+                             const void *v, int64_t v_row, int64_t v_head,
+                             const float *log_decay, const float *S0, const int32_t *cu,
+                             void *o, float *S_T,
+                             void *workspace, size_t workspace_bytes, kdn_stream_t stream);
+
+/*
+ * One token of the same recurrence for each of B sequences, the states updated IN PLACE.
+ * Inputs : q, k [B, H, dk], v [B, H, dv] io_dtype, dense; log_decay [H].
+ * In/out : S [B, H, dk, dv] fp32.   Output: o [B, H, dv] io_dtype.   No workspace, no status.
+ */
+kdn_status kdn_decay_step(int B, int H, int dk, int dv, int io_dtype,
+                          const void *q, const void *k, const void *v, const float *log_decay,
+                          float *S, void *o, kdn_stream_t stream);
+
+/*
+ * Gradients of  L = sum(dO * o) + sum(dS_T * S_T)  of kdn_decay_forward (the decay is a
+ * constant of the layer and has none):
+ *
+ *   dq_t = S_t dO_t;   R_t = g R_{t+1} + q_t dO_t^T  from the end, dS_T added at the last token:
+ *   dk_t = R_t v_t,   dv_t = R_t^T k_t,   dS0 = g R_0.
+ *
+ * Inputs as for the forward call, and dO [n_tok, H, dv] io_dtype; dS_T (states) or NULL (zero).
+ * Outputs: grad_q, grad_k [n_tok, H, dk], grad_v [n_tok, H, dv] io_dtype, dense; grad_S0 (states,
+ * fp32; that of an empty sequence is its dS_T).  They must not overlap each other, the inputs or the
+ * workspace.  Sizes, flags, paths, status as for the forward; kdn_decay_backward_workspace_size() bytes.
+ */
+size_t kdn_decay_backward_workspace_size(int n_seq, int n_tok, int H, int dk, int dv, int io_dtype, uint32_t flags);
+kdn_status kdn_decay_backward(int n_seq, int n_tok, int H, int dk, int dv, int io_dtype, uint32_t flags,
+                              const void *q, int64_t q_row, int64_t q_head,
+                              const void *k, int64_t k_row, int64_t k_head,
+                              const void *v, int64_t v_row, int64_t v_head,
+                              const float *log_decay, const float *S0, const int32_t *cu,
+                              const void *dO, int64_t dO_row, int64_t dO_head, const float *dS_T,
+                              void *grad_q, void *grad_k, void *grad_v, float *grad_S0,
+                              void *workspace, size_t workspace_bytes, kdn_stream_t stream);
+
+typedef enum { KDN_ACT_NONE = 0, KDN_ACT_SILU = 1, KDN_ACT_SIGMOID = 2 } kdn_act;
+
+/*
+ * Norm of every row's groups of d channels, with an activation: over the channels of a group
+ *
+ *   xh = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps),   n = xh weight + bias
+ *   y  = act(n)           (gate NULL)
+ *   y  = n act(gate)      (gate [rows, groups, d])
+ *
+ * Inputs : x, gate [rows, groups, d] io_dtype; weight, bias [groups, d] fp32, each may be NULL
+ *          (one, zero); eps >= 0.
+ * Output : y [rows, groups, d] io_dtype, dense.  No workspace, no status.
+ * Sizes  : d a multiple of 8 up to 256; sums in fp32.
+ */
+kdn_status kdn_group_norm(int rows, int groups, int d, int act, float eps, int io_dtype,
+                          const void *x, int64_t x_row, int64_t x_head,
+                          const float *weight, const float *bias,
+                          const void *gate, int64_t gate_row, int64_t gate_head,
+                          void *y, kdn_stream_t stream);
+
+/*
+ * Its gradients for the upstream gradient dy [rows, groups, d] io_dtype: grad_x and (with a gate)
+ * grad_gate [rows, groups, d] io_dtype, dense; grad_weight and grad_bias [groups, d] fp32, summed over
+ * the rows in a fixed order (required where weight or bias are given, unused otherwise).
+ * Workspace: kdn_group_norm_backward_workspace_size() bytes (sums of the blocks).
+ */
+size_t kdn_group_norm_backward_workspace_size(int rows, int groups, int d, int io_dtype);
+kdn_status kdn_group_norm_backward(int rows, int groups, int d, int act, float eps, int io_dtype,
+                                   const void *x, int64_t x_row, int64_t x_head,
+                                   const float *weight, const float *bias,
+                                   const void *gate, int64_t gate_row, int64_t gate_head,
+                                   const void *dy, int64_t dy_row, int64_t dy_head,
+                                   void *grad_x, void *grad_gate, float *grad_weight, float *grad_bias,
+                                   void *workspace, size_t workspace_bytes, kdn_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Attention layers beside the mixer.  The pages' hybrid backbone alternates KDN

@@ -45,3 +45,13 @@ from .attention import (  # noqa: F401
     kdn_prompt_attention,
     prompt_attention_workspace_size,
 )
+from .retention import (  # noqa: F401
+    decay_backward_workspace_size,
+    decay_workspace_size,
+    group_norm_backward_workspace_size,
+    kdn_decay_backward,
+    kdn_decay_forward,
+    kdn_decay_step,
+    kdn_group_norm,
+    kdn_group_norm_backward,
+)

@@ -30,7 +30,9 @@ EXPORTED = (
     "kdn_backward", "kdn_backward_workspace_size", "kdn_gated_forward", "kdn_gated_workspace_size",
     "kdn_dense_workspace_size", "kdn_cache_plan", "kdn_cache_size", "kdn_cache_write", "kdn_cache_read",
     "kdn_cache_attention", "kdn_cache_attention_workspace_size", "kdn_prompt_attention",
-    "kdn_prompt_attention_workspace_size",
+    "kdn_prompt_attention_workspace_size", "kdn_decay_forward", "kdn_decay_workspace_size", "kdn_decay_step",
+    "kdn_decay_backward", "kdn_decay_backward_workspace_size", "kdn_group_norm", "kdn_group_norm_backward",
+    "kdn_group_norm_backward_workspace_size",
 )
 
 
@@ -113,6 +115,23 @@ def library():
             lib.kdn_prompt_attention_workspace_size.argtypes = [i32] * 6 + [u32]
             lib.kdn_prompt_attention.restype = i32
             lib.kdn_prompt_attention.argtypes = [i32] * 7 + [f32, i32, u32] + st * 3 + [vp] * 4 + [vp, sz, vp]
+            for name in ("kdn_decay_workspace_size", "kdn_decay_backward_workspace_size"):
+                getattr(lib, name).restype = sz
+                getattr(lib, name).argtypes = [i32] * 6 + [u32]
+            lib.kdn_decay_forward.restype = i32
+            lib.kdn_decay_forward.argtypes = [i32] * 6 + [u32] + st * 3 + [fp, fp, vp, vp, fp] + [vp, sz, vp]
+            lib.kdn_decay_step.restype = i32
+            lib.kdn_decay_step.argtypes = [i32] * 5 + [vp] * 3 + [fp, fp, vp, vp]
+            lib.kdn_decay_backward.restype = i32
+            lib.kdn_decay_backward.argtypes = [i32] * 6 + [u32] + st * 3 + [fp, fp, vp] + st + [fp] + [vp] * 3 + \
+                [fp] + [vp, sz, vp]
+            lib.kdn_group_norm.restype = i32
+            lib.kdn_group_norm.argtypes = [i32] * 4 + [f32, i32] + st + [fp, fp] + st + [vp, vp]
+            lib.kdn_group_norm_backward_workspace_size.restype = sz
+            lib.kdn_group_norm_backward_workspace_size.argtypes = [i32] * 4
+            lib.kdn_group_norm_backward.restype = i32
+            lib.kdn_group_norm_backward.argtypes = [i32] * 4 + [f32, i32] + st + [fp, fp] + st * 2 + [vp, vp, fp, fp] + \
+                [vp, sz, vp]
             lib.kdn_abi_version.restype = i32
             lib.kdn_abi_version.argtypes = []
             _lib = lib

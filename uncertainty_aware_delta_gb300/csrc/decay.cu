@@ -1,0 +1,490 @@
+// Linear attention with a decay for each head: the CUDA-core path (fp32 and small heads), the chaining of segments, and the
+// step of one token a sequence.  The tcgen05 path is decay_tc.cu.
+//
+// Chunk form, for tokens 0 .. m - 1 of a chunk, the state S that it begins with and g = exp(log_decay):
+//   o_i  = sum_{j <= i} g^(i - j) (q_i k_j) v_j + g^(i + 1) S^T q_i
+//   S'   = g^m S + sum_j g^(m - 1 - j) k_j v_j^T
+// and from the end (gradients), with S the state that the tokens behind leave, decayed to the chunk's last token:
+//   o_i  = sum_{j >= i} g^(j - i) (q_i k_j) v_j + g^(m - 1 - i) S^T q_i
+//   S'   = g^m S + sum_j g^(j + 1) k_j v_j^T
+// All powers are of whole numbers >= 0, so none overflows for g <= 1, and g = 0 (log_decay = -infinity) is a memory of the
+// token alone.  What is masked is left out by a choice, not by a factor of zero, so that a later token's infinity or NaN
+// stays out of earlier rows.
+
+#include <cuda_bf16.h>
+#include <algorithm>
+#include <math.h>
+
+#include "common.cuh"
+#include "decay.h"
+#include "kdn.h"
+#include "mma_tf32x3.cuh"
+
+namespace kdn {
+namespace {
+
+constexpr int kC = 32, kThreads = 256;   // tokens of a chunk; threads of a block
+constexpr int kSMs = 152;                // GB300
+constexpr uint32_t kAll = 0xffffffffu;
+
+// exp(l n) for a whole n >= 0: 1 for n = 0 whatever l is.
+__device__ __forceinline__ float power(float l, int n) { return n == 0 ? 1.f : expf(l * static_cast<float>(n)); }
+
+// exp(l n) as a sum of two fp32 numbers: the states of thousands of chunks are multiplied by it one after another, and the
+// rounding of one number close to 1 would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).
+__device__ __forceinline__ float2 power2(float l, int n) {
+    const float e = n == 0 ? 0.f : expm1f(l * static_cast<float>(n)), hi = 1.f + e, lo = e - (hi - 1.f);
+    return make_float2(hi, fabsf(lo) < INFINITY ? lo : 0.f);
+}
+
+// Tokens of sequence b: first row and length; false where its bounds run backwards or outside.
+__device__ __forceinline__ bool sequence(const DecayParams& P, int b, int& row, int& len) {
+    if (!P.cu) {
+        len = P.n_tok / P.n_seq;
+        row = b * len;
+        return true;
+    }
+    const int x = P.cu[b], y = P.cu[b + 1];
+    row = x;
+    len = y - x;
+    if (x >= 0 && y >= x && y <= P.n_tok) return true;
+    row = len = 0;
+    return false;
+}
+
+__device__ __forceinline__ float4 load4(const void* p, long long i, int io) {
+    if (io == KDN_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
+}
+
+// A warp's 16 x 8 NT tile of A B in 3xTF32 (fragments: mma_tf32x3.cuh), the MMAs' sums taken over 32 of K and then in fp32
+// (their accumulation is cut off, not rounded).  A(r, k) = A[r lda + k], or A[k lda + r] w[k] where TRANS;
+// B(k, c) = B[k bk + c bc].
+template <int NT, int K, bool TRANS>
+__device__ __forceinline__ void warp_product(float (&out)[NT][4], const float* A, int lda, const float* w, const float* B, int bk,
+                                             int bc) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    constexpr int kSpan = K < 32 ? K : 32;
+#pragma unroll 1
+    for (int k0 = 0; k0 < K; k0 += kSpan) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+        for (int k = k0; k < k0 + kSpan; k += 8) {
+            float a[4];
+            if (TRANS) {
+                const float w0 = w[k + q], w1 = w[k + q + 4];
+                a[0] = A[(k + q) * lda + g] * w0;
+                a[1] = A[(k + q) * lda + g + 8] * w0;
+                a[2] = A[(k + q + 4) * lda + g] * w1;
+                a[3] = A[(k + q + 4) * lda + g + 8] * w1;
+            } else {
+                a[0] = A[g * lda + k + q];
+                a[1] = A[(g + 8) * lda + k + q];
+                a[2] = A[g * lda + k + q + 4];
+                a[3] = A[(g + 8) * lda + k + q + 4];
+            }
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float* b = B + (k + q) * bk + (8 * n + g) * bc;
+                uint32_t bh0, bl0, bh1, bl1;
+                split_tf32(b[0], bh0, bl0);
+                split_tf32(b[4 * bk], bh1, bl1);
+                mma_m16n8k8_tf32(acc[n], al, bh0, bh1);
+                mma_m16n8k8_tf32(acc[n], ah, bl0, bl1);
+                mma_m16n8k8_tf32(acc[n], ah, bh0, bh1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[n][e] += acc[n][e];
+    }
+}
+
+// One block: a head of a sequence (or of a segment of it) and DVS of its value channels; the state in the registers of its
+// warps as their products' fragments, and in shared memory as the next chunk's operand.
+template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_kernel(const __grid_constant__ DecayParams P) {
+    // (rows apart by 4 or 8 banks: the fragments' loads meet no bank twice, but those of K^T two)
+    constexpr int LQ = DK + 4, LV = DVS + 8, LP = kC + 4;
+    extern __shared__ __align__(16) float sm[];
+    float *const sq = sm, *const sk = sq + kC * LQ, *const sv = sk + kC * LQ, *const ss = sv + kC * LV, *const sp = ss + DK * LV;
+    __shared__ float pw[kC + 1], wt[kC], rowf[kC];
+    __shared__ int bad_at[DVS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const DecayJob& J = P.job[blockIdx.z];
+    const int slices = J.dv / DVS, slice = blockIdx.x % slices, bh = blockIdx.x / slices, b = bh / P.H, h = bh % P.H,
+              seg = blockIdx.y, v0 = slice * DVS;
+    int row0, len;
+    if (!sequence(P, b, row0, len) && tid == 0 && blockIdx.x % P.H == 0) set_status(P.status, kStatusRange);
+    const bool outputs = P.pass != kStates;
+    if (P.pass != kWhole) {
+        if (static_cast<long long>(seg) * P.seg_len >= len) return;
+        row0 += seg * P.seg_len;
+        len = min(len - seg * P.seg_len, P.seg_len);
+    }
+    const float l = P.log_decay[h];
+    if (tid <= kC) pw[tid] = power(l, tid);
+
+    // warps' tiles of the state: 16 rows and NS tiles of 8 columns
+    constexpr int RT = DK / 16, WPR = 8 / RT, NS = DVS / 8 / WPR > 0 ? DVS / 8 / WPR : 1;
+    const int s_row = (warp / WPR) * 16, s_col = (warp % WPR) * NS * 8;
+    const bool s_mine = s_col < DVS;
+    const size_t elems = static_cast<size_t>(J.dk) * J.dv;
+    const float* in = nullptr;
+    float* end = nullptr;
+    int i_k = J.s_k, i_v = J.s_v, o_k = J.s_k, o_v = J.s_v;
+    if (P.pass == kWhole) {
+        in = J.S0 ? J.S0 + bh * elems : nullptr;
+        end = J.S_T ? J.S_T + bh * elems : nullptr;
+    } else {
+        float* st = P.states[blockIdx.z] + (static_cast<size_t>(bh) * P.nseg + seg) * elems;
+        i_k = o_k = J.dv;
+        i_v = o_v = 1;
+        if (P.pass == kStates) end = st;
+        else in = st;
+    }
+    float S[NS][4];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = s_row + g + 8 * (e >> 1), j = v0 + s_col + 8 * n + 2 * q + (e & 1);
+            S[n][e] = in && s_mine ? in[static_cast<size_t>(i) * i_k + static_cast<size_t>(j) * i_v] : 0.f;
+        }
+    __syncthreads();
+
+    constexpr int NQ = (kC * DK / 4 + kThreads - 1) / kThreads, NV = (kC * DVS / 4 + kThreads - 1) / kThreads;
+    float4 fq[NQ], fk[NQ], fv[NV];
+    const int chunks = (len + kC - 1) / kC;
+    // chunk n of the walk: its first token and how many there are
+    auto place = [&](int n, int& t0) {
+        t0 = (J.reverse ? chunks - 1 - n : n) * kC;
+        return min(kC, len - t0);
+    };
+    auto fetch = [&](int n) {
+        int t0;
+        const int m = place(n, t0);
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int e = x * kThreads + tid, t = e / (DK / 4), c = e % (DK / 4) * 4;
+            const bool there = t < m;
+            const long long r = static_cast<long long>(row0) + t0 + t;
+            fq[x] = there && outputs ? load4(J.q.p, r * J.q.row + h * J.q.head + c, P.io) : zero;
+            fk[x] = there ? load4(J.k.p, r * J.k.row + h * J.k.head + c, P.io) : zero;
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int e = x * kThreads + tid, t = e / (DVS / 4), c = e % (DVS / 4) * 4;
+            const long long r = static_cast<long long>(row0) + t0 + t;
+            fv[x] = t < m ? load4(J.v.p, r * J.v.row + h * J.v.head + v0 + c, P.io) : zero;
+        }
+    };
+    if (chunks > 0) fetch(0);
+    const float2 c_full = power2(l, kC);
+#pragma unroll 1
+    for (int n = 0; n < chunks; ++n) {
+        int t0;
+        const int m = place(n, t0);
+        // the state and the chunk's tokens into shared memory
+        if (s_mine && outputs)
+#pragma unroll
+            for (int x = 0; x < NS; ++x) {
+                float* d = ss + (s_row + g) * LV + s_col + 8 * x + 2 * q;
+                d[0] = S[x][0]; d[1] = S[x][1];
+                d[8 * LV] = S[x][2]; d[8 * LV + 1] = S[x][3];
+            }
+        int bad = 0;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int e = x * kThreads + tid, t = e / (DK / 4), c = e % (DK / 4) * 4;
+            if (t < kC) {
+                *reinterpret_cast<float4*>(sq + t * LQ + c) = fq[x];
+                *reinterpret_cast<float4*>(sk + t * LQ + c) = fk[x];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int e = x * kThreads + tid, t = e / (DVS / 4), c = e % (DVS / 4) * 4;
+            if (t < kC) *reinterpret_cast<float4*>(sv + t * LV + c) = fv[x];
+            bad |= !(fabsf(fv[x].x) + fabsf(fv[x].y) + fabsf(fv[x].z) + fabsf(fv[x].w) < INFINITY);
+        }
+        if (tid < kC) {
+            const int left = max(m - 1 - tid, 0);
+            wt[tid] = pw[J.reverse ? tid + 1 : left];
+            rowf[tid] = pw[J.reverse ? left : tid + 1];
+        }
+        bad = __syncthreads_or(bad);
+        if (n + 1 < chunks) fetch(n + 1);
+        if (bad) {
+            // A channel's values that are not finite are taken out of the products (a weight of zero would not stop them)
+            // and put into what the first of them reaches: the walk's later rows of the channel, and its state.
+            if (tid < DVS) {
+                int first = kC;   // in the order of the walk
+#pragma unroll 1
+                for (int i = m - 1; i >= 0; --i) {
+                    float& x = sv[(J.reverse ? m - 1 - i : i) * LV + tid];
+                    if (!(fabsf(x) < INFINITY)) {
+                        x = 0.f;
+                        first = i;
+                    }
+                }
+                bad_at[tid] = first;
+            }
+            __syncthreads();
+        }
+
+        if (outputs) {
+            // weights: 2 x 4 tiles, one a warp
+            const int r0 = (warp >> 2) * 16, c0 = (warp & 3) * 8;
+            float a[1][4] = {};
+            warp_product<1, DK, false>(a, sq + r0 * LQ, LQ, nullptr, sk + c0 * LQ, 1, LQ);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = r0 + g + 8 * (e >> 1), j = c0 + 2 * q + (e & 1), gap = J.reverse ? j - i : i - j;
+                sp[i * LP + j] = gap >= 0 ? a[0][e] * pw[max(gap, 0)] : 0.f;
+            }
+            __syncthreads();
+            constexpr int NO = DVS / 32 > 0 ? DVS / 32 : 1;
+            const int oc = (warp & 3) * NO * 8;
+            if (oc < DVS) {
+                float o[NO][4] = {}, y[NO][4] = {};
+                warp_product<NO, DK, false>(o, sq + r0 * LQ, LQ, nullptr, ss + oc, LV, 1);
+                warp_product<NO, kC, false>(y, sp + r0 * LP, LP, nullptr, sv + oc, LV, 1);
+                if (bad)
+#pragma unroll
+                    for (int x = 0; x < NO; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = r0 + g + 8 * (e >> 1);
+                            if (bad_at[oc + 8 * x + 2 * q + (e & 1)] <= (J.reverse ? m - 1 - i : i)) y[x][e] = NAN;
+                        }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int i = r0 + g + 4 * e;
+                    if (i >= m) continue;
+                    const float f = rowf[i];
+#pragma unroll
+                    for (int x = 0; x < NO; ++x) {
+                        const long long at = ((static_cast<long long>(row0) + t0 + i) * P.H + h) * J.dv + v0 + oc + 8 * x + 2 * q;
+                        const float u = fmaf(f, o[x][e], y[x][e]), w = fmaf(f, o[x][e + 1], y[x][e + 1]);
+                        if (P.io == KDN_F32) *reinterpret_cast<float2*>(static_cast<float*>(J.o) + at) = make_float2(u, w);
+                        else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(J.o) + at) = __floats2bfloat162_rn(u, w);
+                    }
+                }
+            }
+        }
+        if (s_mine && (end || n + 1 < chunks)) {
+            float u[NS][4] = {};
+            warp_product<NS, kC, true>(u, sk + s_row, LQ, wt, sv + s_col, LV, 1);
+            const float2 c = m == kC ? c_full : power2(l, m);
+#pragma unroll
+            for (int x = 0; x < NS; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S[x][e] = fmaf(c.x, S[x][e], fmaf(c.y, S[x][e], u[x][e]));
+                    if (bad && bad_at[s_col + 8 * x + 2 * q + (e & 1)] < kC) S[x][e] = NAN;
+                }
+        }
+        __syncthreads();
+    }
+    if (end && s_mine)
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = s_row + g + 8 * (e >> 1), j = v0 + s_col + 8 * n + 2 * q + (e & 1);
+                end[static_cast<size_t>(i) * o_k + static_cast<size_t>(j) * o_v] = S[n][e];
+            }
+}
+
+// Segments' own states -> the states that they begin with, and the last one: an element a thread.
+__global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_constant__ DecayParams P) {
+    const DecayJob& J = P.job[blockIdx.z];
+    const int elems = J.dk * J.dv, e = blockIdx.x * kThreads + threadIdx.x, bh = blockIdx.y, b = bh / P.H;
+    if (e >= elems) return;
+    int row0, len;
+    sequence(P, b, row0, len);
+    const float l = P.log_decay[bh % P.H], full = power(l, P.seg_len);
+    const size_t at = static_cast<size_t>(bh) * elems + static_cast<size_t>(e / J.dv) * J.s_k + static_cast<size_t>(e % J.dv) * J.s_v;
+    float* st = P.states[blockIdx.z] + static_cast<size_t>(bh) * P.nseg * elems + e;
+    float S = J.S0 ? J.S0[at] : 0.f;
+    const int n = (len + P.seg_len - 1) / P.seg_len;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int seg = J.reverse ? n - 1 - i : i;
+        float* p = st + static_cast<size_t>(seg) * elems;
+        const float own = *p;
+        *p = S;
+        S = fmaf(seg == n - 1 ? power(l, len - seg * P.seg_len) : full, S, own);
+    }
+    if (J.S_T) J.S_T[at] = S;
+}
+
+template <int DK, int DVS> cudaError_t start(const DecayParams& P, int n_jobs, cudaStream_t s) {
+    constexpr int bytes = 4 * (2 * kC * (DK + 4) + (kC + DK) * (DVS + 8) + kC * (kC + 4));
+    const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    decay_kernel<DK, DVS><<<dim3(P.n_seq * P.H * (P.job[0].dv / DVS), P.pass == kWhole ? 1 : P.nseg, n_jobs), kThreads, bytes, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <int DK> cudaError_t start_dv(const DecayParams& P, int n_jobs, cudaStream_t s) {
+    if (P.job[0].dv == 16) return start<DK, 16>(P, n_jobs, s);
+    if (P.job[0].dv == 32) return start<DK, 32>(P, n_jobs, s);
+    return start<DK, 64>(P, n_jobs, s);
+}
+
+// Jobs of the same head sizes in one launch.
+cudaError_t start_path(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s) {
+    if (tc) return launch_decay_tc(P, n_jobs, s);
+    switch (P.job[0].dk) {
+        case 16: return start_dv<16>(P, n_jobs, s);
+        case 32: return start_dv<32>(P, n_jobs, s);
+        case 64: return start_dv<64>(P, n_jobs, s);
+        default: return start_dv<128>(P, n_jobs, s);
+    }
+}
+cudaError_t start_pass(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s) {
+    bool same = true;
+    for (int i = 1; i < n_jobs; ++i) same = same && P.job[i].dk == P.job[0].dk && P.job[i].dv == P.job[0].dv;
+    if (same) return start_path(P, n_jobs, tc, s);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n_jobs && e == cudaSuccess; ++i) {
+        DecayParams one = P;
+        one.job[0] = P.job[i];
+        one.states[0] = P.states[i];
+        e = start_path(one, 1, tc, s);
+    }
+    return e;
+}
+
+bool use_tc(int io, int dk, int dv, uint32_t flags) { return !(flags & KDN_FLAG_PORTABLE) && decay_tc_supported(io, dk, dv); }
+
+// Few sequences' heads are cut into segments until there are blocks for all SMs.  A segment has a whole number of chunks of
+// both paths.
+DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
+    DecayPlan p = {1, 0};
+    if ((flags & KDN_FLAG_NO_SPLIT) || n_seq <= 0 || n_tok <= 0 || H <= 0) return p;
+    const bool tc = use_tc(io, dk, dv, flags);
+    const int most = std::max(dk, dv);
+    const long long per = static_cast<long long>(H) * n_jobs * (tc ? 1 : (most + 63) / 64);   // blocks a segment
+    const long long room = (tc ? kSMs : 2 * kSMs) / per;                                      // segments in all
+    const int shortest = 512;
+    if (room < 2ll * n_seq) return p;
+    const long long n = packed ? room - n_seq : room / n_seq, longest = packed ? n_tok : n_tok / n_seq;
+    const long long len = std::max<long long>(shortest, ((longest + n - 1) / n + 63) / 64 * 64);
+    if (len >= longest) return p;
+    p.seg_len = static_cast<int>(len);
+    p.nseg = static_cast<int>((longest + len - 1) / len);
+    return p;
+}
+
+// ---------------------------------------------------------------- one token a sequence
+// S = g S + k v^T, o = S^T q: a head a block, its state read once into registers, written once, and summed over the rows.
+constexpr int kRegs = 16;   // float4 of the state a thread, for 128 x 128
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ log_decay,
+                  float* __restrict__ S, T* __restrict__ o, int H, int DK, int DV) {
+    __shared__ float s_q[128], s_k[128], part[4 * kThreads];
+    const int tid = threadIdx.x, n4 = DV / 4, groups = kThreads / n4, c4 = tid % n4, rg = tid / n4;
+    const size_t bh = blockIdx.x;
+    float4* st = reinterpret_cast<float4*>(S + bh * DK * DV);
+    float4 r[kRegs];
+#pragma unroll
+    for (int m = 0; m < kRegs; ++m) {
+        const int i = rg + m * groups;
+        if (i < DK) r[m] = st[static_cast<size_t>(i) * n4 + c4];
+    }
+    if (tid < DK) {
+        s_q[tid] = IO<T>::load(q, bh * DK + tid);
+        s_k[tid] = IO<T>::load(k, bh * DK + tid);
+    }
+    const float a = expf(log_decay[bh % H]);
+    float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = IO<T>::load(v, bh * DV + c4 * 4 + c);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kRegs; ++m) {
+        const int i = rg + m * groups;
+        if (i < DK) {
+            const float ki = s_k[i], qi = s_q[i];
+            float4 z = r[m];
+            z.x = fmaf(a, z.x, ki * x[0]);
+            z.y = fmaf(a, z.y, ki * x[1]);
+            z.z = fmaf(a, z.z, ki * x[2]);
+            z.w = fmaf(a, z.w, ki * x[3]);
+            st[static_cast<size_t>(i) * n4 + c4] = z;
+            y[0] = fmaf(qi, z.x, y[0]);
+            y[1] = fmaf(qi, z.y, y[1]);
+            y[2] = fmaf(qi, z.z, y[2]);
+            y[3] = fmaf(qi, z.w, y[3]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) part[rg * DV + c4 * 4 + c] = y[c];
+    __syncthreads();
+    if (tid < DV) {
+        float sum = 0.f;
+        for (int i = 0; i < min(groups, DK); ++i) sum += part[i * DV + tid];
+        IO<T>::store(o, bh * DV + tid, sum);
+    }
+}
+
+}  // namespace
+
+size_t decay_scratch(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
+    const DecayPlan p = plan_of(n_seq, n_tok, H, dk, dv, io, flags, packed, n_jobs);
+    return p.nseg > 1 ? static_cast<size_t>(n_jobs) * n_seq * H * p.nseg * dk * dv * sizeof(float) : 0;
+}
+
+cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
+    const int dk = a.job[0].dk, dv = a.job[0].dv;
+    const bool tc = use_tc(a.io, dk, dv, a.flags);
+    const DecayPlan plan = plan_of(a.n_seq, a.n_tok, a.H, dk, dv, a.io, a.flags, a.cu != nullptr, a.n_jobs);
+    DecayParams P = {};
+    for (int i = 0; i < a.n_jobs; ++i) P.job[i] = a.job[i];
+    P.log_decay = a.log_decay; P.cu = a.cu; P.status = a.status;
+    P.n_seq = a.n_seq; P.n_tok = a.n_tok; P.H = a.H; P.io = a.io;
+    P.nseg = plan.nseg; P.seg_len = plan.seg_len;
+    P.probe = (a.flags & KDN_FLAG_TIMEOUT_PROBE) ? 1 : 0;
+    P.pass = kWhole;
+    if (plan.nseg <= 1) return start_pass(P, a.n_jobs, tc, s);
+    for (int i = 0; i < a.n_jobs; ++i) P.states[i] = a.scratch + static_cast<size_t>(i) * a.n_seq * a.H * plan.nseg * dk * dv;
+    P.pass = kStates;
+    cudaError_t e = start_pass(P, a.n_jobs, tc, s);
+    if (e != cudaSuccess) return e;
+    decay_chain_kernel<<<dim3((dk * dv + kThreads - 1) / kThreads, a.n_seq * a.H, a.n_jobs), kThreads, 0, s>>>(P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    P.pass = kOutputs;
+    return start_pass(P, a.n_jobs, tc, s);
+}
+
+bool decay_tc_supported(int, int, int) { return false; }
+cudaError_t launch_decay_tc(const DecayParams&, int, cudaStream_t) { return cudaErrorNotSupported; }
+
+cudaError_t launch_decay_step(const DecayStepArgs& a, cudaStream_t s) {
+    if (a.io == KDN_BF16)
+        decay_step_kernel<__nv_bfloat16><<<a.B * a.H, kThreads, 0, s>>>(
+            static_cast<const __nv_bfloat16*>(a.q), static_cast<const __nv_bfloat16*>(a.k), static_cast<const __nv_bfloat16*>(a.v),
+            a.log_decay, a.S, static_cast<__nv_bfloat16*>(a.o), a.H, a.dk, a.dv);
+    else
+        decay_step_kernel<float><<<a.B * a.H, kThreads, 0, s>>>(
+            static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), a.log_decay, a.S,
+            static_cast<float*>(a.o), a.H, a.dk, a.dv);
+    return cudaGetLastError();
+}
+
+}  // namespace kdn

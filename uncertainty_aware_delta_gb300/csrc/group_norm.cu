@@ -1,0 +1,321 @@
+// Norm of every token's groups of d channels (the heads of a memory's outputs), with an activation, and its gradients.
+//
+//   xh = (x - mean) rstd,  n = xh w + b,  y = act(n)  or, with a gate,  y = n act(gate)
+//   dn = dy act'(n)  or  dy act(gate),  dgate = dy n act'(gate),  dw = sum over tokens of dn xh,  db = that of dn,
+//   dx = rstd (dn w - mean(dn w) - xh mean(dn w xh))
+//
+// A group's channels lie in neighbouring lanes, eight a lane, so its sums are a few shuffles and x is read once.  A thread
+// keeps its channels from token to token: weights stay in registers, and the gradients of weights are sums in registers,
+// written once a block and joined by a second kernel in a fixed order.
+
+#include <cuda_bf16.h>
+#include <algorithm>
+#include <math.h>
+
+#include "common.cuh"
+#include "decay.h"
+#include "kdn.h"
+
+namespace kdn {
+namespace {
+
+constexpr int kMost = 256, kV = 8;    // threads of a block; channels of a lane
+constexpr int kSMs = 152;             // GB300
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct NormParams {
+    NormArgs a;
+    int lanes, groups, rows;          // lanes of a group; groups and rows that a block has at a time
+    int parts;                        // backward: rows of partial sums
+};
+
+template <typename T> struct Vec;     // eight channels, as they are in memory
+template <> struct Vec<__nv_bfloat16> {
+    uint4 x;
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&y)[kV]) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __uint_as_float(w[i] << 16);
+            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ static void store(void* p, long long i, const float (&y)[kV]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Vec<float> {
+    float4 x, z;
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        x = s[0];
+        z = s[1];
+    }
+    __device__ __forceinline__ void get(float (&y)[kV]) const {
+        y[0] = x.x; y[1] = x.y; y[2] = x.z; y[3] = x.w;
+        y[4] = z.x; y[5] = z.y; y[6] = z.z; y[7] = z.w;
+    }
+    __device__ __forceinline__ static void store(void* p, long long i, const float (&y)[kV]) {
+        float4* s = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        s[0] = make_float4(y[0], y[1], y[2], y[3]);
+        s[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+
+// The activation of x, and its slope.
+template <int ACT> __device__ __forceinline__ float act(float x, float& slope) {
+    if (ACT == KDN_ACT_NONE) {
+        slope = 1.f;
+        return x;
+    }
+    const float h = sigmoid(x);
+    if (ACT == KDN_ACT_SIGMOID) {
+        slope = h * (1.f - h);
+        return h;
+    }
+    slope = h * fmaf(x, 1.f - h, 1.f);
+    return x * h;
+}
+
+// Sum over the lanes of a group.
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    return x;
+}
+
+// What a thread works on.
+struct Place {
+    int g, c, row, step;   // group, first channel in it, first row, rows to its next one
+    bool mine;             // whether there is such a channel of such a group
+};
+__device__ __forceinline__ Place place_of(const NormParams& P) {
+    Place p;
+    const int at = threadIdx.x / P.lanes, lane = threadIdx.x % P.lanes;
+    p.g = blockIdx.y * P.groups + at % P.groups;
+    p.c = lane * kV;
+    const int sub = at / P.groups;
+    p.row = blockIdx.x * P.rows + sub;
+    p.step = gridDim.x * P.rows;
+    p.mine = sub < P.rows && p.g < P.a.groups && p.c < P.a.d;
+    return p;
+}
+
+template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMost) group_norm_kernel(const __grid_constant__ NormParams P) {
+    const NormArgs& A = P.a;
+    const Place p = place_of(P);
+    float w[kV], b[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        w[i] = A.w && p.mine ? A.w[p.g * A.d + p.c + i] : 1.f;
+        b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
+    }
+    const float inv = 1.f / A.d;
+    // (all lanes of a warp go on together: the sums are shuffles)
+    for (int row = p.row; __any_sync(kAll, row < A.rows); row += p.step) {
+        const bool mine = p.mine && row < A.rows;
+        float x[kV] = {};
+        Vec<T> gate;
+        if (mine) {
+            Vec<T> v;
+            v.load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
+            if (GATE) gate.load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
+            v.get(x);
+        }
+        float sum = 0.f, sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sum += x[i];
+        const float mean = group_sum(sum, P.lanes) * inv;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            x[i] -= mean;
+            sq = fmaf(x[i], x[i], sq);
+        }
+        const float rstd = rsqrtf(group_sum(mine ? sq : 0.f, P.lanes) * inv + A.eps);
+        if (!mine) continue;
+        float z[kV], slope;
+        if (GATE) gate.get(z);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const float n = fmaf(x[i] * rstd, w[i], b[i]);
+            x[i] = GATE ? n * act<ACT>(z[i], slope) : act<ACT>(n, slope);
+        }
+        Vec<T>::store(A.y, (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c, x);
+    }
+}
+
+template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMost) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
+    const NormArgs& A = P.a;
+    const Place p = place_of(P);
+    float w[kV], b[kV], dw[kV] = {}, db[kV] = {};
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        w[i] = A.w && p.mine ? A.w[p.g * A.d + p.c + i] : 1.f;
+        b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
+    }
+    const float inv = 1.f / A.d;
+    for (int row = p.row; __any_sync(kAll, row < A.rows); row += p.step) {
+        const bool mine = p.mine && row < A.rows;
+        float x[kV] = {}, y[kV] = {}, z[kV] = {};
+        if (mine) {
+            Vec<T> v, u, t;
+            v.load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
+            u.load(A.dy.p, row * A.dy.row + p.g * A.dy.head + p.c);
+            if (GATE) t.load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
+            v.get(x);
+            u.get(y);
+            if (GATE) t.get(z);
+        }
+        float sum = 0.f, sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sum += x[i];
+        const float mean = group_sum(sum, P.lanes) * inv;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            x[i] -= mean;
+            sq = fmaf(x[i], x[i], sq);
+        }
+        const float rstd = rsqrtf(group_sum(mine ? sq : 0.f, P.lanes) * inv + A.eps);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const float xh = x[i] * rstd, n = fmaf(xh, w[i], b[i]);
+            float slope, dn;
+            if (GATE) {
+                const float f = act<ACT>(z[i], slope);
+                z[i] = y[i] * n * slope;
+                dn = y[i] * f;
+            } else {
+                act<ACT>(n, slope);
+                dn = y[i] * slope;
+            }
+            if (mine) {
+                dw[i] = fmaf(dn, xh, dw[i]);
+                db[i] += dn;
+            }
+            x[i] = xh;
+            y[i] = dn * w[i];
+            s1 += y[i];
+            s2 = fmaf(y[i], xh, s2);
+        }
+        s1 = group_sum(mine ? s1 : 0.f, P.lanes) * inv;
+        s2 = group_sum(mine ? s2 : 0.f, P.lanes) * inv;
+        if (!mine) continue;
+        const long long at = (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) y[i] = rstd * (y[i] - s1 - x[i] * s2);
+        Vec<T>::store(A.dx, at, y);
+        if (GATE) Vec<T>::store(A.dgate, at, z);
+    }
+    if (!p.mine) return;
+    float* part = A.scratch + static_cast<size_t>(p.row) * A.groups * A.d + p.g * A.d + p.c;
+    if (A.dw) Vec<float>::store(part, 0, dw);
+    if (A.db) Vec<float>::store(part + static_cast<size_t>(P.parts) * A.groups * A.d, 0, db);
+}
+
+// Sums of the parts, a channel a lane: eight warps take every eighth part, and one adds them up.
+__global__ void __launch_bounds__(kMost) group_norm_join_kernel(const __grid_constant__ NormParams P) {
+    __shared__ float sums[8][33];
+    const int n = P.a.groups * P.a.d, lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float* out = blockIdx.y ? P.a.db : P.a.dw;
+    if (!out) return;
+    const float* part = P.a.scratch + static_cast<size_t>(blockIdx.y) * P.parts * n;
+    float sum = 0.f;
+    if (c < n)
+#pragma unroll 4
+        for (int i = warp; i < P.parts; i += 8) sum += part[static_cast<size_t>(i) * n + c];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp || c >= n) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += sums[i][lane];
+    out[c] = sum;
+}
+
+// How the channels lie in a block's threads.
+struct Shape {
+    int lanes, groups, rows, blocks_y, threads;
+};
+Shape shape_of(int groups, int d) {
+    Shape s;
+    for (s.lanes = 1; s.lanes * kV < d; s.lanes *= 2) {}
+    const int most = kMost / s.lanes;
+    s.blocks_y = (groups + most - 1) / most;
+    s.groups = (groups + s.blocks_y - 1) / s.blocks_y;
+    s.rows = most / s.groups;
+    s.threads = (s.rows * s.groups * s.lanes + 31) / 32 * 32;
+    return s;
+}
+int blocks_x(const Shape& s, int rows, int per_sm) {
+    const long long want = (static_cast<long long>(rows) + s.rows - 1) / s.rows, room = std::max(1, per_sm * kSMs / s.blocks_y);
+    return static_cast<int>(std::min(want, room));
+}
+constexpr int kForwardBlocks = 6, kBackwardBlocks = 3;   // an SM
+
+template <typename T, int ACT> cudaError_t forward(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
+    if (P.a.gate.p) group_norm_kernel<T, ACT, true><<<grid, threads, 0, s>>>(P);
+    else group_norm_kernel<T, ACT, false><<<grid, threads, 0, s>>>(P);
+    return cudaGetLastError();
+}
+template <typename T, int ACT> cudaError_t backward(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
+    if (P.a.gate.p) group_norm_backward_kernel<T, ACT, true><<<grid, threads, 0, s>>>(P);
+    else group_norm_backward_kernel<T, ACT, false><<<grid, threads, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+NormParams params_of(const NormArgs& a, const Shape& s) {
+    NormParams P = {};
+    P.a = a;
+    P.lanes = s.lanes; P.groups = s.groups; P.rows = s.rows;
+    return P;
+}
+
+}  // namespace
+
+size_t norm_scratch(int rows, int groups, int d) {
+    if (rows <= 0 || groups <= 0) return 0;
+    const Shape s = shape_of(groups, d);
+    return 2 * sizeof(float) * static_cast<size_t>(blocks_x(s, rows, kBackwardBlocks)) * s.rows * groups * d;
+}
+
+cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t s) {
+    const Shape sh = shape_of(a.groups, a.d);
+    const NormParams P = params_of(a, sh);
+    const dim3 grid(blocks_x(sh, a.rows, kForwardBlocks), sh.blocks_y);
+    const auto run = [&](auto type) {
+        using T = decltype(type);
+        if (a.act == KDN_ACT_NONE) return forward<T, KDN_ACT_NONE>(P, grid, sh.threads, s);
+        if (a.act == KDN_ACT_SILU) return forward<T, KDN_ACT_SILU>(P, grid, sh.threads, s);
+        return forward<T, KDN_ACT_SIGMOID>(P, grid, sh.threads, s);
+    };
+    return a.io == KDN_BF16 ? run(__nv_bfloat16()) : run(float());
+}
+
+cudaError_t launch_group_norm_backward(const NormArgs& a, cudaStream_t s) {
+    const Shape sh = shape_of(a.groups, a.d);
+    NormParams P = params_of(a, sh);
+    const dim3 grid(blocks_x(sh, a.rows, kBackwardBlocks), sh.blocks_y);
+    P.parts = grid.x * sh.rows;
+    const auto run = [&](auto type) {
+        using T = decltype(type);
+        if (a.act == KDN_ACT_NONE) return backward<T, KDN_ACT_NONE>(P, grid, sh.threads, s);
+        if (a.act == KDN_ACT_SILU) return backward<T, KDN_ACT_SILU>(P, grid, sh.threads, s);
+        return backward<T, KDN_ACT_SIGMOID>(P, grid, sh.threads, s);
+    };
+    const cudaError_t e = a.io == KDN_BF16 ? run(__nv_bfloat16()) : run(float());
+    if (e != cudaSuccess || (!a.dw && !a.db)) return e;
+    group_norm_join_kernel<<<dim3((a.groups * a.d + 31) / 32, 2), kMost, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace kdn
