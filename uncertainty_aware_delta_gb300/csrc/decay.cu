@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "decay.h"
+#include "decay_common.cuh"
 #include "kdn.h"
 #include "mma_tf32x3.cuh"
 
@@ -26,31 +27,6 @@ namespace {
 constexpr int kC = 32, kThreads = 256;   // tokens of a chunk; threads of a block
 constexpr int kSMs = 152;                // GB300
 constexpr uint32_t kAll = 0xffffffffu;
-
-// exp(l n) for a whole n >= 0: 1 for n = 0 whatever l is.
-__device__ __forceinline__ float power(float l, int n) { return n == 0 ? 1.f : expf(l * static_cast<float>(n)); }
-
-// exp(l n) as a sum of two fp32 numbers: the states of thousands of chunks are multiplied by it one after another, and the
-// rounding of one number close to 1 would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).
-__device__ __forceinline__ float2 power2(float l, int n) {
-    const float e = n == 0 ? 0.f : expm1f(l * static_cast<float>(n)), hi = 1.f + e, lo = e - (hi - 1.f);
-    return make_float2(hi, fabsf(lo) < INFINITY ? lo : 0.f);
-}
-
-// Tokens of sequence b: first row and length; false where its bounds run backwards or outside.
-__device__ __forceinline__ bool sequence(const DecayParams& P, int b, int& row, int& len) {
-    if (!P.cu) {
-        len = P.n_tok / P.n_seq;
-        row = b * len;
-        return true;
-    }
-    const int x = P.cu[b], y = P.cu[b + 1];
-    row = x;
-    len = y - x;
-    if (x >= 0 && y >= x && y <= P.n_tok) return true;
-    row = len = 0;
-    return false;
-}
 
 __device__ __forceinline__ float4 load4(const void* p, long long i, int io) {
     if (io == KDN_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
@@ -451,7 +427,7 @@ size_t decay_scratch(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     const int dk = a.job[0].dk, dv = a.job[0].dv;
-    const bool tc = use_tc(a.io, dk, dv, a.flags);
+    const bool tc = use_tc(a.io, dk, dv, a.flags) && a.n_tok > 0;
     const DecayPlan plan = plan_of(a.n_seq, a.n_tok, a.H, dk, dv, a.io, a.flags, a.cu != nullptr, a.n_jobs);
     DecayParams P = {};
     for (int i = 0; i < a.n_jobs; ++i) P.job[i] = a.job[i];
@@ -471,9 +447,6 @@ cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     P.pass = kOutputs;
     return start_pass(P, a.n_jobs, tc, s);
 }
-
-bool decay_tc_supported(int, int, int) { return false; }
-cudaError_t launch_decay_tc(const DecayParams&, int, cudaStream_t) { return cudaErrorNotSupported; }
 
 cudaError_t launch_decay_step(const DecayStepArgs& a, cudaStream_t s) {
     if (a.io == KDN_BF16)

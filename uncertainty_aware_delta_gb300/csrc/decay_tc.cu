@@ -1,0 +1,632 @@
+// Linear attention with a decay for each head on tcgen05 tensor cores: bf16, dk and dv 64 or 128.
+//
+// One block walks a head of a sequence (or of a segment of it) in chunks of 64 tokens (the chunk form: decay.cu).  All
+// products have the value channels in their rows (TMEM lanes), so that the state lies in the registers of one warpgroup, a
+// value channel a thread, and goes back into the products through TMEM:
+//   W  = Q K^T              (rows: 64 of K, not used, and 64 of Q; an MMA of 64 rows takes as long)
+//   P  = W g^(i-j)          bf16, shared memory
+//   U^T = V'^T K            V'_j = g^(m-1-j) v_j in bf16 parts, written to TMEM by a warpgroup that reads V transposed
+//   S   = g^m S + U         fp32, registers;  bf16 S^T to TMEM
+//   O^T = V^T P^T + (S^T Q^T) g^(i+1)
+// V' has three parts (24 bits) where the final state is wanted and two (16) where only outputs in bf16 are: one part
+// would add as much to the error of o as its own rounding does.  S^T goes in as bf16, P too.
+//
+// U depends on no state, so a chunk's products run while the last chunk's state is still on its way: the walk's only serial
+// step is S = g^m S + U, a fused multiply-add an element.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <mutex>
+
+#include "common.cuh"
+#include "decay.h"
+#include "decay_common.cuh"
+#include "kdn.h"
+#include "sm100.cuh"
+
+namespace kdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kC = 64;                        // tokens of a chunk
+constexpr int kThreads = 512;                 // loader, products, two weight warps; state, V' and output warpgroups
+constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 136, kOutputRegs = 96;   // 4 x 128 in all, as launched
+constexpr int kStages = 3;
+constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr uint32_t kHalf = 8192;              // 64 tokens of 64 channels
+constexpr int kMarks = 4;                     // chunks whose marks of values that are not finite are kept
+
+struct TcParams {
+    CUtensorMap q[kMaxDecayJobs], k[kMaxDecayJobs], v[kMaxDecayJobs], o[kMaxDecayJobs];
+    DecayParams d;
+};
+
+template <int DK, int DV> struct Layout {
+    static constexpr int kKHalves = DK / 64, kVHalves = DV / 64;
+    // a stage: halves of K and Q in turn (128 rows of a product), then halves of V
+    static constexpr uint32_t kV = kKHalves * 2 * kHalf, kStage = kV + kVHalves * kHalf;
+    static constexpr uint32_t kP = kStages * kStage, kO = kP + 2 * kHalf;   // weights of two chunks; outputs: 4 KB a warp, twice
+    // (products read 128 value channels: with 64, the second half is what lies behind, and its rows are not used)
+    static constexpr uint32_t kSmem = kO + 2 * 4 * 4096 + 1024;
+};
+
+// TMEM columns: W; O within the chunk and from the state; U; parts of V'; S^T
+constexpr uint32_t kTmW = 0, kTmI = 64, kTmX = 128, kTmU = 192, kTmV = 320, kTmS = 416, kTmCols = 512;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0), "r"(c1),
+                 "r"(c2), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// The warp that issues products runs as a whole, so that descriptors stay in uniform registers; one lane's predicate issues.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead));
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead));
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {   // after tmem_wait_ld(): ties the registers to that point
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));
+    return x;
+}
+
+// OUT: outputs, else the state alone.  PARTS: of V'.
+template <int DK, int DV, bool OUT, int PARTS>
+__global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcParams T) {
+    using L = Layout<DK, DV>;
+    const DecayParams& P = T.d;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * kStages + 11];
+    __shared__ float pw[kC + 1];
+    __shared__ __align__(16) float vf[2][kC], rf[2][kC];   // factors of the chunk's tokens in V' and in outputs: whole chunk, last one
+    __shared__ int marks[kMarks][128];                     // per value channel, the walk's first token that is not finite
+    __shared__ volatile int aborted;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages, bar_w = bar_empty + 8 * kStages, bar_p = bar_w + 8,
+                   bar_v = bar_p + 8, bar_u = bar_v + 8, bar_u_free = bar_u + 8, bar_s = bar_u_free + 8, bar_s_free = bar_s + 8,
+                   bar_o = bar_s_free + 8, bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int job = blockIdx.z, bh = blockIdx.x, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
+    const DecayJob& J = P.job[job];
+    const bool rev = J.reverse != 0;
+
+    int row0, len;
+    if (!sequence(P, b, row0, len) && tid == 0 && h == 0) set_status(P.status, kStatusRange);
+    constexpr size_t elems = static_cast<size_t>(DK) * DV;
+    if (P.pass != kWhole) {
+        if (static_cast<long long>(seg) * P.seg_len >= len) return;
+        row0 += seg * P.seg_len;
+        len = min(len - seg * P.seg_len, P.seg_len);
+    }
+    const float* in = nullptr;
+    float* end = nullptr;
+    int s_k = J.s_k, s_v = J.s_v;
+    if (P.pass == kWhole) {
+        in = J.S0 ? J.S0 + bh * elems : nullptr;
+        end = J.S_T ? J.S_T + bh * elems : nullptr;
+    } else {
+        float* st = P.states[job] + (static_cast<size_t>(bh) * P.nseg + seg) * elems;
+        s_k = DV;
+        s_v = 1;
+        if (P.pass == kStates) end = st;
+        else in = st;
+    }
+    if (len == 0) {
+        if (end)
+            for (int i = tid; i < static_cast<int>(elems); i += kThreads) end[i] = in ? in[i] : 0.f;   // (the same layout)
+        return;
+    }
+    const int chunks = (len + kC - 1) / kC, m_last = len - (chunks - 1) * kC;   // tokens of the chunk that may be short
+    const float l = P.log_decay[h];
+    // chunk n of the walk: its place among the chunks, and whether it is the short one
+    auto place = [&](int n) { return rev ? chunks - 1 - n : n; };
+    auto is_last = [&](int n) { return place(n) == chunks - 1; };
+
+    if (tid == 0) {
+        aborted = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        mbar_init(bar_w, 1);
+        mbar_init(bar_p, 2);
+        mbar_init(bar_v, 4);
+        mbar_init(bar_u, 1);
+        mbar_init(bar_u_free, 4);
+        mbar_init(bar_s, 4);
+        mbar_init(bar_s_free, 1);
+        mbar_init(bar_o, 1);
+        mbar_init(bar_o_free, 4);
+        mbar_init(bar_drain, 1);
+        mbar_init(bar_probe, 1);   // completed by nothing
+        mbar_fence_init();
+    }
+    if (tid <= kC) pw[tid] = power(l, tid);
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&tmem_slot), kTmCols);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid < 2 * kC) {
+        const int last = tid / kC, i = tid % kC, m = last ? m_last : kC, left = m - 1 - i;
+        vf[last][i] = left < 0 ? 0.f : pw[rev ? i + 1 : left];
+        rf[last][i] = left < 0 ? 0.f : pw[rev ? left : i + 1];
+    }
+    tc_fence_after();
+    __syncthreads();
+    const uint32_t tmem = tmem_slot;
+
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (mbar_test(bar, parity)) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kWaitLimit; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (aborted) return false;
+        }
+        aborted = 1;
+        set_status(P.status, kStatusTimeout);
+        return false;
+    };
+    auto await = [&](uint32_t bar, uint32_t parity) { return __all_sync(kAll, wait(bar, parity)); };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        if (warp == 0) {
+            if (lane == 0) {
+                // ---- loader
+                int n = 0;
+#pragma unroll 1
+                for (; n < chunks; ++n) {
+                    const int slot = n % kStages;
+                    if (n >= kStages && !wait(bar_empty + 8 * slot, (n / kStages - 1) & 1)) break;
+                    const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
+                    const int t = row0 + place(n) * kC;
+                    mbar_expect_tx(full, OUT ? L::kStage : L::kKHalves * kHalf + L::kVHalves * kHalf);
+                    for (int f = 0; f < L::kKHalves; ++f) {
+                        tma_load_3d(st + 2 * f * kHalf, &T.k[job], 64 * f, h, t, full);
+                        if (OUT) tma_load_3d(st + (2 * f + 1) * kHalf, &T.q[job], 64 * f, h, t, full);
+                    }
+                    for (int f = 0; f < L::kVHalves; ++f) tma_load_3d(st + L::kV + f * kHalf, &T.v[job], 64 * f, h, t, full);
+                    if (P.probe && n == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
+                        aborted = 1;
+                        set_status(P.status, kStatusTimeout);
+                    }
+                    if (aborted) {
+                        ++n;
+                        break;
+                    }
+                }
+                // copies already issued land before the block's shared memory goes away
+                if (aborted)
+                    for (int i = max(n - kStages, 0); i < n; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
+            }
+        } else if (warp == 1) {
+            // ---- products
+            constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 0, 0), id_u = idesc_bf16(128, DK, 0, 1, 0), id_i = idesc_bf16(128, 64, 1, 0, 0);
+            const uint32_t lead = elect_one();
+            auto one = [](uint32_t x) { return __shfl_sync(kAll, x, 0); };
+            const uint32_t base = one(sb), tm = one(tmem);
+            const uint64_t kq = sw128_desc(base, 16, 1024), kt = sw128_desc(base, 2 * kHalf, 1024), vt = sw128_desc(base + L::kV, kHalf, 1024),
+                           pd = sw128_desc(base + L::kP, 16, 1024);
+            auto weights = [&](uint32_t at) {
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k) {
+                    const uint64_t x = desc_add(kq, at + (k / 4) * 2 * kHalf + (k % 4) * 32);
+                    mma_ss(lead, tm + kTmW, x, x, id_w, k > 0);
+                }
+                commit(lead, bar_w);
+            };
+            uint32_t slot = 0, phase = 0;
+            bool ok = await(bar_full, 0);
+            tc_fence_after();
+            if (ok && OUT) weights(0);
+#pragma unroll 1
+            for (int n = 0; ok && n < chunks; ++n) {
+                const uint32_t at = slot * L::kStage, par = n & 1;
+                if (!(ok = await(bar_v, par))) break;
+                if (n > 0 && !(ok = await(bar_u_free, par ^ 1))) break;
+                tc_fence_after();
+                // (the small parts first: the sums' last bits are cut off)
+#pragma unroll
+                for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ts(lead, tm + kTmU, tm + kTmV + 32 * p + 8 * k, desc_add(kt, at + k * 2048), id_u, p < PARTS - 1 || k > 0);
+                commit(lead, bar_u);
+                if (!OUT) commit(lead, bar_empty + 8 * slot);
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (OUT) {
+                    if (!(ok = await(bar_p, par))) break;
+                    if (n + 1 < chunks) {
+                        if (!(ok = await(bar_full + 8 * slot, phase))) break;
+                        tc_fence_after();
+                        weights(slot * L::kStage);
+                    }
+                    if (!(ok = await(bar_s, par))) break;
+                    if (n > 0 && !(ok = await(bar_o_free, par ^ 1))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_ts(lead, tm + kTmX, tm + kTmS + 8 * k, desc_add(kq, at + kHalf + (k / 4) * 2 * kHalf + (k % 4) * 32), id_w, k > 0);
+                    commit(lead, bar_s_free);
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ss(lead, tm + kTmI, desc_add(vt, at + k * 2048), desc_add(pd, par * kHalf + k * 32), id_i, k > 0);
+                    commit(lead, bar_o);
+                    commit(lead, bar_empty + 8 * (at / L::kStage));
+                }
+            }
+            // products already issued end before TMEM goes away
+            commit(lead, bar_drain);
+            mbar_wait(bar_drain, 0, kWaitLimit);
+        } else if (OUT) {
+            // ---- weights: row i of the chunk a thread (TMEM lanes 64 + i)
+            const int i = (warp - 2) * 32 + lane;
+            const uint32_t tw = tmem + kTmW + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+            for (int n = 0; n < chunks; ++n) {
+                if (!await(bar_w, n & 1)) break;
+                tc_fence_after();
+                const int m = is_last(n) ? m_last : kC;
+                const uint32_t to = sb + L::kP + (n & 1) * kHalf;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(tw + 32 * c, x);
+                    tmem_wait_ld();
+                    loaded(x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int at = 32 * c + j, gap = rev ? at - i : i - at;
+                        const bool keep = gap >= 0 && at < m;
+                        x[j] = __float_as_uint(keep ? __uint_as_float(x[j]) * pw[keep ? gap : 0] : 0.f);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + sw128_off(i, 4 * c + j)), "r"(y[0]), "r"(y[1]),
+                                     "r"(y[2]), "r"(y[3])
+                                     : "memory");
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_p);
+            }
+        }
+    } else if (warp < 8) {
+        // ---- state: value channel j a thread, all key channels in its registers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
+        const int j = tid - 128;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, tu = tmem + kTmU + lanes, ts = tmem + kTmS + lanes;
+        const bool mine = j < DV;
+        float S[DK];
+        if (in && mine) {
+            const float* p = in + static_cast<size_t>(j) * s_v;
+            if (s_k == 1) {
+#pragma unroll
+                for (int i = 0; i < DK; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(p + i);
+                    S[i] = x.x; S[i + 1] = x.y; S[i + 2] = x.z; S[i + 3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < DK; ++i) S[i] = p[static_cast<size_t>(i) * s_k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < DK; ++i) S[i] = 0.f;
+        }
+        auto give = [&]() {   // S^T as the next products' operand
+#pragma unroll
+            for (int c = 0; c < DK; c += 64) {
+                uint32_t x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = pack_bf16(S[c + 2 * i], S[c + 2 * i + 1]);
+                tmem_st32(ts + c / 2, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_s);
+        };
+        if (OUT) give();
+        const float2 f_full = power2(l, kC), f_last = power2(l, m_last);
+#pragma unroll 1
+        for (int n = 0; n < chunks; ++n) {
+            if (!await(bar_u, n & 1)) break;
+            tc_fence_after();
+            const float2 f = is_last(n) ? f_last : f_full;
+#pragma unroll
+            for (int c = 0; c < DK; c += 32) {
+                uint32_t x[32];
+                tmem_ld32(tu + c, x);
+                tmem_wait_ld();
+                loaded(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[c + i] = fmaf(f.x, S[c + i], fmaf(f.y, S[c + i], __uint_as_float(x[i])));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_u_free);
+            if (OUT && n + 1 < chunks) {
+                if (!await(bar_s_free, n & 1)) break;
+                tc_fence_after();
+                give();
+            }
+        }
+        if (end && mine && !aborted)
+#pragma unroll
+            for (int i = 0; i < DK; ++i) end[static_cast<size_t>(i) * s_k + static_cast<size_t>(j) * s_v] = S[i];
+    } else if (warp < 12) {
+        // ---- V': value channel j a thread, its tokens two a column
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kValueRegs));
+        const int j = tid - 256;
+        const uint32_t tv = tmem + kTmV + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t slot = 0, phase = 0;
+#pragma unroll 1
+        for (int n = 0; n < chunks; ++n) {
+            if (!await(bar_full + 8 * slot, phase)) break;
+            const bool last = is_last(n);
+            const int m = last ? m_last : kC;
+            const uint32_t st = sb + slot * L::kStage, mine = st + L::kV + (j / 64) * kHalf + (j % 8) * 2;
+            const uint32_t chunk = (j % 64) / 8;
+            const float* f = vf[last];
+            uint32_t part[3][32];
+            float odd = 0.f;   // NaN where a value is not finite
+            if (j < DV) {
+#pragma unroll
+                for (int t = 0; t < kC; t += 2) {
+                    float x0 = __uint_as_float(lds16(mine + t * 128 + ((chunk ^ (t & 7)) << 4)) << 16),
+                          x1 = __uint_as_float(lds16(mine + (t + 1) * 128 + ((chunk ^ ((t + 1) & 7)) << 4)) << 16);
+                    if (last) {
+                        x0 = t < m ? x0 : 0.f;
+                        x1 = t + 1 < m ? x1 : 0.f;
+                    }
+                    odd = fmaf(x0, 0.f, fmaf(x1, 0.f, odd));
+                    x0 *= f[t];
+                    x1 *= f[t + 1];
+                    part[0][t / 2] = pack_bf16(x0, x1);
+                    x0 -= bf_lo(part[0][t / 2]);
+                    x1 -= bf_hi(part[0][t / 2]);
+                    part[1][t / 2] = pack_bf16(x0, x1);
+                    if (PARTS == 3) {
+                        x0 -= bf_lo(part[1][t / 2]);
+                        x1 -= bf_hi(part[1][t / 2]);
+                        part[2][t / 2] = pack_bf16(x0, x1);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) part[0][t] = part[1][t] = part[2][t] = 0;
+            }
+            if (n > 0 && !await(bar_u, (n - 1) & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) tmem_st32(tv + 32 * p, part[p]);
+            if (OUT) {
+                // Values that are not finite are taken out of the product with the weights (a weight of zero would not stop
+                // them); the walk's rows from the first of them on get it back.
+                int mark = kC;
+                if (__any_sync(kAll, odd != 0.f)) {
+                    if (odd != 0.f)
+#pragma unroll 1
+                        for (int i = m - 1; i >= 0; --i) {
+                            const int t = rev ? m - 1 - i : i;
+                            const uint32_t a = mine + t * 128 + ((chunk ^ (t & 7)) << 4);
+                            if ((lds16(a) & 0x7f80u) == 0x7f80u) {
+                                mark = i;
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
+                            }
+                        }
+                    fence_proxy_async();
+                }
+                marks[n % kMarks][tid - 256] = mark;
+            }
+            if (m < kC) {   // rows of other sequences
+                constexpr int kRows = (L::kKHalves + L::kVHalves) * 8;   // pieces of a token
+                for (int i = j; i < (kC - m) * kRows; i += 128) {
+                    const int t = m + i / kRows, c = i % kRows / 8;
+                    const uint32_t a = st + (c < L::kKHalves ? 2 * c * kHalf : L::kV + (c - L::kKHalves) * kHalf) + t * 128 + (i % 8) * 16;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0) : "memory");
+                }
+                fence_proxy_async();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_v);
+            if (++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    } else {
+        // ---- outputs: value channel j a thread; a warp's 32 channels of the chunk are put in token order and stored
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
+        const int j = tid - 384;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, ti = tmem + kTmI + lanes, tx = tmem + kTmX + lanes;
+        if (OUT) {
+#pragma unroll 1
+            for (int n = 0; n < chunks; ++n) {
+                const bool last = is_last(n);
+                const int m = last ? m_last : kC;
+                const uint32_t out = sb + L::kO + ((n & 1) * 4 + (warp & 3)) * 4096;
+                if (lane == 0) bulk_wait_read1();   // the store of two chunks ago has read its place
+                __syncwarp();
+                if (!await(bar_o, n & 1)) break;
+                tc_fence_after();
+                const int mark = marks[n % kMarks][j];
+                const float* f = rf[last];
+#pragma unroll
+                for (int c = 0; c < kC; c += 32) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32(ti + c, x);
+                    tmem_ld32(tx + c, y);
+                    tmem_wait_ld();
+                    loaded(x);
+                    loaded(y);
+                    if (c + 32 == kC) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_o_free);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(f[c + i], __uint_as_float(y[i]), __uint_as_float(x[i])));
+                    if (__any_sync(kAll, mark < kC))
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if ((rev ? m - 1 - (c + i) : c + i) >= mark) x[i] = 0x7fc00000u;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const uint32_t z = pack_bf16(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + (c + i) * 64 + lane * 2), "h"(static_cast<uint16_t>(z)) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + (c + i + 1) * 64 + lane * 2), "h"(static_cast<uint16_t>(z >> 16))
+                                     : "memory");
+                    }
+                }
+                const int t = row0 + place(n) * kC;
+                if (j - lane >= DV) continue;   // (the warps behind the value channels)
+                if (m == kC) {
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&T.o[job], out, j, h, t);
+                        bulk_commit();
+                    }
+                } else {   // the rows behind are another sequence's
+                    __syncwarp();
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(J.o) + (static_cast<long long>(t) * P.H + h) * DV + (j - lane);
+                    for (int i = lane / 4; i < m; i += 8) {
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(out + i * 64 + lane % 4 * 16));
+                        *reinterpret_cast<uint4*>(o + static_cast<long long>(i) * P.H * DV + lane % 4 * 8) = x;
+                    }
+                    __syncwarp();
+                    if (lane == 0) bulk_commit();   // (an empty group: the count of groups goes on)
+                }
+            }
+            if (lane == 0) bulk_wait_all();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmCols);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// [rows, heads, d] bf16, tiles of 64 rows and `channels` of one head.
+bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d, int channels, CUtensorMapSwizzle swizzle) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.head) * 2, static_cast<cuuint64_t>(x.row) * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(channels), 1, kC}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, bool OUT, int PARTS> cudaError_t start(const TcParams& T, int n_jobs, cudaStream_t s) {
+    constexpr int bytes = Layout<DK, DV>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<DK, DV, OUT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(T.d.n_seq * T.d.H, T.d.pass == kWhole ? 1 : T.d.nseg, n_jobs);
+    decay_tc_kernel<DK, DV, OUT, PARTS><<<grid, kThreads, bytes, s>>>(T);
+    return cudaGetLastError();
+}
+
+template <int DK, int DV> cudaError_t start_pass(const TcParams& T, int n_jobs, cudaStream_t s) {
+    if (T.d.pass == kStates) return start<DK, DV, false, 3>(T, n_jobs, s);
+    if (T.d.pass == kOutputs) return start<DK, DV, true, 2>(T, n_jobs, s);
+    return start<DK, DV, true, 3>(T, n_jobs, s);
+}
+
+}  // namespace
+
+bool decay_tc_supported(int io, int dk, int dv) { return io == KDN_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
+
+cudaError_t launch_decay_tc(const DecayParams& P, int n_jobs, cudaStream_t s) {
+    TcParams T;
+    T.d = P;
+    const int dk = P.job[0].dk, dv = P.job[0].dv;
+    for (int i = 0; i < n_jobs; ++i) {
+        const DecayJob& j = P.job[i];
+        const Strided o = {j.o, static_cast<long long>(P.H) * dv, dv};
+        if (!encode(&T.q[i], j.q, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode(&T.k[i], j.k, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode(&T.v[i], j.v, P.n_tok, P.H, dv, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode(&T.o[i], o, P.n_tok, P.H, dv, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    }
+    if (dk == 128) return dv == 128 ? start_pass<128, 128>(T, n_jobs, s) : start_pass<128, 64>(T, n_jobs, s);
+    return dv == 128 ? start_pass<64, 128>(T, n_jobs, s) : start_pass<64, 64>(T, n_jobs, s);
+}
+
+}  // namespace kdn
