@@ -102,8 +102,52 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {   // after tmem_wait
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
-__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// Fragments of 16 lanes: 32-bit column t % 4 of lanes t / 4 and t / 4 + 8 (and again four columns on, eight times in all) ...
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+// ... and columns 2 (t % 4), + 1 of lane t / 4, then those of lane t / 4 + 8 (and again eight columns on, eight times in all).
+__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16 bits, transposed: a lane's address is a row's (matrix lane / 8, row lane % 8).
+__device__ __forceinline__ void ldmatrix_t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void stmatrix_t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+// two fp32 operations an instruction
+typedef unsigned long long pair_t;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<pair_t&>(d))
+        : "l"(reinterpret_cast<pair_t&>(a)), "l"(reinterpret_cast<pair_t&>(b)), "l"(reinterpret_cast<pair_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<pair_t&>(d)) : "l"(reinterpret_cast<pair_t&>(a)), "l"(reinterpret_cast<pair_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
+__device__ __forceinline__ float2 less2(float2 a, uint32_t b) {   // a - b
+    const float2 y = unpack2(b);
+    return fma2(y, make_float2(-1.f, -1.f), a);
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t x;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));
@@ -119,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     __shared__ uint64_t bars[2 * kStages + 11];
     __shared__ float pw[kC + 1];
     __shared__ __align__(16) float vf[2][kC], rf[2][kC];   // factors of the chunk's tokens in V' and in outputs: whole chunk, last one
+    __shared__ __align__(16) float fars[32];               // powers of the columns of a block that the diagonal does not cut
     __shared__ int marks[kMarks][128];                     // per value channel, the walk's first token that is not finite
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
@@ -193,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         vf[last][i] = left < 0 ? 0.f : pw[rev ? i + 1 : left];
         rf[last][i] = left < 0 ? 0.f : pw[rev ? left : i + 1];
     }
+    if (tid < 32) fars[tid] = pw[rev ? tid + 1 : 31 - tid];
     tc_fence_after();
     __syncthreads();
     const uint32_t tmem = tmem_slot;
@@ -304,36 +350,64 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             commit(lead, bar_drain);
             mbar_wait(bar_drain, 0, kWaitLimit);
         } else if (OUT) {
-            // ---- weights: row i of the chunk a thread (TMEM lanes 64 + i)
-            const int i = (warp - 2) * 32 + lane;
+            // ---- weights: row i of the chunk a thread (TMEM lanes 64 + i).  Of the two blocks of 32 columns one is cut by the
+            // diagonal, with the same powers in every chunk, and one is seen whole or not at all.
+            const int low = warp - 2, i = lane;   // rows 32 low + i
+            const bool whole = rev ? low == 0 : low == 1;
             const uint32_t tw = tmem + kTmW + (static_cast<uint32_t>(warp * 32) << 16);
+            float near[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) near[j] = pw[abs(i - j)];
+            const float far = pw[rev ? 31 - i : i + 1];
+            const uint32_t far_at = smem_addr(fars);
+            const uint32_t cut = rev ? ~((1u << i) - 1u) : (2u << i) - 1u;   // columns of the block that the row sees
+            auto to = [&](int n, int c, int j) { return sb + L::kP + (n & 1) * kHalf + sw128_off(32 * low + i, 4 * c + j); };
+            auto put = [&](uint32_t a, const uint32_t* x) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+            };
+            if (!whole)
+                for (int n = 0; n < 2; ++n)
+                    for (int j = 0; j < 4; ++j)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to(n, low ^ 1, j)), "r"(0) : "memory");
 #pragma unroll 1
             for (int n = 0; n < chunks; ++n) {
                 if (!await(bar_w, n & 1)) break;
                 tc_fence_after();
-                const int m = is_last(n) ? m_last : kC;
-                const uint32_t to = sb + L::kP + (n & 1) * kHalf;
+                // (a short chunk's last columns are masked by the diagonal in a forward walk)
+                const int m = rev && is_last(n) ? m_last : kC;
+                uint32_t x[32];
+                tmem_ld32(tw + 32 * low, x);
+                tmem_wait_ld();
+                loaded(x);
+                uint32_t seen = cut;
+                if (m - 32 * low < 32) seen &= m > 32 * low ? (1u << (m - 32 * low)) - 1u : 0u;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t x[32];
+                for (int j = 0; j < 32; ++j) x[j] = seen >> j & 1u ? __float_as_uint(__uint_as_float(x[j]) * near[j]) : 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) put(to(n, low, j), x + 8 * j);
+                if (whole) {
+                    const int c = low ^ 1;
                     tmem_ld32(tw + 32 * c, x);
                     tmem_wait_ld();
                     loaded(x);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int at = 32 * c + j, gap = rev ? at - i : i - at;
-                        const bool keep = gap >= 0 && at < m;
-                        x[j] = __float_as_uint(keep ? __uint_as_float(x[j]) * pw[keep ? gap : 0] : 0.f);
+                    for (int j = 0; j < 32; j += 4) {
+                        float f[4];   // (read again in every chunk: there are no registers for them)
+                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                                     : "r"(far_at + 4 * j));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[j + e] = __float_as_uint(__uint_as_float(x[j + e]) * far * f[e]);
+                    }
+                    if (m < kC) {
+                        seen = m > 32 ? (1u << (m - 32)) - 1u : 0u;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = seen >> j & 1u ? x[j] : 0u;
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[8 * j + 2 * e]), __uint_as_float(x[8 * j + 2 * e + 1]));
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + sw128_off(i, 4 * c + j)), "r"(y[0]), "r"(y[1]),
-                                     "r"(y[2]), "r"(y[3])
-                                     : "memory");
-                    }
+                    for (int j = 0; j < 4; ++j) put(to(n, c, j), x + 8 * j);
                 }
                 tc_fence_before();
                 fence_proxy_async();
@@ -383,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         for (int n = 0; n < chunks; ++n) {
             if (!await(bar_u, n & 1)) break;
             tc_fence_after();
-            const float2 f = is_last(n) ? f_last : f_full;
+            const float2 f = is_last(n) ? f_last : f_full, fx = make_float2(f.x, f.x), fy = make_float2(f.y, f.y);
 #pragma unroll
             for (int c = 0; c < DK; c += 32) {
                 uint32_t x[32];
@@ -391,7 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tmem_wait_ld();
                 loaded(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[c + i] = fmaf(f.x, S[c + i], fmaf(f.y, S[c + i], __uint_as_float(x[i])));
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 y = make_float2(S[c + i], S[c + i + 1]),
+                                 z = fma2(fx, y, fma2(fy, y, make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]))));
+                    S[c + i] = z.x;
+                    S[c + i + 1] = z.y;
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -406,61 +485,58 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < DK; ++i) end[static_cast<size_t>(i) * s_k + static_cast<size_t>(j) * s_v] = S[i];
     } else if (warp < 12) {
-        // ---- V': value channel j a thread, its tokens two a column
+        // ---- V': 32 value channels a warp, transposed on the way from shared memory to fragments: a thread has tokens
+        // 8 t + 2 (lane % 4), + 1 of channels lane / 4 + 0, 8, 16, 24
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kValueRegs));
-        const int j = tid - 256;
+        const int j = tid - 256;   // the channel whose marks the thread keeps
         const uint32_t tv = tmem + kTmV + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t rows = L::kV + (j / 64) * kHalf + (lane & 7) * 128 + (((j % 64 / 32 * 4 + lane / 8) ^ (lane & 7)) << 4);
         uint32_t slot = 0, phase = 0;
 #pragma unroll 1
         for (int n = 0; n < chunks; ++n) {
             if (!await(bar_full + 8 * slot, phase)) break;
             const bool last = is_last(n);
             const int m = last ? m_last : kC;
-            const uint32_t st = sb + slot * L::kStage, mine = st + L::kV + (j / 64) * kHalf + (j % 8) * 2;
-            const uint32_t chunk = (j % 64) / 8;
-            const float* f = vf[last];
-            uint32_t part[3][32];
-            float odd = 0.f;   // NaN where a value is not finite
-            if (j < DV) {
+            const uint32_t st = sb + slot * L::kStage;
+            uint32_t part[PARTS][2][16];   // of lanes 0 .. 15 and 16 .. 31
+            float2 odd = make_float2(0.f, 0.f);   // NaN where a value is not finite
 #pragma unroll
-                for (int t = 0; t < kC; t += 2) {
-                    float x0 = __uint_as_float(lds16(mine + t * 128 + ((chunk ^ (t & 7)) << 4)) << 16),
-                          x1 = __uint_as_float(lds16(mine + (t + 1) * 128 + ((chunk ^ ((t + 1) & 7)) << 4)) << 16);
-                    if (last) {
-                        x0 = t < m ? x0 : 0.f;
-                        x1 = t + 1 < m ? x1 : 0.f;
-                    }
-                    odd = fmaf(x0, 0.f, fmaf(x1, 0.f, odd));
-                    x0 *= f[t];
-                    x1 *= f[t + 1];
-                    part[0][t / 2] = pack_bf16(x0, x1);
-                    x0 -= bf_lo(part[0][t / 2]);
-                    x1 -= bf_hi(part[0][t / 2]);
-                    part[1][t / 2] = pack_bf16(x0, x1);
-                    if (PARTS == 3) {
-                        x0 -= bf_lo(part[1][t / 2]);
-                        x1 -= bf_hi(part[1][t / 2]);
-                        part[2][t / 2] = pack_bf16(x0, x1);
+            for (int t = 0; t < 8; ++t) {
+                uint32_t r[4] = {0, 0, 0, 0};
+                if (j - lane < DV) ldmatrix_t(st + rows + t * 1024, r);
+                const int at = 8 * t + 2 * (lane % 4);
+                const float2 f = *reinterpret_cast<const float2*>(&vf[last][at]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (last) r[c] &= at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
+                    float2 x = unpack2(r[c]);
+                    odd = fma2(x, make_float2(0.f, 0.f), odd);
+                    x = mul2(x, f);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) {
+                        const uint32_t y = pack_bf16(x.x, x.y);
+                        part[p][c / 2][2 * t + c % 2] = y;
+                        if (p + 1 < PARTS) x = less2(x, y);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int t = 0; t < 32; ++t) part[0][t] = part[1][t] = part[2][t] = 0;
             }
             if (n > 0 && !await(bar_u, (n - 1) & 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) tmem_st32(tv + 32 * p, part[p]);
+            for (int p = 0; p < PARTS; ++p) {
+                tmem_st_frag8(tv + 32 * p, part[p][0]);
+                tmem_st_frag8(tv + 32 * p + (16u << 16), part[p][1]);
+            }
             if (OUT) {
                 // Values that are not finite are taken out of the product with the weights (a weight of zero would not stop
                 // them); the walk's rows from the first of them on get it back.
                 int mark = kC;
-                if (__any_sync(kAll, odd != 0.f)) {
-                    if (odd != 0.f)
+                if (__any_sync(kAll, odd.x + odd.y != 0.f)) {
+                    if (j < DV)
 #pragma unroll 1
                         for (int i = m - 1; i >= 0; --i) {
                             const int t = rev ? m - 1 - i : i;
-                            const uint32_t a = mine + t * 128 + ((chunk ^ (t & 7)) << 4);
+                            const uint32_t a = st + L::kV + (j / 64) * kHalf + t * 128 + (((j % 64 / 8) ^ (t & 7)) << 4) + (j % 8) * 2;
                             if ((lds16(a) & 0x7f80u) == 0x7f80u) {
                                 mark = i;
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
@@ -468,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                         }
                     fence_proxy_async();
                 }
-                marks[n % kMarks][tid - 256] = mark;
+                marks[n % kMarks][j] = mark;
             }
             if (m < kC) {   // rows of other sequences
                 constexpr int kRows = (L::kKHalves + L::kVHalves) * 8;   // pieces of a token
@@ -489,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
         }
     } else {
-        // ---- outputs: value channel j a thread; a warp's 32 channels of the chunk are put in token order and stored
+        // ---- outputs: 32 value channels a warp, as fragments like those of V', put in token order and stored
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
         const int j = tid - 384;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, ti = tmem + kTmI + lanes, tx = tmem + kTmX + lanes;
@@ -499,37 +575,48 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 const bool last = is_last(n);
                 const int m = last ? m_last : kC;
                 const uint32_t out = sb + L::kO + ((n & 1) * 4 + (warp & 3)) * 4096;
+                // 16 bytes `c` of token t
+                auto piece = [&](int t, int c) { return out + t * 64 + ((c ^ (t >> 1 & 3)) << 4); };
                 if (lane == 0) bulk_wait_read1();   // the store of two chunks ago has read its place
                 __syncwarp();
                 if (!await(bar_o, n & 1)) break;
                 tc_fence_after();
                 const int mark = marks[n % kMarks][j];
-                const float* f = rf[last];
 #pragma unroll
-                for (int c = 0; c < kC; c += 32) {
+                for (int half = 0; half < 2; ++half) {
                     uint32_t x[32], y[32];
-                    tmem_ld32(ti + c, x);
-                    tmem_ld32(tx + c, y);
+                    tmem_ld_frag8(ti + half * (16u << 16), x);
+                    tmem_ld_frag8(tx + half * (16u << 16), y);
                     tmem_wait_ld();
                     loaded(x);
                     loaded(y);
-                    if (c + 32 == kC) {
+                    if (half) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_o_free);
                     }
+                    uint32_t z[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(f[c + i], __uint_as_float(y[i]), __uint_as_float(x[i])));
-                    if (__any_sync(kAll, mark < kC))
+                    for (int t = 0; t < 8; ++t) {
+                        const float2 f = *reinterpret_cast<const float2*>(&rf[last][8 * t + 2 * (lane % 4)]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((rev ? m - 1 - (c + i) : c + i) >= mark) x[i] = 0x7fc00000u;
+                        for (int c = 0; c < 2; ++c) {
+                            const int e = 4 * t + 2 * c;
+                            const float2 o = fma2(f, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
+                                                  make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                            z[2 * t + c] = pack_bf16(o.x, o.y);
+                        }
+                    }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const uint32_t z = pack_bf16(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + (c + i) * 64 + lane * 2), "h"(static_cast<uint16_t>(z)) : "memory");
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(out + (c + i + 1) * 64 + lane * 2), "h"(static_cast<uint16_t>(z >> 16))
-                                     : "memory");
+                    for (int t = 0; t < 8; t += 2)
+                        stmatrix_t(piece(8 * (t + lane / 16) + lane % 8, 2 * half + lane / 8 % 2), z[2 * t], z[2 * t + 1], z[2 * t + 2], z[2 * t + 3]);
+                }
+                if (__any_sync(kAll, mark < kC)) {
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = mark; i < m; ++i) {
+                        const int t = rev ? m - 1 - i : i;
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(piece(t, lane / 8) + lane % 8 * 2), "h"(static_cast<uint16_t>(0x7fc0)) : "memory");
                     }
                 }
                 const int t = row0 + place(n) * kC;
@@ -547,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     for (int i = lane / 4; i < m; i += 8) {
                         uint4 x;
                         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                     : "r"(out + i * 64 + lane % 4 * 16));
+                                     : "r"(piece(i, lane % 4)));
                         *reinterpret_cast<uint4*>(o + static_cast<long long>(i) * P.H * DV + lane % 4 * 8) = x;
                     }
                     __syncwarp();
@@ -622,7 +709,7 @@ cudaError_t launch_decay_tc(const DecayParams& P, int n_jobs, cudaStream_t s) {
         if (!encode(&T.q[i], j.q, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode(&T.k[i], j.k, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode(&T.v[i], j.v, P.n_tok, P.H, dv, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode(&T.o[i], o, P.n_tok, P.H, dv, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
+            !encode(&T.o[i], o, P.n_tok, P.H, dv, 32, CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
     }
     if (dk == 128) return dv == 128 ? start_pass<128, 128>(T, n_jobs, s) : start_pass<128, 64>(T, n_jobs, s);
