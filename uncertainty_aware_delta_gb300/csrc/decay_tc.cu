@@ -30,12 +30,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;                        // tokens of a chunk
-constexpr int kThreads = 512;                 // loader, products, two weight warps; state, V' and output warpgroups
-constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 136, kOutputRegs = 96;   // 4 x 128 in all, as launched
+constexpr int kThreads = 512;                 // two product warps, two weight warps; state, V' and output warpgroups
+constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 104, kOutputRegs = 128;   // 4 x 128 in all; the last as launched
 constexpr int kStages = 3;
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kHalf = 8192;              // 64 tokens of 64 channels
+constexpr uint32_t kFRow = 36 * 4;            // 32 powers; rows apart by 4 banks
 constexpr int kMarks = 4;                     // chunks whose marks of values that are not finite are kept
 
 struct TcParams {
@@ -48,8 +49,9 @@ template <int DK, int DV> struct Layout {
     // a stage: halves of K and Q in turn (128 rows of a product), then halves of V
     static constexpr uint32_t kV = kKHalves * 2 * kHalf, kStage = kV + kVHalves * kHalf;
     static constexpr uint32_t kP = kStages * kStage, kO = kP + 2 * kHalf;   // weights of two chunks; outputs: 4 KB a warp, twice
+    static constexpr uint32_t kF = kO + 2 * 4 * 4096;   // the weights' powers, 2 x 32 rows
     // (products read 128 value channels: with 64, the second half is what lies behind, and its rows are not used)
-    static constexpr uint32_t kSmem = kO + 2 * 4 * 4096 + 1024;
+    static constexpr uint32_t kSmem = kF + 2 * 32 * kFRow + 1024;
 };
 
 // TMEM columns: W; O within the chunk and from the state; U; parts of V'; S^T
@@ -98,16 +100,19 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {   // after tmem_wait_ld(): ties the registers to that point
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
 }
-// Fragments of 16 lanes: 32-bit column t % 4 of lanes t / 4 and t / 4 + 8 (and again four columns on, eight times in all) ...
-__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+template <int N> __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {   // after tmem_wait_ld(): ties the registers to that point
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// Fragments of 16 lanes: 32-bit column t % 4 of lanes t / 4 and t / 4 + 8 (and again four columns on) ...
+__device__ __forceinline__ void tmem_st_frag2(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 }
 // ... and columns 2 (t % 4), + 1 of lane t / 4, then those of lane t / 4 + 8 (and again eight columns on, eight times in all).
 __device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t (&r)[32]) {
@@ -144,10 +149,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 __device__ __forceinline__ float2 unpack2(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
-__device__ __forceinline__ float2 less2(float2 a, uint32_t b) {   // a - b
-    const float2 y = unpack2(b);
-    return fma2(y, make_float2(-1.f, -1.f), a);
-}
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t x;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));
@@ -160,17 +161,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     using L = Layout<DK, DV>;
     const DecayParams& P = T.d;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * kStages + 11];
+    __shared__ uint64_t bars[3 * kStages + 12];
     __shared__ float pw[kC + 1];
     __shared__ __align__(16) float vf[2][kC], rf[2][kC];   // factors of the chunk's tokens in V' and in outputs: whole chunk, last one
-    __shared__ __align__(16) float fars[32];               // powers of the columns of a block that the diagonal does not cut
     __shared__ int marks[kMarks][128];                     // per value channel, the walk's first token that is not finite
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages, bar_w = bar_empty + 8 * kStages, bar_p = bar_w + 8,
-                   bar_v = bar_p + 8, bar_u = bar_v + 8, bar_u_free = bar_u + 8, bar_s = bar_u_free + 8, bar_s_free = bar_s + 8,
-                   bar_o = bar_s_free + 8, bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;
+    // a barrier a stage: loaded, free, its values in V' (and what is not to be multiplied taken out)
+    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages, bar_v2 = bar_empty + 8 * kStages,
+                   bar_w = bar_v2 + 8 * kStages, bar_p = bar_w + 8, bar_v1 = bar_p + 8, bar_u1 = bar_v1 + 8, bar_u = bar_u1 + 8,
+                   bar_u_free = bar_u + 8, bar_s = bar_u_free + 8, bar_s_free = bar_s + 8, bar_o = bar_s_free + 8,
+                   bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;   // bar_v1, bar_u1: the first 32 tokens
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int job = blockIdx.z, bh = blockIdx.x, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
     const DecayJob& J = P.job[job];
@@ -212,18 +214,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         aborted = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(bar_full + 8 * i, 1);
-            mbar_init(bar_empty + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, OUT ? 2 : 1);
+            mbar_init(bar_v2 + 8 * i, 4);
         }
         mbar_init(bar_w, 1);
         mbar_init(bar_p, 2);
-        mbar_init(bar_v, 4);
+        mbar_init(bar_v1, 4);
+        mbar_init(bar_u1, 1);
         mbar_init(bar_u, 1);
         mbar_init(bar_u_free, 4);
         mbar_init(bar_s, 4);
         mbar_init(bar_s_free, 1);
         mbar_init(bar_o, 1);
         mbar_init(bar_o_free, 4);
-        mbar_init(bar_drain, 1);
+        mbar_init(bar_drain, OUT ? 2 : 1);
         mbar_init(bar_probe, 1);   // completed by nothing
         mbar_fence_init();
     }
@@ -238,7 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         vf[last][i] = left < 0 ? 0.f : pw[rev ? i + 1 : left];
         rf[last][i] = left < 0 ? 0.f : pw[rev ? left : i + 1];
     }
-    if (tid < 32) fars[tid] = pw[rev ? tid + 1 : 31 - tid];
+    // powers of the weights' two blocks of 32 x 32
+    for (int e = tid; e < 2 * 32 * 32; e += kThreads) {
+        const int i = e / 32 % 32, j = e % 32, gap = rev ? j - i : i - j;
+        const float f = e < 1024 ? pw[abs(gap)] : pw[32 + gap];
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + L::kF + (e / 32) * kFRow + 4 * j), "f"(f) : "memory");
+    }
     tc_fence_after();
     __syncthreads();
     const uint32_t tmem = tmem_slot;
@@ -258,108 +267,126 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 0, 0), id_u = idesc_bf16(128, DK, 0, 1, 0), id_i = idesc_bf16(128, 64, 1, 0, 0);
+        auto one = [](uint32_t x) { return __shfl_sync(kAll, x, 0); };
+        const uint32_t base = one(sb), tm = one(tmem);
         if (warp == 0) {
-            if (lane == 0) {
-                // ---- loader
-                int n = 0;
-#pragma unroll 1
-                for (; n < chunks; ++n) {
-                    const int slot = n % kStages;
-                    if (n >= kStages && !wait(bar_empty + 8 * slot, (n / kStages - 1) & 1)) break;
-                    const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
-                    const int t = row0 + place(n) * kC;
-                    mbar_expect_tx(full, OUT ? L::kStage : L::kKHalves * kHalf + L::kVHalves * kHalf);
-                    for (int f = 0; f < L::kKHalves; ++f) {
-                        tma_load_3d(st + 2 * f * kHalf, &T.k[job], 64 * f, h, t, full);
-                        if (OUT) tma_load_3d(st + (2 * f + 1) * kHalf, &T.q[job], 64 * f, h, t, full);
-                    }
-                    for (int f = 0; f < L::kVHalves; ++f) tma_load_3d(st + L::kV + f * kHalf, &T.v[job], 64 * f, h, t, full);
-                    if (P.probe && n == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
-                        aborted = 1;
-                        set_status(P.status, kStatusTimeout);
-                    }
-                    if (aborted) {
-                        ++n;
-                        break;
-                    }
-                }
-                // copies already issued land before the block's shared memory goes away
-                if (aborted)
-                    for (int i = max(n - kStages, 0); i < n; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
-            }
-        } else if (warp == 1) {
-            // ---- products
-            constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 0, 0), id_u = idesc_bf16(128, DK, 0, 1, 0), id_i = idesc_bf16(128, 64, 1, 0, 0);
+            // ---- products of the state, and loader: a chunk's copies are asked for after the products of the one two before it
             const uint32_t lead = elect_one();
-            auto one = [](uint32_t x) { return __shfl_sync(kAll, x, 0); };
-            const uint32_t base = one(sb), tm = one(tmem);
-            const uint64_t kq = sw128_desc(base, 16, 1024), kt = sw128_desc(base, 2 * kHalf, 1024), vt = sw128_desc(base + L::kV, kHalf, 1024),
-                           pd = sw128_desc(base + L::kP, 16, 1024);
-            auto weights = [&](uint32_t at) {
+            int sent = 0;
+            auto load = [&]() {   // (one lane)
+                const int slot = sent % kStages;
+                if (sent >= kStages && !wait(bar_empty + 8 * slot, (sent / kStages - 1) & 1)) return;
+                const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
+                const int t = row0 + place(sent) * kC;
+                mbar_expect_tx(full, OUT ? L::kStage : L::kKHalves * kHalf + L::kVHalves * kHalf);
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint64_t x = desc_add(kq, at + (k / 4) * 2 * kHalf + (k % 4) * 32);
-                    mma_ss(lead, tm + kTmW, x, x, id_w, k > 0);
+                for (int f = 0; f < L::kKHalves; ++f) {
+                    tma_load_3d(st + 2 * f * kHalf, &T.k[job], 64 * f, h, t, full);
+                    if (OUT) tma_load_3d(st + (2 * f + 1) * kHalf, &T.q[job], 64 * f, h, t, full);
                 }
+#pragma unroll
+                for (int f = 0; f < L::kVHalves; ++f) tma_load_3d(st + L::kV + f * kHalf, &T.v[job], 64 * f, h, t, full);
+                if (P.probe && sent == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
+                    aborted = 1;
+                    set_status(P.status, kStatusTimeout);
+                }
+                ++sent;
+            };
+#pragma unroll 1
+            for (int i = 0; i < kStages - 1 && i < chunks && !aborted; ++i)
+                if (lead) load();
+            __syncwarp();
+            const uint64_t kt = sw128_desc(base, 2 * kHalf, 1024);
+            uint32_t slot = 0, phase = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int n = 0; n < chunks; ++n) {
+                const uint32_t at = slot * L::kStage, par = n & 1;
+                if (n > 0 && !(ok = await(bar_u_free, par ^ 1))) break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = await(half ? bar_v2 + 8 * slot : bar_v1, half ? phase : par))) break;
+                    tc_fence_after();
+                    // (the small parts first: the sums' last bits are cut off)
+#pragma unroll
+                    for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_ts(lead, tm + kTmU, tm + kTmV + 32 * p + 16 * half + 8 * k, desc_add(kt, at + half * 4096 + k * 2048), id_u,
+                                   half || p < PARTS - 1 || k > 0);
+                    commit(lead, half ? bar_u : bar_u1);
+                }
+                if (!ok) break;
+                commit(lead, bar_empty + 8 * slot);
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (lead && sent < chunks && !aborted) load();
+                __syncwarp();
+            }
+            // products already issued end before TMEM goes away, and copies before shared memory does
+            commit(lead, bar_drain);
+            mbar_wait(bar_drain, 0, kWaitLimit);
+            if (lead && aborted)
+                for (int i = max(sent - kStages, 0); i < sent; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
+        } else if (warp == 1 && OUT) {
+            // ---- products of the outputs
+            const uint32_t lead = elect_one();
+            const uint64_t kq = sw128_desc(base, 16, 1024), vt = sw128_desc(base + L::kV, kHalf, 1024), pd = sw128_desc(base + L::kP, 16, 1024);
+            auto weights = [&](uint32_t at) {
+#pragma unroll 1
+                for (int f = 0; f < L::kKHalves; ++f)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t x = desc_add(kq, at + f * 2 * kHalf + k * 32);
+                        mma_ss(lead, tm + kTmW, x, x, id_w, f > 0 || k > 0);
+                    }
                 commit(lead, bar_w);
             };
             uint32_t slot = 0, phase = 0;
             bool ok = await(bar_full, 0);
             tc_fence_after();
-            if (ok && OUT) weights(0);
+            if (ok) weights(0);
 #pragma unroll 1
             for (int n = 0; ok && n < chunks; ++n) {
-                const uint32_t at = slot * L::kStage, par = n & 1;
-                if (!(ok = await(bar_v, par))) break;
-                if (n > 0 && !(ok = await(bar_u_free, par ^ 1))) break;
-                tc_fence_after();
-                // (the small parts first: the sums' last bits are cut off)
-#pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)
-                        mma_ts(lead, tm + kTmU, tm + kTmV + 32 * p + 8 * k, desc_add(kt, at + k * 2048), id_u, p < PARTS - 1 || k > 0);
-                commit(lead, bar_u);
-                if (!OUT) commit(lead, bar_empty + 8 * slot);
+                const uint32_t here = slot, at = here * L::kStage, par = n & 1, turn = phase;
                 if (++slot == kStages) {
                     slot = 0;
                     phase ^= 1;
                 }
-                if (OUT) {
-                    if (!(ok = await(bar_p, par))) break;
-                    if (n + 1 < chunks) {
-                        if (!(ok = await(bar_full + 8 * slot, phase))) break;
-                        tc_fence_after();
-                        weights(slot * L::kStage);
-                    }
-                    if (!(ok = await(bar_s, par))) break;
-                    if (n > 0 && !(ok = await(bar_o_free, par ^ 1))) break;
+                if (!(ok = await(bar_p, par))) break;
+                if (n + 1 < chunks) {
+                    if (!(ok = await(bar_full + 8 * slot, phase))) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_ts(lead, tm + kTmX, tm + kTmS + 8 * k, desc_add(kq, at + kHalf + (k / 4) * 2 * kHalf + (k % 4) * 32), id_w, k > 0);
-                    commit(lead, bar_s_free);
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)
-                        mma_ss(lead, tm + kTmI, desc_add(vt, at + k * 2048), desc_add(pd, par * kHalf + k * 32), id_i, k > 0);
-                    commit(lead, bar_o);
-                    commit(lead, bar_empty + 8 * (at / L::kStage));
+                    weights(slot * L::kStage);
                 }
+                if (!(ok = await(bar_s, par))) break;
+                if (n > 0 && !(ok = await(bar_o_free, par ^ 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int f = 0; f < L::kKHalves; ++f)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(lead, tm + kTmX, tm + kTmS + 32 * f + 8 * k, desc_add(kq, at + kHalf + f * 2 * kHalf + k * 32), id_w, f > 0 || k > 0);
+                commit(lead, bar_s_free);
+                if (!(ok = await(bar_v2 + 8 * here, turn))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k)
+                    mma_ss(lead, tm + kTmI, desc_add(vt, at + k * 2048), desc_add(pd, par * kHalf + k * 32), id_i, k > 0);
+                commit(lead, bar_o);
+                commit(lead, bar_empty + 8 * here);
             }
-            // products already issued end before TMEM goes away
             commit(lead, bar_drain);
             mbar_wait(bar_drain, 0, kWaitLimit);
-        } else if (OUT) {
+        } else if (warp >= 2 && OUT) {
             // ---- weights: row i of the chunk a thread (TMEM lanes 64 + i).  Of the two blocks of 32 columns one is cut by the
             // diagonal, with the same powers in every chunk, and one is seen whole or not at all.
             const int low = warp - 2, i = lane;   // rows 32 low + i
             const bool whole = rev ? low == 0 : low == 1;
-            const uint32_t tw = tmem + kTmW + (static_cast<uint32_t>(warp * 32) << 16);
-            float near[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) near[j] = pw[abs(i - j)];
-            const float far = pw[rev ? 31 - i : i + 1];
-            const uint32_t far_at = smem_addr(fars);
+            const uint32_t tw = tmem + kTmW + (static_cast<uint32_t>(warp * 32) << 16), mine = sb + L::kF + i * kFRow;
             const uint32_t cut = rev ? ~((1u << i) - 1u) : (2u << i) - 1u;   // columns of the block that the row sees
             auto to = [&](int n, int c, int j) { return sb + L::kP + (n & 1) * kHalf + sw128_off(32 * low + i, 4 * c + j); };
             auto put = [&](uint32_t a, const uint32_t* x) {
@@ -378,33 +405,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 tc_fence_after();
                 // (a short chunk's last columns are masked by the diagonal in a forward walk)
                 const int m = rev && is_last(n) ? m_last : kC;
-                uint32_t x[32];
-                tmem_ld32(tw + 32 * low, x);
-                tmem_wait_ld();
-                loaded(x);
-                uint32_t seen = cut;
-                if (m - 32 * low < 32) seen &= m > 32 * low ? (1u << (m - 32 * low)) - 1u : 0u;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = seen >> j & 1u ? __float_as_uint(__uint_as_float(x[j]) * near[j]) : 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) put(to(n, low, j), x + 8 * j);
-                if (whole) {
-                    const int c = low ^ 1;
+#pragma unroll 1
+                for (int e = 0; e < (whole ? 2 : 1); ++e) {   // the block that is cut, then the other
+                    const int c = low ^ e;
+                    uint32_t x[32];
                     tmem_ld32(tw + 32 * c, x);
+                    uint32_t seen = e ? kAll : cut;
+                    if (m - 32 * c < 32) seen &= m > 32 * c ? (1u << (m - 32 * c)) - 1u : 0u;
                     tmem_wait_ld();
                     loaded(x);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        float f[4];   // (read again in every chunk: there are no registers for them)
+                        float f[4];
                         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                                     : "r"(far_at + 4 * j));
+                                     : "r"(mine + e * 32 * kFRow + 4 * j));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[j + e] = __float_as_uint(__uint_as_float(x[j + e]) * far * f[e]);
-                    }
-                    if (m < kC) {
-                        seen = m > 32 ? (1u << (m - 32)) - 1u : 0u;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = seen >> j & 1u ? x[j] : 0u;
+                        for (int y = 0; y < 4; ++y)
+                            x[j + y] = seen >> (j + y) & 1u ? __float_as_uint(__uint_as_float(x[j + y]) * f[y]) : 0u;
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) put(to(n, c, j), x + 8 * j);
@@ -458,16 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             if (!await(bar_u, n & 1)) break;
             tc_fence_after();
             const float2 f = is_last(n) ? f_last : f_full, fx = make_float2(f.x, f.x), fy = make_float2(f.y, f.y);
+            uint32_t x[2][16];   // the next columns are on their way while these are added
+            tmem_ld16(tu, x[0]);
 #pragma unroll
-            for (int c = 0; c < DK; c += 32) {
-                uint32_t x[32];
-                tmem_ld32(tu + c, x);
+            for (int c = 0; c < DK; c += 16) {
                 tmem_wait_ld();
-                loaded(x);
+                loaded(x[c / 16 % 2]);
+                if (c + 16 < DK) tmem_ld16(tu + c + 16, x[(c / 16 + 1) % 2]);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < 16; i += 2) {
+                    const uint32_t* u = x[c / 16 % 2] + i;
                     const float2 y = make_float2(S[c + i], S[c + i + 1]),
-                                 z = fma2(fx, y, fma2(fy, y, make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]))));
+                                 z = fma2(fx, y, fma2(fy, y, make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]))));
                     S[c + i] = z.x;
                     S[c + i + 1] = z.y;
                 }
@@ -487,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     } else if (warp < 12) {
         // ---- V': 32 value channels a warp, transposed on the way from shared memory to fragments: a thread has tokens
         // 8 t + 2 (lane % 4), + 1 of channels lane / 4 + 0, 8, 16, 24
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kValueRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kValueRegs));
         const int j = tid - 256;   // the channel whose marks the thread keeps
         const uint32_t tv = tmem + kTmV + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t rows = L::kV + (j / 64) * kHalf + (lane & 7) * 128 + (((j % 64 / 32 * 4 + lane / 8) ^ (lane & 7)) << 4);
@@ -498,35 +517,58 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             const bool last = is_last(n);
             const int m = last ? m_last : kC;
             const uint32_t st = sb + slot * L::kStage;
-            uint32_t part[PARTS][2][16];   // of lanes 0 .. 15 and 16 .. 31
             float2 odd = make_float2(0.f, 0.f);   // NaN where a value is not finite
+            bool ok = true;
+            // (in a loop of four, as short as may be: the block's roles together hardly fit the instruction cache)
+#pragma unroll 1
+            for (int t = 0; t < 8; t += 2) {
+                if (n > 0 && t % 4 == 0) {   // the last chunk's tokens have been used, half by half
+                    if (!(ok = await(t ? bar_u : bar_u1, (n - 1) & 1))) break;
+                    tc_fence_after();
+                }
+                uint32_t v[2][4] = {};
+                float2 f[2];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                uint32_t r[4] = {0, 0, 0, 0};
-                if (j - lane < DV) ldmatrix_t(st + rows + t * 1024, r);
-                const int at = 8 * t + 2 * (lane % 4);
-                const float2 f = *reinterpret_cast<const float2*>(&vf[last][at]);
+                for (int e = 0; e < 2; ++e) {
+                    if (j - lane < DV) ldmatrix_t(st + rows + (t + e) * 1024, v[e]);
+                    const int at = 8 * (t + e) + 2 * (lane % 4);
+                    f[e] = *reinterpret_cast<const float2*>(&vf[last][at]);
+                    if (m < kC) {   // rows of other sequences
+                        const uint32_t there = at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (last) r[c] &= at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
-                    float2 x = unpack2(r[c]);
-                    odd = fma2(x, make_float2(0.f, 0.f), odd);
-                    x = mul2(x, f);
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        const uint32_t y = pack_bf16(x.x, x.y);
-                        part[p][c / 2][2 * t + c % 2] = y;
-                        if (p + 1 < PARTS) x = less2(x, y);
+                        for (int c = 0; c < 4; ++c) v[e][c] &= there;
                     }
                 }
-            }
-            if (n > 0 && !await(bar_u, (n - 1) & 1)) break;
-            tc_fence_after();
+                uint32_t part[PARTS][2][4];   // of lanes 0 .. 15 and 16 .. 31
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                tmem_st_frag8(tv + 32 * p, part[p][0]);
-                tmem_st_frag8(tv + 32 * p + (16u << 16), part[p][1]);
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float2 x = unpack2(v[e][c]);
+                        odd = fma2(x, make_float2(0.f, 0.f), odd);
+                        x = mul2(x, f[e]);
+                        // (parts cut off, not rounded: three have all 24 bits, and cutting off takes one instruction a pair)
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {
+                            part[p][c / 2][2 * e + c % 2] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+                            if (p + 1 < PARTS)
+                                x = fma2(make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
+                                         make_float2(-1.f, -1.f), x);
+                        }
+                    }
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    tmem_st_frag2(tv + 32 * p + 4 * t, part[p][0]);
+                    tmem_st_frag2(tv + 32 * p + 4 * t + (16u << 16), part[p][1]);
+                }
+                if (t == 2 && m == kC) {   // (a short chunk's keys are not ready yet)
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_v1);
+                }
             }
+            if (!ok) break;
             if (OUT) {
                 // Values that are not finite are taken out of the product with the weights (a weight of zero would not stop
                 // them); the walk's rows from the first of them on get it back.
@@ -558,7 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_v);
+            if (lane == 0) {
+                if (m < kC) mbar_arrive(bar_v1);
+                mbar_arrive(bar_v2 + 8 * slot);
+            }
             if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1;
@@ -566,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
     } else {
         // ---- outputs: 32 value channels a warp, as fragments like those of V', put in token order and stored
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
         const int j = tid - 384;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, ti = tmem + kTmI + lanes, tx = tmem + kTmX + lanes;
         if (OUT) {
@@ -582,11 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (!await(bar_o, n & 1)) break;
                 tc_fence_after();
                 const int mark = marks[n % kMarks][j];
+                uint32_t x[32], y[32];
+                tmem_ld_frag8(ti, x);
+                tmem_ld_frag8(tx, y);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t x[32], y[32];
-                    tmem_ld_frag8(ti + half * (16u << 16), x);
-                    tmem_ld_frag8(tx + half * (16u << 16), y);
                     tmem_wait_ld();
                     loaded(x);
                     loaded(y);
@@ -606,6 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                                                   make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
                             z[2 * t + c] = pack_bf16(o.x, o.y);
                         }
+                    }
+                    if (!half) {
+                        tmem_ld_frag8(ti + (16u << 16), x);
+                        tmem_ld_frag8(tx + (16u << 16), y);
                     }
 #pragma unroll
                     for (int t = 0; t < 8; t += 2)
