@@ -3,7 +3,7 @@
 // One block walks a head of a sequence (or of a segment of it) in chunks of 64 tokens (the chunk form: decay.cu).  All
 // products have the value channels in their rows (TMEM lanes), so that the state lies in the registers of one warpgroup, a
 // value channel a thread, and goes back into the products through TMEM:
-//   W  = Q K^T              (rows: 64 of K, not used, and 64 of Q; an MMA of 64 rows takes as long)
+//   W  = Q K^T              (64 rows of 128: an MMA of 64 takes as long)
 //   P  = W g^(i-j)          bf16, shared memory
 //   U^T = V'^T K            V'_j = g^(m-1-j) v_j in bf16 parts, written to TMEM by a warpgroup that reads V transposed
 //   S   = g^m S + U         fp32, registers;  bf16 S^T to TMEM
@@ -30,9 +30,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;                        // tokens of a chunk
-constexpr int kThreads = 512;                 // two product warps, two weight warps; state, V' and output warpgroups
-constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 104, kOutputRegs = 128;   // 4 x 128 in all; the last as launched
-constexpr int kStages = 3;
+// two weight warps and two product warps; the state; V' of a chunk's first and second 32 tokens; outputs: a warpgroup each.  (A
+// warp more would leave 80 registers a thread at launch: a quarter of the SM's registers is for six warps then.)
+constexpr int kThreads = 640;
+constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 64, kOutputRegs = 72;   // 96 + 184 + 2 x 64 + 72 = 5 x 96, as launched
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kHalf = 8192;              // 64 tokens of 64 channels
@@ -44,25 +45,24 @@ struct TcParams {
     DecayParams d;
 };
 
-template <int DK, int DV> struct Layout {
-    static constexpr int kKHalves = DK / 64, kVHalves = DV / 64;
-    // a stage: halves of K and Q in turn (128 rows of a product), then halves of V
-    static constexpr uint32_t kV = kKHalves * 2 * kHalf, kStage = kV + kVHalves * kHalf;
+template <int DK, int DV, bool OUT> struct Layout {
+    static constexpr int kStages = OUT ? (DK + DV == 128 ? 6 : 3) : 6, kKHalves = DK / 64, kVHalves = DV / 64;
+    // a stage: halves of K, of Q, of V.  (Products read 128 rows of Q and 128 value channels: what lies behind a half, or behind
+    // 64 channels, is multiplied too, and its rows are not used.)
+    static constexpr uint32_t kQ = kKHalves * kHalf, kV = (OUT ? 2 : 1) * kQ, kStage = kV + kVHalves * kHalf;
     static constexpr uint32_t kP = kStages * kStage, kO = kP + 2 * kHalf;   // weights of two chunks; outputs: 4 KB a warp, twice
     static constexpr uint32_t kF = kO + 2 * 4 * 4096;   // the weights' powers, 2 x 32 rows
-    // (products read 128 value channels: with 64, the second half is what lies behind, and its rows are not used)
-    static constexpr uint32_t kSmem = kF + 2 * 32 * kFRow + 1024;
+    static constexpr uint32_t kSmem = (OUT ? kF + 2 * 32 * kFRow : kP + kHalf) + 1024;
 };
 
-// TMEM columns: W; O within the chunk and from the state; U; parts of V'; S^T
-constexpr uint32_t kTmW = 0, kTmI = 64, kTmX = 128, kTmU = 192, kTmV = 320, kTmS = 416, kTmCols = 512;
+// TMEM columns: W; O within the chunk and from the state; U; parts of V'; S^T.  Where the state alone is wanted there is room
+// for U and V' of two chunks.
+template <bool OUT> struct Tm {
+    static constexpr int kBufs = OUT ? 1 : 2;
+    static constexpr uint32_t kW = 0, kI = 64, kX = 128, kU = 192, kV = OUT ? 320 : 0, kS = 416;
+};
+constexpr uint32_t kTmCols = 512;
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0), "r"(c1),
                  "r"(c2), "r"(src)
@@ -100,12 +100,6 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
 template <int N> __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {   // after tmem_wait_ld(): ties the registers to that point
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
@@ -114,17 +108,12 @@ template <int N> __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {   //
 __device__ __forceinline__ void tmem_st_frag2(uint32_t taddr, const uint32_t (&r)[4]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 }
-// ... and columns 2 (t % 4), + 1 of lane t / 4, then those of lane t / 4 + 8 (and again eight columns on, eight times in all).
-__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
+// ... and columns 2 (t % 4), + 1 of lane t / 4, then those of lane t / 4 + 8 (and again eight columns on).
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
 }
 // Four 8 x 8 matrices of 16 bits, transposed: a lane's address is a row's (matrix lane / 8, row lane % 8).
 __device__ __forceinline__ void ldmatrix_t(uint32_t a, uint32_t (&r)[4]) {
@@ -158,21 +147,23 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 // OUT: outputs, else the state alone.  PARTS: of V'.
 template <int DK, int DV, bool OUT, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_constant__ TcParams T) {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, OUT>;
+    using M = Tm<OUT>;
+    constexpr int kStages = L::kStages;
     const DecayParams& P = T.d;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[3 * kStages + 12];
+    __shared__ uint64_t bars[4 * kStages + 13];
     __shared__ float pw[kC + 1];
     __shared__ __align__(16) float vf[2][kC], rf[2][kC];   // factors of the chunk's tokens in V' and in outputs: whole chunk, last one
-    __shared__ int marks[kMarks][128];                     // per value channel, the walk's first token that is not finite
+    __shared__ int marks[kMarks][2][128];                  // per value channel, the first token of the walk (in a half) that is not finite
     __shared__ volatile int aborted;
     __shared__ uint32_t tmem_slot;
     const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    // a barrier a stage: loaded, free, its values in V' (and what is not to be multiplied taken out)
-    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages, bar_v2 = bar_empty + 8 * kStages,
-                   bar_w = bar_v2 + 8 * kStages, bar_p = bar_w + 8, bar_v1 = bar_p + 8, bar_u1 = bar_v1 + 8, bar_u = bar_u1 + 8,
-                   bar_u_free = bar_u + 8, bar_s = bar_u_free + 8, bar_s_free = bar_s + 8, bar_o = bar_s_free + 8,
-                   bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;   // bar_v1, bar_u1: the first 32 tokens
+    // a barrier a stage: loaded, free, V' of the first 32 tokens, V' of all (and what is not to be multiplied taken out)
+    const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages, bar_v1 = bar_empty + 8 * kStages,
+                   bar_v2 = bar_v1 + 8 * kStages, bar_u = bar_v2 + 8 * kStages, bar_u_free = bar_u + 16, bar_u1 = bar_u_free + 16,
+                   bar_w = bar_u1 + 8, bar_p = bar_w + 8, bar_s = bar_p + 8, bar_s_free = bar_s + 8, bar_o = bar_s_free + 8,
+                   bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;   // bar_u1: the first 32 tokens
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int job = blockIdx.z, bh = blockIdx.x, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
     const DecayJob& J = P.job[job];
@@ -215,14 +206,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         for (int i = 0; i < kStages; ++i) {
             mbar_init(bar_full + 8 * i, 1);
             mbar_init(bar_empty + 8 * i, OUT ? 2 : 1);
-            mbar_init(bar_v2 + 8 * i, 4);
+            mbar_init(bar_v1 + 8 * i, 4);
+            mbar_init(bar_v2 + 8 * i, 8);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_u + 8 * i, 1);
+            mbar_init(bar_u_free + 8 * i, 4);
+        }
+        mbar_init(bar_u1, 1);
         mbar_init(bar_w, 1);
         mbar_init(bar_p, 2);
-        mbar_init(bar_v1, 4);
-        mbar_init(bar_u1, 1);
-        mbar_init(bar_u, 1);
-        mbar_init(bar_u_free, 4);
         mbar_init(bar_s, 4);
         mbar_init(bar_s_free, 1);
         mbar_init(bar_o, 1);
@@ -243,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         rf[last][i] = left < 0 ? 0.f : pw[rev ? left : i + 1];
     }
     // powers of the weights' two blocks of 32 x 32
-    for (int e = tid; e < 2 * 32 * 32; e += kThreads) {
+    for (int e = tid; OUT && e < 2 * 32 * 32; e += kThreads) {
         const int i = e / 32 % 32, j = e % 32, gap = rev ? j - i : i - j;
         const float f = e < 1024 ? pw[abs(gap)] : pw[32 + gap];
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(sb + L::kF + (e / 32) * kFRow + 4 * j), "f"(f) : "memory");
@@ -266,56 +259,32 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     auto await = [&](uint32_t bar, uint32_t parity) { return __all_sync(kAll, wait(bar, parity)); };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 0, 0), id_u = idesc_bf16(128, DK, 0, 1, 0), id_i = idesc_bf16(128, 64, 1, 0, 0);
         auto one = [](uint32_t x) { return __shfl_sync(kAll, x, 0); };
         const uint32_t base = one(sb), tm = one(tmem);
-        if (warp == 0) {
-            // ---- products of the state, and loader: a chunk's copies are asked for after the products of the one two before it
+        if (warp == 2) {
+            // ---- products of the state
             const uint32_t lead = elect_one();
-            int sent = 0;
-            auto load = [&]() {   // (one lane)
-                const int slot = sent % kStages;
-                if (sent >= kStages && !wait(bar_empty + 8 * slot, (sent / kStages - 1) & 1)) return;
-                const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
-                const int t = row0 + place(sent) * kC;
-                mbar_expect_tx(full, OUT ? L::kStage : L::kKHalves * kHalf + L::kVHalves * kHalf);
-#pragma unroll
-                for (int f = 0; f < L::kKHalves; ++f) {
-                    tma_load_3d(st + 2 * f * kHalf, &T.k[job], 64 * f, h, t, full);
-                    if (OUT) tma_load_3d(st + (2 * f + 1) * kHalf, &T.q[job], 64 * f, h, t, full);
-                }
-#pragma unroll
-                for (int f = 0; f < L::kVHalves; ++f) tma_load_3d(st + L::kV + f * kHalf, &T.v[job], 64 * f, h, t, full);
-                if (P.probe && sent == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
-                    aborted = 1;
-                    set_status(P.status, kStatusTimeout);
-                }
-                ++sent;
-            };
-#pragma unroll 1
-            for (int i = 0; i < kStages - 1 && i < chunks && !aborted; ++i)
-                if (lead) load();
-            __syncwarp();
-            const uint64_t kt = sw128_desc(base, 2 * kHalf, 1024);
+            const uint64_t kt = sw128_desc(base, kHalf, 1024);
             uint32_t slot = 0, phase = 0;
             bool ok = true;
 #pragma unroll 1
             for (int n = 0; n < chunks; ++n) {
-                const uint32_t at = slot * L::kStage, par = n & 1;
-                if (n > 0 && !(ok = await(bar_u_free, par ^ 1))) break;
+                const uint32_t at = slot * L::kStage, buf = n % M::kBufs, turn = n / M::kBufs;
+                if (turn > 0 && !(ok = await(bar_u_free + 8 * buf, (turn - 1) & 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    if (!(ok = await(half ? bar_v2 + 8 * slot : bar_v1, half ? phase : par))) break;
+                    if (!(ok = await((half ? bar_v2 : bar_v1) + 8 * slot, phase))) break;
                     tc_fence_after();
                     // (the small parts first: the sums' last bits are cut off)
 #pragma unroll
                     for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            mma_ts(lead, tm + kTmU, tm + kTmV + 32 * p + 16 * half + 8 * k, desc_add(kt, at + half * 4096 + k * 2048), id_u,
-                                   half || p < PARTS - 1 || k > 0);
-                    commit(lead, half ? bar_u : bar_u1);
+                            mma_ts(lead, tm + M::kU + 128 * buf, tm + M::kV + 96 * buf + 32 * p + 16 * half + 8 * k,
+                                   desc_add(kt, at + half * 4096 + k * 2048), id_u, half || p < PARTS - 1 || k > 0);
+                    if (half) commit(lead, bar_u + 8 * buf);
+                    else if (OUT) commit(lead, bar_u1);
                 }
                 if (!ok) break;
                 commit(lead, bar_empty + 8 * slot);
@@ -323,25 +292,21 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     slot = 0;
                     phase ^= 1;
                 }
-                if (lead && sent < chunks && !aborted) load();
-                __syncwarp();
             }
-            // products already issued end before TMEM goes away, and copies before shared memory does
+            // products already issued end before TMEM goes away
             commit(lead, bar_drain);
             mbar_wait(bar_drain, 0, kWaitLimit);
-            if (lead && aborted)
-                for (int i = max(sent - kStages, 0); i < sent; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
-        } else if (warp == 1 && OUT) {
+        } else if (warp == 3 && OUT) {
             // ---- products of the outputs
             const uint32_t lead = elect_one();
-            const uint64_t kq = sw128_desc(base, 16, 1024), vt = sw128_desc(base + L::kV, kHalf, 1024), pd = sw128_desc(base + L::kP, 16, 1024);
+            const uint64_t kd = sw128_desc(base, 16, 1024), qd = sw128_desc(base + L::kQ, 16, 1024), vt = sw128_desc(base + L::kV, kHalf, 1024), pd = sw128_desc(base + L::kP, 16, 1024);
             auto weights = [&](uint32_t at) {
 #pragma unroll 1
                 for (int f = 0; f < L::kKHalves; ++f)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint64_t x = desc_add(kq, at + f * 2 * kHalf + k * 32);
-                        mma_ss(lead, tm + kTmW, x, x, id_w, f > 0 || k > 0);
+                        const uint32_t x = at + f * kHalf + k * 32;
+                        mma_ss(lead, tm + M::kW, desc_add(qd, x), desc_add(kd, x), id_w, f > 0 || k > 0);
                     }
                 commit(lead, bar_w);
             };
@@ -369,24 +334,51 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 for (int f = 0; f < L::kKHalves; ++f)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(lead, tm + kTmX, tm + kTmS + 32 * f + 8 * k, desc_add(kq, at + kHalf + f * 2 * kHalf + k * 32), id_w, f > 0 || k > 0);
+                        mma_ts(lead, tm + M::kX, tm + M::kS + 32 * f + 8 * k, desc_add(qd, at + f * kHalf + k * 32), id_w, f > 0 || k > 0);
                 commit(lead, bar_s_free);
                 if (!(ok = await(bar_v2 + 8 * here, turn))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k)
-                    mma_ss(lead, tm + kTmI, desc_add(vt, at + k * 2048), desc_add(pd, par * kHalf + k * 32), id_i, k > 0);
+                    mma_ss(lead, tm + M::kI, desc_add(vt, at + k * 2048), desc_add(pd, par * kHalf + k * 32), id_i, k > 0);
                 commit(lead, bar_o);
                 commit(lead, bar_empty + 8 * here);
             }
             commit(lead, bar_drain);
             mbar_wait(bar_drain, 0, kWaitLimit);
-        } else if (warp >= 2 && OUT) {
-            // ---- weights: row i of the chunk a thread (TMEM lanes 64 + i).  Of the two blocks of 32 columns one is cut by the
+        } else if (warp < 2) {
+            // ---- loader, a lane of the warp that has less to do otherwise (asked for by the warp of the state's products or of
+            // the outputs, copies held these up by 600 to 1000 cycles a chunk)
+            const bool loads = lane == 0 && warp == (rev ? 1 : 0);
+            int sent = 0, slot = 0;
+            uint32_t phase = 1;
+            auto load = [&]() {   // the next chunk, once its stage is free
+                if (sent >= kStages && !wait(bar_empty + 8 * slot, phase)) return;
+                const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
+                const int t = row0 + place(sent) * kC;
+                mbar_expect_tx(full, L::kStage);
+                tma_load_4d(st, &T.k[job], 0, t, 0, h, full);
+                if (OUT) tma_load_4d(st + L::kQ, &T.q[job], 0, t, 0, h, full);
+                tma_load_4d(st + L::kV, &T.v[job], 0, t, 0, h, full);
+                if (P.probe && sent == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
+                    aborted = 1;
+                    set_status(P.status, kStatusTimeout);
+                }
+                ++sent;
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            if (loads)
+#pragma unroll 1
+                while (sent < chunks && (!OUT || sent < kStages) && !aborted) load();
+            __syncwarp();
+            // ---- weights: row i of the chunk a thread.  Of the two blocks of 32 columns one is cut by the
             // diagonal, with the same powers in every chunk, and one is seen whole or not at all.
-            const int low = warp - 2, i = lane;   // rows 32 low + i
+            const int low = warp, i = lane;   // rows 32 low + i
             const bool whole = rev ? low == 0 : low == 1;
-            const uint32_t tw = tmem + kTmW + (static_cast<uint32_t>(warp * 32) << 16), mine = sb + L::kF + i * kFRow;
+            const uint32_t tw = tmem + M::kW + (static_cast<uint32_t>(warp * 32) << 16), mine = sb + L::kF + i * kFRow;
             const uint32_t cut = rev ? ~((1u << i) - 1u) : (2u << i) - 1u;   // columns of the block that the row sees
             auto to = [&](int n, int c, int j) { return sb + L::kP + (n & 1) * kHalf + sw128_off(32 * low + i, 4 * c + j); };
             auto put = [&](uint32_t a, const uint32_t* x) {
@@ -395,12 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                 asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
             };
-            if (!whole)
+            if (OUT && !whole)
                 for (int n = 0; n < 2; ++n)
                     for (int j = 0; j < 4; ++j)
                         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to(n, low ^ 1, j)), "r"(0) : "memory");
 #pragma unroll 1
-            for (int n = 0; n < chunks; ++n) {
+            for (int n = 0; OUT && n < chunks; ++n) {
                 if (!await(bar_w, n & 1)) break;
                 tc_fence_after();
                 // (a short chunk's last columns are masked by the diagonal in a forward walk)
@@ -430,13 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_p);
+                // (the stage of the last chunk: done with by the time that this one's weights are used)
+                if (loads && n > 0 && sent < chunks && !aborted) load();
+                __syncwarp();
             }
+            // copies already issued land before the block's shared memory goes away
+            if (loads && aborted)
+                for (int i = max(sent - kStages, 0); i < sent; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
         }
     } else if (warp < 8) {
         // ---- state: value channel j a thread, all key channels in its registers
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
         const int j = tid - 128;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, tu = tmem + kTmU + lanes, ts = tmem + kTmS + lanes;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, tu = tmem + M::kU + lanes, ts = tmem + M::kS + lanes;
         const bool mine = j < DV;
         float S[DK];
         if (in && mine) {
@@ -472,19 +470,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         const float2 f_full = power2(l, kC), f_last = power2(l, m_last);
 #pragma unroll 1
         for (int n = 0; n < chunks; ++n) {
-            if (!await(bar_u, n & 1)) break;
+            const uint32_t buf = n % M::kBufs, here = tu + 128 * buf;
+            if (!await(bar_u + 8 * buf, n / M::kBufs & 1)) break;
             tc_fence_after();
             const float2 f = is_last(n) ? f_last : f_full, fx = make_float2(f.x, f.x), fy = make_float2(f.y, f.y);
-            uint32_t x[2][16];   // the next columns are on their way while these are added
-            tmem_ld16(tu, x[0]);
+            uint32_t x[2][32];   // the next columns are on their way while these are added
+            tmem_ld32(here, x[0]);
 #pragma unroll
-            for (int c = 0; c < DK; c += 16) {
+            for (int c = 0; c < DK; c += 32) {
                 tmem_wait_ld();
-                loaded(x[c / 16 % 2]);
-                if (c + 16 < DK) tmem_ld16(tu + c + 16, x[(c / 16 + 1) % 2]);
+                loaded(x[c / 32 % 2]);
+                if (c + 32 < DK) tmem_ld32(here + c + 32, x[(c / 32 + 1) % 2]);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const uint32_t* u = x[c / 16 % 2] + i;
+                for (int i = 0; i < 32; i += 2) {
+                    const uint32_t* u = x[c / 32 % 2] + i;
                     const float2 y = make_float2(S[c + i], S[c + i + 1]),
                                  z = fma2(fx, y, fma2(fy, y, make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]))));
                     S[c + i] = z.x;
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_u_free);
+            if (lane == 0) mbar_arrive(bar_u_free + 8 * buf);
             if (OUT && n + 1 < chunks) {
                 if (!await(bar_s_free, n & 1)) break;
                 tc_fence_after();
@@ -503,37 +502,36 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         if (end && mine && !aborted)
 #pragma unroll
             for (int i = 0; i < DK; ++i) end[static_cast<size_t>(i) * s_k + static_cast<size_t>(j) * s_v] = S[i];
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ---- V': 32 value channels a warp, transposed on the way from shared memory to fragments: a thread has tokens
-        // 8 t + 2 (lane % 4), + 1 of channels lane / 4 + 0, 8, 16, 24
+        // 8 t + 2 (lane % 4), + 1 of channels lane / 4 + 0, 8, 16, 24.  A warpgroup has tokens 0 .. 31, the other the rest.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kValueRegs));
-        const int j = tid - 256;   // the channel whose marks the thread keeps
-        const uint32_t tv = tmem + kTmV + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t rows = L::kV + (j / 64) * kHalf + (lane & 7) * 128 + (((j % 64 / 32 * 4 + lane / 8) ^ (lane & 7)) << 4);
+        const int j = tid % 128, half = warp >= 12;   // the channel whose marks the thread keeps
+        const uint32_t tv = tmem + M::kV + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t rows = L::kV + (j / 64) * kHalf + half * 4096 + (lane & 7) * 128 + (((j % 64 / 32 * 4 + lane / 8) ^ (lane & 7)) << 4);
         uint32_t slot = 0, phase = 0;
 #pragma unroll 1
         for (int n = 0; n < chunks; ++n) {
+            const uint32_t buf = n % M::kBufs;
             if (!await(bar_full + 8 * slot, phase)) break;
+            // the place of V' has been read
+            if (n >= M::kBufs && !await(OUT && !half ? bar_u1 : bar_u + 8 * buf, (n / M::kBufs - 1) & 1)) break;
+            tc_fence_after();
             const bool last = is_last(n);
-            const int m = last ? m_last : kC;
+            const int m = (last ? m_last : kC) - 32 * half;   // tokens from the half's first on
             const uint32_t st = sb + slot * L::kStage;
             float2 odd = make_float2(0.f, 0.f);   // NaN where a value is not finite
-            bool ok = true;
-            // (in a loop of four, as short as may be: the block's roles together hardly fit the instruction cache)
+            // (in a loop, as short as may be: the block's roles together hardly fit the instruction cache)
 #pragma unroll 1
-            for (int t = 0; t < 8; t += 2) {
-                if (n > 0 && t % 4 == 0) {   // the last chunk's tokens have been used, half by half
-                    if (!(ok = await(t ? bar_u : bar_u1, (n - 1) & 1))) break;
-                    tc_fence_after();
-                }
+            for (int t = 0; t < 4; t += 2) {
                 uint32_t v[2][4] = {};
                 float2 f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (j - lane < DV) ldmatrix_t(st + rows + (t + e) * 1024, v[e]);
                     const int at = 8 * (t + e) + 2 * (lane % 4);
-                    f[e] = *reinterpret_cast<const float2*>(&vf[last][at]);
-                    if (m < kC) {   // rows of other sequences
+                    f[e] = *reinterpret_cast<const float2*>(&vf[last][32 * half + at]);
+                    if (m < 32) {   // rows of other sequences
                         const uint32_t there = at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) v[e][c] &= there;
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float2 x = unpack2(v[e][c]);
-                        odd = fma2(x, make_float2(0.f, 0.f), odd);
+                        if (OUT) odd = fma2(x, make_float2(0.f, 0.f), odd);
                         x = mul2(x, f[e]);
                         // (parts cut off, not rounded: three have all 24 bits, and cutting off takes one instruction a pair)
 #pragma unroll
@@ -558,17 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                     }
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
-                    tmem_st_frag2(tv + 32 * p + 4 * t, part[p][0]);
-                    tmem_st_frag2(tv + 32 * p + 4 * t + (16u << 16), part[p][1]);
-                }
-                if (t == 2 && m == kC) {   // (a short chunk's keys are not ready yet)
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_v1);
+                    tmem_st_frag2(tv + 96 * buf + 32 * p + 4 * t, part[p][0]);
+                    tmem_st_frag2(tv + 96 * buf + 32 * p + 4 * t + (16u << 16), part[p][1]);
                 }
             }
-            if (!ok) break;
             if (OUT) {
                 // Values that are not finite are taken out of the product with the weights (a weight of zero would not stop
                 // them); the walk's rows from the first of them on get it back.
@@ -576,23 +567,24 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (__any_sync(kAll, odd.x + odd.y != 0.f)) {
                     if (j < DV)
 #pragma unroll 1
-                        for (int i = m - 1; i >= 0; --i) {
-                            const int t = rev ? m - 1 - i : i;
-                            const uint32_t a = st + L::kV + (j / 64) * kHalf + t * 128 + (((j % 64 / 8) ^ (t & 7)) << 4) + (j % 8) * 2;
-                            if ((lds16(a) & 0x7f80u) == 0x7f80u) {
-                                mark = i;
+                        for (int i = 31; i >= 0; --i) {
+                            const int t = rev ? 31 - i : i;
+                            const uint32_t a = st + L::kV + (j / 64) * kHalf + half * 4096 + t * 128 + (((j % 64 / 8) ^ (t & 7)) << 4) + (j % 8) * 2;
+                            if (t < m && (lds16(a) & 0x7f80u) == 0x7f80u) {
+                                mark = 32 * half + t;
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
                             }
                         }
                     fence_proxy_async();
                 }
-                marks[n % kMarks][j] = mark;
+                marks[n % kMarks][half][j] = mark;
             }
-            if (m < kC) {   // rows of other sequences
+            if (m < 32) {   // rows of other sequences
                 constexpr int kRows = (L::kKHalves + L::kVHalves) * 8;   // pieces of a token
-                for (int i = j; i < (kC - m) * kRows; i += 128) {
-                    const int t = m + i / kRows, c = i % kRows / 8;
-                    const uint32_t a = st + (c < L::kKHalves ? 2 * c * kHalf : L::kV + (c - L::kKHalves) * kHalf) + t * 128 + (i % 8) * 16;
+                const int gone = max(m, 0);
+                for (int i = j; i < (32 - gone) * kRows; i += 128) {
+                    const int t = 32 * half + gone + i / kRows, c = i % kRows / 8;
+                    const uint32_t a = st + (c < L::kKHalves ? c * kHalf : L::kV + (c - L::kKHalves) * kHalf) + t * 128 + (i % 8) * 16;
                     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0) : "memory");
                 }
                 fence_proxy_async();
@@ -601,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (m < kC) mbar_arrive(bar_v1);
+                if (!half) mbar_arrive(bar_v1 + 8 * slot);
                 mbar_arrive(bar_v2 + 8 * slot);
             }
             if (++slot == kStages) {
@@ -611,8 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         }
     } else {
         // ---- outputs: 32 value channels a warp, as fragments like those of V', put in token order and stored
-        const int j = tid - 384;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, ti = tmem + kTmI + lanes, tx = tmem + kTmX + lanes;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutputRegs));
+        const int j = tid - 512;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16, ti = tmem + M::kI + lanes, tx = tmem + M::kX + lanes;
         if (OUT) {
 #pragma unroll 1
             for (int n = 0; n < chunks; ++n) {
@@ -625,47 +618,42 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 __syncwarp();
                 if (!await(bar_o, n & 1)) break;
                 tc_fence_after();
-                const int mark = marks[n % kMarks][j];
-                uint32_t x[32], y[32];
-                tmem_ld_frag8(ti, x);
-                tmem_ld_frag8(tx, y);
+                const int mark0 = marks[n % kMarks][0][j], mark1 = marks[n % kMarks][1][j];
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {   // 16 channels and 32 tokens at a time
+                    const uint32_t at = ((e >> 1) * 16u << 16) + 32 * (e & 1);
+                    uint32_t x[16], y[16];
+                    tmem_ld_frag4(ti + at, x);
+                    tmem_ld_frag4(tx + at, y);
+                    float2 f[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                    for (int t = 0; t < 4; ++t) f[t] = *reinterpret_cast<const float2*>(&rf[last][32 * (e & 1) + 8 * t + 2 * (lane % 4)]);
                     tmem_wait_ld();
                     loaded(x);
                     loaded(y);
-                    if (half) {
+                    if (e == 3) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_o_free);
                     }
-                    uint32_t z[16];
+                    uint32_t z[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const float2 f = *reinterpret_cast<const float2*>(&rf[last][8 * t + 2 * (lane % 4)]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int e = 4 * t + 2 * c;
-                            const float2 o = fma2(f, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
-                                                  make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-                            z[2 * t + c] = pack_bf16(o.x, o.y);
-                        }
-                    }
-                    if (!half) {
-                        tmem_ld_frag8(ti + (16u << 16), x);
-                        tmem_ld_frag8(tx + (16u << 16), y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 o = fma2(f[i / 2], make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
+                                              make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
+                        z[i] = pack_bf16(o.x, o.y);
                     }
 #pragma unroll
-                    for (int t = 0; t < 8; t += 2)
-                        stmatrix_t(piece(8 * (t + lane / 16) + lane % 8, 2 * half + lane / 8 % 2), z[2 * t], z[2 * t + 1], z[2 * t + 2], z[2 * t + 3]);
+                    for (int t = 0; t < 4; t += 2)
+                        stmatrix_t(piece(32 * (e & 1) + 8 * (t + lane / 16) + lane % 8, (e & 2) + lane / 8 % 2), z[2 * t], z[2 * t + 1], z[2 * t + 2],
+                                   z[2 * t + 3]);
                 }
-                if (__any_sync(kAll, mark < kC)) {
+                if (__any_sync(kAll, min(mark0, mark1) < kC)) {
                     __syncwarp();
+                    const int first = rev ? (mark1 < kC ? mark1 : mark0 < kC ? mark0 : -1) : min(mark0, mark1);   // the walk's first
 #pragma unroll 1
-                    for (int i = mark; i < m; ++i) {
-                        const int t = rev ? m - 1 - i : i;
+                    for (int t = rev ? 0 : first; t < (rev ? first + 1 : m); ++t)
                         asm volatile("st.shared.u16 [%0], %1;" ::"r"(piece(t, lane / 8) + lane % 8 * 2), "h"(static_cast<uint16_t>(0x7fc0)) : "memory");
-                    }
                 }
                 const int t = row0 + place(n) * kC;
                 if (j - lane >= DV) continue;   // (the warps behind the value channels)
@@ -717,19 +705,29 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [rows, heads, d] bf16, tiles of 64 rows and `channels` of one head.
-bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d, int channels, CUtensorMapSwizzle swizzle) {
+// [rows, heads, d] bf16 as (channel of a half, row, half, head): tiles of 64 rows of one head, half after half.
+bool encode(CUtensorMap* m, const Strided& x, int rows, int heads, int d) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.row) * 2, 128, static_cast<cuuint64_t>(x.head) * 2};
+    const cuuint32_t box[4] = {64, kC, static_cast<cuuint32_t>(d / 64), 1}, step[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same for outputs: tiles of 64 rows and 32 channels.
+bool encode_out(CUtensorMap* m, void* p, int rows, int heads, int d) {
     const EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.head) * 2, static_cast<cuuint64_t>(x.row) * 2};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(channels), 1, kC}, step[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(heads) * d * 2};
+    const cuuint32_t box[3] = {32, 1, kC}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DK, int DV, bool OUT, int PARTS> cudaError_t start(const TcParams& T, int n_jobs, cudaStream_t s) {
-    constexpr int bytes = Layout<DK, DV>::kSmem;
+    constexpr int bytes = Layout<DK, DV, OUT>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<DK, DV, OUT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid(T.d.n_seq * T.d.H, T.d.pass == kWhole ? 1 : T.d.nseg, n_jobs);
@@ -753,11 +751,8 @@ cudaError_t launch_decay_tc(const DecayParams& P, int n_jobs, cudaStream_t s) {
     const int dk = P.job[0].dk, dv = P.job[0].dv;
     for (int i = 0; i < n_jobs; ++i) {
         const DecayJob& j = P.job[i];
-        const Strided o = {j.o, static_cast<long long>(P.H) * dv, dv};
-        if (!encode(&T.q[i], j.q, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode(&T.k[i], j.k, P.n_tok, P.H, dk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode(&T.v[i], j.v, P.n_tok, P.H, dv, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode(&T.o[i], o, P.n_tok, P.H, dv, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        if (!encode(&T.q[i], j.q, P.n_tok, P.H, dk) || !encode(&T.k[i], j.k, P.n_tok, P.H, dk) ||
+            !encode(&T.v[i], j.v, P.n_tok, P.H, dv) || !encode_out(&T.o[i], j.o, P.n_tok, P.H, dv))
             return cudaErrorInvalidValue;
     }
     if (dk == 128) return dv == 128 ? start_pass<128, 128>(T, n_jobs, s) : start_pass<128, 64>(T, n_jobs, s);
