@@ -48,7 +48,7 @@ struct DecayParams {
     const float* log_decay;
     const int32_t* cu;
     uint32_t* status;
-    int n_seq, n_tok, H, io, nseg, seg_len, pass, probe;   // pass: kWhole, kStates or kOutputs
+    int n_seq, n_tok, H, io, n_jobs, nseg, seg_len, pass, probe;   // pass: kWhole, kStates or kOutputs
 };
 enum { kWhole = 0, kStates = 1, kOutputs = 2 };
 

@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                    bar_w = bar_u1 + 8, bar_p = bar_w + 8, bar_s = bar_p + 8, bar_s_free = bar_s + 8, bar_o = bar_s_free + 8,
                    bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;   // bar_u1: the first 32 tokens
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int job = blockIdx.z, bh = blockIdx.x, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
+    // (the jobs of a head side by side: those of one direction read the same tokens at about the same time)
+    const int job = blockIdx.x % P.n_jobs, bh = blockIdx.x / P.n_jobs, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
     const DecayJob& J = P.job[job];
     const bool rev = J.reverse != 0;
 
@@ -730,7 +731,7 @@ template <int DK, int DV, bool OUT, int PARTS> cudaError_t start(const TcParams&
     constexpr int bytes = Layout<DK, DV, OUT>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<DK, DV, OUT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(T.d.n_seq * T.d.H, T.d.pass == kWhole ? 1 : T.d.nseg, n_jobs);
+    const dim3 grid(T.d.n_seq * T.d.H * n_jobs, T.d.pass == kWhole ? 1 : T.d.nseg);
     decay_tc_kernel<DK, DV, OUT, PARTS><<<grid, kThreads, bytes, s>>>(T);
     return cudaGetLastError();
 }
@@ -748,6 +749,7 @@ bool decay_tc_supported(int io, int dk, int dv) { return io == KDN_BF16 && (dk =
 cudaError_t launch_decay_tc(const DecayParams& P, int n_jobs, cudaStream_t s) {
     TcParams T;
     T.d = P;
+    T.d.n_jobs = n_jobs;
     const int dk = P.job[0].dk, dv = P.job[0].dv;
     for (int i = 0; i < n_jobs; ++i) {
         const DecayJob& j = P.job[i];

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kMost = 256, kV = 8;    // threads of a block; channels of a lane
 constexpr int kSMs = 152;             // GB300
+constexpr int kAt = 2;                // rows of a thread at a time
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct NormParams {
@@ -71,15 +72,20 @@ template <> struct Vec<float> {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// 1 / (1 + exp(-x)).  The fast exponential is off by |x| 2^-23 of its value, which is nothing beside a rounding to bf16.
+template <typename T> __device__ __forceinline__ float sigmoid(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.f + (sizeof(T) == 2 ? __expf(-x) : expf(-x))));
+    return y;
+}
 
 // The activation of x, and its slope.
-template <int ACT> __device__ __forceinline__ float act(float x, float& slope) {
+template <typename T, int ACT> __device__ __forceinline__ float act(float x, float& slope) {
     if (ACT == KDN_ACT_NONE) {
         slope = 1.f;
         return x;
     }
-    const float h = sigmoid(x);
+    const float h = sigmoid<T>(x);
     if (ACT == KDN_ACT_SIGMOID) {
         slope = h * (1.f - h);
         return h;
@@ -88,9 +94,14 @@ template <int ACT> __device__ __forceinline__ float act(float x, float& slope) {
     return x * h;
 }
 
-// Sum over the lanes of a group.
-__device__ __forceinline__ float group_sum(float x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+// Sum over the lanes of a group (LANES: how many, 0: `lanes`).
+template <int LANES> __device__ __forceinline__ float group_sum(float x, int lanes) {
+    if (LANES) {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    } else {
+        for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    }
     return x;
 }
 
@@ -111,7 +122,7 @@ __device__ __forceinline__ Place place_of(const NormParams& P) {
     return p;
 }
 
-template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMost) group_norm_kernel(const __grid_constant__ NormParams P) {
+template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost) group_norm_kernel(const __grid_constant__ NormParams P) {
     const NormArgs& A = P.a;
     const Place p = place_of(P);
     float w[kV], b[kV];
@@ -121,40 +132,50 @@ template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMos
         b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
     }
     const float inv = 1.f / A.d;
-    // (all lanes of a warp go on together: the sums are shuffles)
-    for (int row = p.row; __any_sync(kAll, row < A.rows); row += p.step) {
-        const bool mine = p.mine && row < A.rows;
-        float x[kV] = {};
-        Vec<T> gate;
-        if (mine) {
-            Vec<T> v;
-            v.load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
-            if (GATE) gate.load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
-            v.get(x);
-        }
-        float sum = 0.f, sq = 0.f;
+    // kAt rows at a time, their loads ahead of all else (all lanes of a warp go on together: the sums are shuffles)
+    for (int row = p.row; __any_sync(kAll, row < A.rows); row += kAt * p.step) {
+        Vec<T> v[kAt], gate[kAt];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum += x[i];
-        const float mean = group_sum(sum, P.lanes) * inv;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            x[i] -= mean;
-            sq = fmaf(x[i], x[i], sq);
+        for (int e = 0; e < kAt; ++e) {
+            const int r = row + e * p.step;
+            if (p.mine && r < A.rows) {
+                v[e].load(A.x.p, r * A.x.row + p.g * A.x.head + p.c);
+                if (GATE) gate[e].load(A.gate.p, r * A.gate.row + p.g * A.gate.head + p.c);
+            } else {
+                v[e] = Vec<T>{};
+            }
         }
-        const float rstd = rsqrtf(group_sum(mine ? sq : 0.f, P.lanes) * inv + A.eps);
-        if (!mine) continue;
-        float z[kV], slope;
-        if (GATE) gate.get(z);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float n = fmaf(x[i] * rstd, w[i], b[i]);
-            x[i] = GATE ? n * act<ACT>(z[i], slope) : act<ACT>(n, slope);
+        for (int e = 0; e < kAt; ++e) {
+            const int r = row + e * p.step;
+            const bool mine = p.mine && r < A.rows;
+            float x[kV];
+            v[e].get(x);
+            float sum = 0.f, sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) sum += x[i];
+            const float mean = group_sum<LANES>(sum, P.lanes) * inv;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                x[i] -= mean;
+                sq = fmaf(x[i], x[i], sq);
+            }
+            const float rstd = rsqrtf(group_sum<LANES>(mine ? sq : 0.f, P.lanes) * inv + A.eps);
+            if (mine) {
+                float z[kV], slope;
+                if (GATE) gate[e].get(z);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) {
+                    const float n = fmaf(x[i] * rstd, w[i], b[i]);
+                    x[i] = GATE ? n * act<T, ACT>(z[i], slope) : act<T, ACT>(n, slope);
+                }
+                Vec<T>::store(A.y, (static_cast<long long>(r) * A.groups + p.g) * A.d + p.c, x);
+            }
         }
-        Vec<T>::store(A.y, (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c, x);
     }
 }
 
-template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMost) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
+template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
     const NormArgs& A = P.a;
     const Place p = place_of(P);
     float w[kV], b[kV], dw[kV] = {}, db[kV] = {};
@@ -179,24 +200,24 @@ template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMos
         float sum = 0.f, sq = 0.f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) sum += x[i];
-        const float mean = group_sum(sum, P.lanes) * inv;
+        const float mean = group_sum<LANES>(sum, P.lanes) * inv;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             x[i] -= mean;
             sq = fmaf(x[i], x[i], sq);
         }
-        const float rstd = rsqrtf(group_sum(mine ? sq : 0.f, P.lanes) * inv + A.eps);
+        const float rstd = rsqrtf(group_sum<LANES>(mine ? sq : 0.f, P.lanes) * inv + A.eps);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const float xh = x[i] * rstd, n = fmaf(xh, w[i], b[i]);
             float slope, dn;
             if (GATE) {
-                const float f = act<ACT>(z[i], slope);
+                const float f = act<T, ACT>(z[i], slope);
                 z[i] = y[i] * n * slope;
                 dn = y[i] * f;
             } else {
-                act<ACT>(n, slope);
+                act<T, ACT>(n, slope);
                 dn = y[i] * slope;
             }
             if (mine) {
@@ -208,8 +229,8 @@ template <typename T, int ACT, bool GATE> __global__ void __launch_bounds__(kMos
             s1 += y[i];
             s2 = fmaf(y[i], xh, s2);
         }
-        s1 = group_sum(mine ? s1 : 0.f, P.lanes) * inv;
-        s2 = group_sum(mine ? s2 : 0.f, P.lanes) * inv;
+        s1 = group_sum<LANES>(mine ? s1 : 0.f, P.lanes) * inv;
+        s2 = group_sum<LANES>(mine ? s2 : 0.f, P.lanes) * inv;
         if (!mine) continue;
         const long long at = (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c;
 #pragma unroll
@@ -262,14 +283,26 @@ int blocks_x(const Shape& s, int rows, int per_sm) {
 }
 constexpr int kForwardBlocks = 6, kBackwardBlocks = 3;   // an SM
 
+template <typename T, int ACT, int LANES> void forward_lanes(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
+    if (P.a.gate.p) group_norm_kernel<T, ACT, true, LANES><<<grid, threads, 0, s>>>(P);
+    else group_norm_kernel<T, ACT, false, LANES><<<grid, threads, 0, s>>>(P);
+}
 template <typename T, int ACT> cudaError_t forward(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
-    if (P.a.gate.p) group_norm_kernel<T, ACT, true><<<grid, threads, 0, s>>>(P);
-    else group_norm_kernel<T, ACT, false><<<grid, threads, 0, s>>>(P);
+    // heads of 64 and of 128 (the number of lanes known: 8 and 4 fewer instructions a sum), others
+    if (P.lanes == 8) forward_lanes<T, ACT, 8>(P, grid, threads, s);
+    else if (P.lanes == 16) forward_lanes<T, ACT, 16>(P, grid, threads, s);
+    else forward_lanes<T, ACT, 0>(P, grid, threads, s);
     return cudaGetLastError();
 }
+template <typename T, int ACT, int LANES> void backward_lanes(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
+    if (P.a.gate.p) group_norm_backward_kernel<T, ACT, true, LANES><<<grid, threads, 0, s>>>(P);
+    else group_norm_backward_kernel<T, ACT, false, LANES><<<grid, threads, 0, s>>>(P);
+}
 template <typename T, int ACT> cudaError_t backward(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
-    if (P.a.gate.p) group_norm_backward_kernel<T, ACT, true><<<grid, threads, 0, s>>>(P);
-    else group_norm_backward_kernel<T, ACT, false><<<grid, threads, 0, s>>>(P);
+    // heads of 64 and of 128 (the number of lanes known: 8 and 4 fewer instructions a sum), others
+    if (P.lanes == 8) backward_lanes<T, ACT, 8>(P, grid, threads, s);
+    else if (P.lanes == 16) backward_lanes<T, ACT, 16>(P, grid, threads, s);
+    else backward_lanes<T, ACT, 0>(P, grid, threads, s);
     return cudaGetLastError();
 }
 
