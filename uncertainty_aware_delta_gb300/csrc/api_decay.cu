@@ -87,8 +87,7 @@ kdn_status kdn_decay_forward(int n_seq, int n_tok, int H, int dk, int dv, int io
                         {S0 == S_T ? nullptr : S0, states}};   // (states resumed in place are allowed)
     if ((st = check_alias(out, in)) != KDN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
-    if (!any) return KDN_OK;
+    if (!any) return done(cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s));
     return done(kdn::launch_decay(a, s));
 }
 
@@ -153,8 +152,7 @@ kdn_status kdn_decay_backward(int n_seq, int n_tok, int H, int dk, int dv, int i
     a.job[1] = {sv, so, sq, grad_k, dS_T, nullptr, dv, dk, 1, dv, 1};
     a.job[2] = {sk, sq, so, grad_v, dS_T, grad_S0, dk, dv, dv, 1, 1};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
-    if (!any) return KDN_OK;
+    if (!any) return done(cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s));
     return done(kdn::launch_decay(a, s));
 }
 
@@ -216,6 +214,7 @@ kdn_status kdn_group_norm_backward(int rows, int groups, int d, int act, float e
     a.w = weight; a.b = bias;
     a.dx = grad_x; a.dgate = gate ? grad_gate : nullptr;
     a.dw = weight ? grad_weight : nullptr; a.db = bias ? grad_bias : nullptr;
+    a.status = static_cast<uint32_t*>(workspace);
     a.scratch = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
     if (any) {
         if ((st = check_strided(&a.x, rows, groups, d, esz)) != KDN_OK) return st;
@@ -227,8 +226,8 @@ kdn_status kdn_group_norm_backward(int rows, int groups, int d, int act, float e
                         gate ? range_of(a.gate, rows, groups, d, esz) : Range{nullptr, 0}, {weight, params}, {bias, params}};
     if ((st = check_alias(out, in)) != KDN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
     if (!any) {   // sums of nothing
+        if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KDN_ERR_CUDA;
         if (params && a.dw && cudaMemsetAsync(a.dw, 0, params, s) != cudaSuccess) return KDN_ERR_CUDA;
         if (params && a.db && cudaMemsetAsync(a.db, 0, params, s) != cudaSuccess) return KDN_ERR_CUDA;
         return KDN_OK;

@@ -26,13 +26,19 @@ namespace {
 
 constexpr int kC = 32, kThreads = 256;   // tokens of a chunk; threads of a block
 constexpr int kSMs = 152;                // GB300
-constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ float4 load4(const void* p, long long i, int io) {
     if (io == KDN_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
     return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
                        __uint_as_float(x.y & 0xffff0000u));
+}
+
+// x = hi + lo, both TF32: hi rounded to nearest, the rest cut off (to 2^-22 of x, of either sign), by integer operations
+// where the conversion is a slow one.  A NaN stays one in lo, whatever the carry makes of it in hi; an infinity, too, leaves a NaN there.
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
 // A warp's 16 x 8 NT tile of A B in 3xTF32 (fragments: mma_tf32x3.cuh), the MMAs' sums taken over 32 of K and then in fp32
@@ -45,11 +51,9 @@ __device__ __forceinline__ void warp_product(float (&out)[NT][4], const float* A
     constexpr int kSpan = K < 32 ? K : 32;
 #pragma unroll 1
     for (int k0 = 0; k0 < K; k0 += kSpan) {
-        float acc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+        // (few tiles: a sum for each of the three products, as the MMAs of one sum wait for one another)
+        constexpr int kSums = NT <= 2 ? 3 : 1;
+        float acc[kSums][NT][4] = {};
 #pragma unroll
         for (int k = k0; k < k0 + kSpan; k += 8) {
             float a[4];
@@ -67,22 +71,22 @@ __device__ __forceinline__ void warp_product(float (&out)[NT][4], const float* A
             }
             uint32_t ah[4], al[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
+            for (int e = 0; e < 4; ++e) split(a[e], ah[e], al[e]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float* b = B + (k + q) * bk + (8 * n + g) * bc;
                 uint32_t bh0, bl0, bh1, bl1;
-                split_tf32(b[0], bh0, bl0);
-                split_tf32(b[4 * bk], bh1, bl1);
-                mma_m16n8k8_tf32(acc[n], al, bh0, bh1);
-                mma_m16n8k8_tf32(acc[n], ah, bl0, bl1);
-                mma_m16n8k8_tf32(acc[n], ah, bh0, bh1);
+                split(b[0], bh0, bl0);
+                split(b[4 * bk], bh1, bl1);
+                mma_m16n8k8_tf32(acc[kSums - 1][n], al, bh0, bh1);
+                mma_m16n8k8_tf32(acc[kSums / 2][n], ah, bl0, bl1);
+                mma_m16n8k8_tf32(acc[0][n], ah, bh0, bh1);
             }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[n][e] += acc[n][e];
+            for (int e = 0; e < 4; ++e) out[n][e] += kSums == 1 ? acc[0][n][e] : acc[0][n][e] + (acc[1][n][e] + acc[kSums - 1][n][e]);
     }
 }
 
@@ -101,6 +105,7 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
               seg = blockIdx.y, v0 = slice * DVS;
     int row0, len;
     if (!sequence(P, b, row0, len) && tid == 0 && blockIdx.x % P.H == 0) set_status(P.status, kStatusRange);
+    if (P.clear && tid == 0 && blockIdx.x + blockIdx.z == 0) *P.status = 0;   // (nothing else can be found then)
     const bool outputs = P.pass != kStates;
     if (P.pass != kWhole) {
         if (static_cast<long long>(seg) * P.seg_len >= len) return;
@@ -308,8 +313,10 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
 
 template <int DK, int DVS> cudaError_t start(const DecayParams& P, int n_jobs, cudaStream_t s) {
     constexpr int bytes = 4 * (2 * kC * (DK + 4) + (kC + DK) * (DVS + 8) + kC * (kC + 4));
-    const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
     decay_kernel<DK, DVS><<<dim3(P.n_seq * P.H * (P.job[0].dv / DVS), P.pass == kWhole ? 1 : P.nseg, n_jobs), kThreads, bytes, s>>>(P);
     return cudaGetLastError();
 }
@@ -331,15 +338,14 @@ cudaError_t start_path(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s
     }
 }
 cudaError_t start_pass(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s) {
-    bool same = true;
-    for (int i = 1; i < n_jobs; ++i) same = same && P.job[i].dk == P.job[0].dk && P.job[i].dv == P.job[0].dv;
-    if (same) return start_path(P, n_jobs, tc, s);
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < n_jobs && e == cudaSuccess; ++i) {
+    for (int i = 0, n; i < n_jobs && e == cudaSuccess; i += n) {
         DecayParams one = P;
-        one.job[0] = P.job[i];
-        one.states[0] = P.states[i];
-        e = start_path(one, 1, tc, s);
+        for (n = 0; i + n < n_jobs && P.job[i + n].dk == P.job[i].dk && P.job[i + n].dv == P.job[i].dv; ++n) {
+            one.job[n] = P.job[i + n];
+            one.states[n] = P.states[i + n];
+        }
+        e = start_path(one, n, tc, s);
     }
     return e;
 }
@@ -353,9 +359,11 @@ DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t 
     if ((flags & KDN_FLAG_NO_SPLIT) || n_seq <= 0 || n_tok <= 0 || H <= 0) return p;
     const bool tc = use_tc(io, dk, dv, flags);
     const int most = std::max(dk, dv);
-    const long long per = static_cast<long long>(H) * n_jobs * (tc ? 1 : (most + 63) / 64);   // blocks a segment
+    // blocks a segment in one launch (the gradients' jobs are two and one where dk and dv differ)
+    const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (most + 63) / 64);
     const long long room = (tc ? kSMs : 2 * kSMs) / per;                                      // segments in all
-    const int shortest = 512;
+    // a segment's two passes and the chaining have to be worth their launches, and what the tensor cores' blocks take to begin
+    const int shortest = tc ? 512 : 128;
     if (room < 2ll * n_seq) return p;
     const long long n = packed ? room - n_seq : room / n_seq, longest = packed ? n_tok : n_tok / n_seq;
     const long long len = std::max<long long>(shortest, ((longest + n - 1) / n + 63) / 64 * 64);
@@ -436,6 +444,12 @@ cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     P.nseg = plan.nseg; P.seg_len = plan.seg_len;
     P.probe = (a.flags & KDN_FLAG_TIMEOUT_PROBE) ? 1 : 0;
     P.pass = kWhole;
+    // the status word: where the first kernel cannot write it without a race, by a call of its own
+    P.clear = !a.cu && !tc && plan.nseg <= 1;
+    if (!P.clear) {
+        const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s);
+        if (e != cudaSuccess) return e;
+    }
     if (plan.nseg <= 1) return start_pass(P, a.n_jobs, tc, s);
     for (int i = 0; i < a.n_jobs; ++i) P.states[i] = a.scratch + static_cast<size_t>(i) * a.n_seq * a.H * plan.nseg * dk * dv;
     P.pass = kStates;

@@ -48,7 +48,7 @@ struct DecayParams {
     const float* log_decay;
     const int32_t* cu;
     uint32_t* status;
-    int n_seq, n_tok, H, io, n_jobs, nseg, seg_len, pass, probe;   // pass: kWhole, kStates or kOutputs
+    int n_seq, n_tok, H, io, n_jobs, nseg, seg_len, pass, probe, clear;   // pass: kWhole, kStates or kOutputs
 };
 enum { kWhole = 0, kStates = 1, kOutputs = 2 };
 
@@ -73,6 +73,7 @@ struct NormArgs {
     const float *w, *b;                      // [groups, d], or null
     void *y, *dx, *dgate;                    // dense
     float *dw, *db;                          // [groups, d]
+    uint32_t* status;                        // backward: there is nothing to report, 0
     float* scratch;                          // backward: norm_scratch() bytes
 };
 size_t norm_scratch(int rows, int groups, int d);

@@ -21,7 +21,10 @@ namespace {
 
 constexpr int kMost = 256, kV = 8;    // threads of a block; channels of a lane
 constexpr int kSMs = 152;             // GB300
-constexpr int kAt = 2;                // rows of a thread at a time
+// rows of a thread whose loads are under way: forward (together), backward (while one is worked on)
+template <typename T> constexpr int kAt = sizeof(T) == 2 ? 4 : 2;
+template <typename T> constexpr int kNext = sizeof(T) == 2 ? 2 : 1;
+constexpr int kForwardBlocks = 3, kBackwardBlocks = 2;   // an SM
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct NormParams {
@@ -133,10 +136,10 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     }
     const float inv = 1.f / A.d;
     // kAt rows at a time, their loads ahead of all else (all lanes of a warp go on together: the sums are shuffles)
-    for (int row = p.row; __any_sync(kAll, row < A.rows); row += kAt * p.step) {
-        Vec<T> v[kAt], gate[kAt];
+    for (int row = p.row; __any_sync(kAll, row < A.rows); row += kAt<T> * p.step) {
+        Vec<T> v[kAt<T>], gate[kAt<T>];
 #pragma unroll
-        for (int e = 0; e < kAt; ++e) {
+        for (int e = 0; e < kAt<T>; ++e) {
             const int r = row + e * p.step;
             if (p.mine && r < A.rows) {
                 v[e].load(A.x.p, r * A.x.row + p.g * A.x.head + p.c);
@@ -146,7 +149,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
             }
         }
 #pragma unroll
-        for (int e = 0; e < kAt; ++e) {
+        for (int e = 0; e < kAt<T>; ++e) {
             const int r = row + e * p.step;
             const bool mine = p.mine && r < A.rows;
             float x[kV];
@@ -175,9 +178,10 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     }
 }
 
-template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
+template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost, kBackwardBlocks) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
     const NormArgs& A = P.a;
     const Place p = place_of(P);
+    if (blockIdx.x + blockIdx.y + threadIdx.x == 0) *A.status = 0;
     float w[kV], b[kV], dw[kV] = {}, db[kV] = {};
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
@@ -185,18 +189,27 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
         b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
     }
     const float inv = 1.f / A.d;
-    for (int row = p.row; __any_sync(kAll, row < A.rows); row += p.step) {
-        const bool mine = p.mine && row < A.rows;
-        float x[kV] = {}, y[kV] = {}, z[kV] = {};
-        if (mine) {
-            Vec<T> v, u, t;
-            v.load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
-            u.load(A.dy.p, row * A.dy.row + p.g * A.dy.head + p.c);
-            if (GATE) t.load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
-            v.get(x);
-            u.get(y);
-            if (GATE) t.get(z);
+    // the next kNext rows' loads are under way while a row is worked on
+    Vec<T> v[kNext<T>] = {}, u[kNext<T>] = {}, t[kNext<T>] = {};
+    auto fetch = [&](int row, int e) {
+        if (p.mine && row < A.rows) {
+            v[e].load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
+            u[e].load(A.dy.p, row * A.dy.row + p.g * A.dy.head + p.c);
+            if (GATE) t[e].load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
         }
+    };
+#pragma unroll
+    for (int e = 0; e < kNext<T>; ++e) fetch(p.row + e * p.step, e);
+    for (int row0 = p.row; __any_sync(kAll, row0 < A.rows); row0 += kNext<T> * p.step)
+#pragma unroll
+    for (int e = 0; e < kNext<T>; ++e) {
+        const int row = row0 + e * p.step;
+        const bool mine = p.mine && row < A.rows;
+        float x[kV], y[kV], z[kV];
+        v[e].get(x);
+        u[e].get(y);
+        if (GATE) t[e].get(z);
+        fetch(row + kNext<T> * p.step, e);
         float sum = 0.f, sq = 0.f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) sum += x[i];
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(kMost) group_norm_join_kernel(const __grid_con
     const float* part = P.a.scratch + static_cast<size_t>(blockIdx.y) * P.parts * n;
     float sum = 0.f;
     if (c < n)
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < P.parts; i += 8) sum += part[static_cast<size_t>(i) * n + c];
     sums[warp][lane] = sum;
     __syncthreads();
@@ -277,11 +290,12 @@ Shape shape_of(int groups, int d) {
     s.threads = (s.rows * s.groups * s.lanes + 31) / 32 * 32;
     return s;
 }
-int blocks_x(const Shape& s, int rows, int per_sm) {
+// Blocks for `each` rows of a thread at least (what more of them would save, the sum of their parts costs), but for 64 of them.
+int blocks_x(const Shape& s, int rows, int per_sm, int each) {
     const long long want = (static_cast<long long>(rows) + s.rows - 1) / s.rows, room = std::max(1, per_sm * kSMs / s.blocks_y);
-    return static_cast<int>(std::min(want, room));
+    return static_cast<int>(std::min(std::min(want, room), std::max(64ll, want / each)));
 }
-constexpr int kForwardBlocks = 6, kBackwardBlocks = 3;   // an SM
+constexpr int kBackwardRows = 8;      // of a thread
 
 template <typename T, int ACT, int LANES> void forward_lanes(const NormParams& P, dim3 grid, int threads, cudaStream_t s) {
     if (P.a.gate.p) group_norm_kernel<T, ACT, true, LANES><<<grid, threads, 0, s>>>(P);
@@ -318,13 +332,13 @@ NormParams params_of(const NormArgs& a, const Shape& s) {
 size_t norm_scratch(int rows, int groups, int d) {
     if (rows <= 0 || groups <= 0) return 0;
     const Shape s = shape_of(groups, d);
-    return 2 * sizeof(float) * static_cast<size_t>(blocks_x(s, rows, kBackwardBlocks)) * s.rows * groups * d;
+    return 2 * sizeof(float) * static_cast<size_t>(blocks_x(s, rows, kBackwardBlocks, kBackwardRows)) * s.rows * groups * d;
 }
 
 cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t s) {
     const Shape sh = shape_of(a.groups, a.d);
     const NormParams P = params_of(a, sh);
-    const dim3 grid(blocks_x(sh, a.rows, kForwardBlocks), sh.blocks_y);
+    const dim3 grid(blocks_x(sh, a.rows, kForwardBlocks, 1), sh.blocks_y);
     const auto run = [&](auto type) {
         using T = decltype(type);
         if (a.act == KDN_ACT_NONE) return forward<T, KDN_ACT_NONE>(P, grid, sh.threads, s);
@@ -337,7 +351,7 @@ cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t s) {
 cudaError_t launch_group_norm_backward(const NormArgs& a, cudaStream_t s) {
     const Shape sh = shape_of(a.groups, a.d);
     NormParams P = params_of(a, sh);
-    const dim3 grid(blocks_x(sh, a.rows, kBackwardBlocks), sh.blocks_y);
+    const dim3 grid(blocks_x(sh, a.rows, kBackwardBlocks, kBackwardRows), sh.blocks_y);
     P.parts = grid.x * sh.rows;
     const auto run = [&](auto type) {
         using T = decltype(type);

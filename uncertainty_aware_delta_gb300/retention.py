@@ -6,22 +6,35 @@ from __future__ import annotations
 
 import torch
 
-from .attention import _call, _int, _io, _rows, _tensor, _workspace
+from .attention import _call, _int, _io, _refuse, _tensor, _workspace
 from .binding import KDN_BF16, library
 
 _ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 
 
 def _tokens(t, name):
-    """[B, T, heads, d] as [B T, heads, d] (strides kept), [tokens, heads, d] as it is."""
+    """Tokens, heads and channels of [B, T, heads, d] or [tokens, heads, d]."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
         raise ValueError(f"{name} must be a tensor [B, T, heads, d] or [tokens, heads, d]")
-    if t.dim() == 3:
-        return t
-    try:
-        return t.view(t.shape[0] * t.shape[1], t.shape[2], t.shape[3])
-    except RuntimeError:
-        raise ValueError(f"the sequences of {name} must lie one after another") from None
+    s = t.shape
+    return (s[0] * s[1], s[2], s[3]) if len(s) == 4 else (s[0], s[1], s[2])
+
+
+def _operand(t, name, dtype, shape, device):
+    """Pointer, row stride and head stride of a [B, T, heads, d] or [tokens, heads, d] operand of this shape (no view of it is
+    made: that would take longer than the checks)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape:
+        if len(shape) == 3:
+            row, head, one = t.stride()
+        else:
+            seq, row, head, one = t.stride()
+            if shape[1] == 1:
+                row = seq
+            elif shape[0] > 1 and seq != row * shape[1] and t.numel():
+                raise ValueError(f"the sequences of {name} must lie one after another")
+        if one == 1 or shape[-1] <= 1 or t.numel() == 0:
+            return t.data_ptr(), row, head
+    _refuse(t, name, dtype, shape, device, False)
 
 
 def _maybe(t, name, dtype, shape, device):
@@ -58,22 +71,22 @@ def kdn_decay_forward(q, k, v, log_decay, S0=None, *, cu=None, flags=0, out=None
     log_decay [H], S0 and S_T [sequences, H, dk, dv] fp32.  ``out=(o, S_T)`` writes into tensors (S_T may be S0).
     """
     lib = library()
-    shape, device, io, flags = v.shape, q.device, _io(q, "q"), _int(flags, "flags")
+    device, io, flags = q.device, _io(q, "q"), _int(flags, "flags")
+    tok, H, dk = _tokens(q, "q")
     n, cu_ptr = _sequences(q, cu, device)
-    q, k, v = _tokens(q, "q"), _tokens(k, "k"), _tokens(v, "v")
-    tok, H, dk = q.shape
-    tok, dv, f32 = _int(tok, "tokens"), v.shape[-1], torch.float32
+    keys, dv, f32 = q.shape, v.shape[-1], torch.float32
+    shape, tok, dt = (*keys[:-1], dv), _int(tok, "tokens"), q.dtype
     made = []
     if out is None:
-        made = [torch.empty(shape, dtype=q.dtype, device=device), torch.empty((n, H, dk, dv), dtype=f32, device=device)]
+        made = [torch.empty(shape, dtype=dt, device=device), torch.empty((n, H, dk, dv), dtype=f32, device=device)]
         out = tuple(made)
     o, S_T = out
     need = lib.kdn_decay_workspace_size(n, tok, H, dk, dv, io, flags)
     ws, ws_bytes = _workspace(workspace, need, device, made)
     _call(lib.kdn_decay_forward, device, stream,
-          (n, tok, H, dk, dv, io, flags, *_rows(q, "q", q.dtype, (tok, H, dk), device), *_rows(k, "k", q.dtype, (tok, H, dk), device),
-           *_rows(v, "v", q.dtype, (tok, H, dv), device), _tensor(log_decay, "log_decay", f32, (H,), device),
-           _maybe(S0, "S0", f32, (n, H, dk, dv), device), cu_ptr, _tensor(o, "o", q.dtype, shape, device),
+          (n, tok, H, dk, dv, io, flags, *_operand(q, "q", dt, keys, device), *_operand(k, "k", dt, keys, device),
+           *_operand(v, "v", dt, shape, device), _tensor(log_decay, "log_decay", f32, (H,), device),
+           _maybe(S0, "S0", f32, (n, H, dk, dv), device), cu_ptr, _tensor(o, "o", dt, shape, device),
            _tensor(S_T, "S_T", f32, (n, H, dk, dv), device), ws, ws_bytes), made)
     return o, S_T
 
@@ -99,21 +112,20 @@ def kdn_decay_backward(q, k, v, log_decay, S0=None, dO=None, dS_T=None, *, cu=No
     the type of the inputs) and S0 (fp32)."""
     lib = library()
     device, io, flags = q.device, _io(q, "q"), _int(flags, "flags")
-    shapes = {"q": q.shape, "k": k.shape, "v": v.shape}
+    tok, H, dk = _tokens(q, "q")
     n, cu_ptr = _sequences(q, cu, device)
-    q, k, v, dO = _tokens(q, "q"), _tokens(k, "k"), _tokens(v, "v"), _tokens(dO, "dO")
-    tok, H, dk = q.shape
-    tok, dv, f32 = _int(tok, "tokens"), v.shape[-1], torch.float32
+    keys, dv, f32 = q.shape, v.shape[-1], torch.float32
+    values, tok, dt = (*keys[:-1], dv), _int(tok, "tokens"), q.dtype
     states = (n, H, dk, dv)
-    grads = {name: torch.empty(shape, dtype=q.dtype, device=device) for name, shape in shapes.items()}
+    grads = {name: torch.empty(shape, dtype=dt, device=device) for name, shape in (("q", keys), ("k", keys), ("v", values))}
     grads["S0"] = torch.empty(states, dtype=f32, device=device)
     made = list(grads.values())
     need = lib.kdn_decay_backward_workspace_size(n, tok, H, dk, dv, io, flags)
     ws, ws_bytes = _workspace(workspace, need, device, made)
     _call(lib.kdn_decay_backward, device, stream,
-          (n, tok, H, dk, dv, io, flags, *_rows(q, "q", q.dtype, (tok, H, dk), device), *_rows(k, "k", q.dtype, (tok, H, dk), device),
-           *_rows(v, "v", q.dtype, (tok, H, dv), device), _tensor(log_decay, "log_decay", f32, (H,), device),
-           _maybe(S0, "S0", f32, states, device), cu_ptr, *_rows(dO, "dO", q.dtype, (tok, H, dv), device),
+          (n, tok, H, dk, dv, io, flags, *_operand(q, "q", dt, keys, device), *_operand(k, "k", dt, keys, device),
+           *_operand(v, "v", dt, values, device), _tensor(log_decay, "log_decay", f32, (H,), device),
+           _maybe(S0, "S0", f32, states, device), cu_ptr, *_operand(dO, "dO", dt, values, device),
            _maybe(dS_T, "dS_T", f32, states, device), *(grads[name].data_ptr() for name in ("q", "k", "v", "S0")), ws, ws_bytes), made)
     return grads
 
@@ -130,15 +142,14 @@ def kdn_group_norm(x, weight=None, bias=None, *, gate=None, act="none", eps=1e-5
     x, gate [rows, groups, d] or [B, T, groups, d] fp32 or bf16; weight, bias [groups, d] fp32; act "none", "silu" or "sigmoid".
     """
     shape, device, io, kind = x.shape, x.device, _io(x, "x"), _activation(act)
-    x = _tokens(x, "x")
-    rows, G, d = x.shape
+    rows, G, d = _tokens(x, "x")
     made = []
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=device)
         made.append(out)
-    gates = (None, 0, 0) if gate is None else _rows(_tokens(gate, "gate"), "gate", x.dtype, (rows, G, d), device)
+    gates = (None, 0, 0) if gate is None else _operand(gate, "gate", x.dtype, shape, device)
     _call(library().kdn_group_norm, device, stream,
-          (_int(rows, "rows"), G, d, kind, eps, io, *_rows(x, "x", x.dtype, (rows, G, d), device),
+          (_int(rows, "rows"), G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
            _maybe(weight, "weight", torch.float32, (G, d), device), _maybe(bias, "bias", torch.float32, (G, d), device), *gates,
            _tensor(out, "out", x.dtype, shape, device)), made)
     return out
@@ -153,19 +164,18 @@ def kdn_group_norm_backward(x, dy, weight=None, bias=None, *, gate=None, act="no
     inputs), weight, bias (fp32); None for what was not given."""
     lib = library()
     shape, device, io, kind = x.shape, x.device, _io(x, "x"), _activation(act)
-    x, dy = _tokens(x, "x"), _tokens(dy, "dy")
-    rows, G, d = x.shape
+    rows, G, d = _tokens(x, "x")
     f32 = dict(dtype=torch.float32, device=device)
     grads = {"x": torch.empty(shape, dtype=x.dtype, device=device),
              "gate": None if gate is None else torch.empty(shape, dtype=x.dtype, device=device),
              "weight": None if weight is None else torch.empty((G, d), **f32),
              "bias": None if bias is None else torch.empty((G, d), **f32)}
     made = [t for t in grads.values() if t is not None]
-    gates = (None, 0, 0) if gate is None else _rows(_tokens(gate, "gate"), "gate", x.dtype, (rows, G, d), device)
+    gates = (None, 0, 0) if gate is None else _operand(gate, "gate", x.dtype, shape, device)
     ws, ws_bytes = _workspace(workspace, lib.kdn_group_norm_backward_workspace_size(_int(rows, "rows"), G, d, io), device, made)
     _call(lib.kdn_group_norm_backward, device, stream,
-          (rows, G, d, kind, eps, io, *_rows(x, "x", x.dtype, (rows, G, d), device),
+          (rows, G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
            _maybe(weight, "weight", torch.float32, (G, d), device), _maybe(bias, "bias", torch.float32, (G, d), device), *gates,
-           *_rows(dy, "dy", x.dtype, (rows, G, d), device),
+           *_operand(dy, "dy", x.dtype, shape, device),
            *(None if grads[name] is None else grads[name].data_ptr() for name in ("x", "gate", "weight", "bias")), ws, ws_bytes), made)
     return grads
