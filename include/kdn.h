@@ -456,8 +456,8 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *   - Sequences are dense (cu NULL: n_tok / n_seq tokens each, one after another, which is
  *     [B, T, H, d]) or packed: sequence s has the rows cu[s] .. cu[s + 1].  cu [n_seq + 1] is
  *     device data: a sequence whose bounds run backwards or outside n_tok is taken as empty, and
- *     KDN_ERR_RANGE is recorded.  Rows of no sequence are left unwritten; rows that
- *     then lie in two hold the outputs of either.
+ *     KDN_ERR_RANGE is recorded.  Rows of no sequence are left unwritten; what shares
+ *     rows with it is then not defined.
  *   - States are [n_seq, H, dk, dv] fp32.
  *   - A value that is not finite makes the outputs that depend on it not finite (infinities
  *     may become NaN) and no others: not those of earlier tokens, of other heads or sequences.
@@ -480,8 +480,8 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *          (products in 3xTF32).  On tcgen05 the weights g^(i-j) (q_i k_j) and the state that a chunk
  *          begins with are rounded to bf16 for their products with v and q; what is added to the
  *          state is not (g^(m-1-j) v_j goes in as three bf16 parts), and the state itself is fp32.
- *          Few sequences' heads are cut into segments that run side by side, as those of the mixer's
- *          forward (KDN_FLAG_NO_SPLIT: they are not).
+ *          Few sequences' heads, and packed sequences much longer than the others, are cut into segments
+ *          that run side by side, as those of the mixer's forward (KDN_FLAG_NO_SPLIT: they are not).
  * Workspace: kdn_decay_workspace_size() bytes; its first 256 hold the status word.
  */
 size_t kdn_decay_workspace_size(int n_seq, int n_tok, int H, int dk, int dv, int io_dtype, uint32_t flags);

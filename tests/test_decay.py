@@ -67,6 +67,31 @@ def test_segments(io, dk, dv, packed):
     check_all([1400, 700] if packed else [1400], 1, dk, dv, io, packed)
 
 
+@pytest.mark.parametrize("io,dk,dv", [("f32", 32, 64), ("bf16", 64, 64), ("bf16", 128, 64)])
+def test_long_sequences_among_short_ones(io, dk, dv):
+    """Packed: only the long ones are cut into segments (more than 32 sequences: the forward alone)."""
+    lengths = [3, 40, 0, 1700, 64, 1] + [17 + 9 * (i % 4) for i in range(5)] + [1000, 65, 0]
+    check_all(lengths, 1, dk, dv, io, True)
+    check_all(lengths + [30] * 24, 1, dk, dv, io, True)
+
+
+def test_bounds_out_of_order_with_segments():
+    """More segments than there is room for: nothing outside is written, the status word says so."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    n, H, d = 40, 1, 64
+    x = inputs([1600] + [20] * 39, H, d, d, "bf16", True)
+    tok = x["q"].shape[0]
+    cu = torch.tensor([0 if i % 2 == 0 else tok for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    need = kdn.decay_workspace_size(n, tok, H, d, d, 1)
+    assert need > 4096
+    room = torch.full((need + 65536,), 7, dtype=torch.uint8, device="cuda")
+    o, S = torch.full((tok + 64, H, d), 7, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x["S0"])
+    kdn.kdn_decay_forward(x["q"], x["k"], x["v"], x["log_decay"], x["S0"], cu=cu, out=(o[:tok], S), workspace=room[:need])
+    assert kdn.kdn_read_device_status(room) == 9
+    assert bool((room[need:] == 7).all()) and bool((o[tok:] == 7).all())
+
+
 @pytest.mark.parametrize("io,d", [("f32", 32), ("bf16", 128)])
 @pytest.mark.parametrize("log_decay", [0.0, -1e-6, -30.0, -float("inf")])
 def test_extreme_decays(io, d, log_decay):

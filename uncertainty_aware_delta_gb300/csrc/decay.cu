@@ -101,17 +101,14 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
     __shared__ int bad_at[DVS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const DecayJob& J = P.job[blockIdx.z];
-    const int slices = J.dv / DVS, slice = blockIdx.x % slices, bh = blockIdx.x / slices, b = bh / P.H, h = bh % P.H,
-              seg = blockIdx.y, v0 = slice * DVS;
-    int row0, len;
-    if (!sequence(P, b, row0, len) && tid == 0 && blockIdx.x % P.H == 0) set_status(P.status, kStatusRange);
+    const int slices = J.dv / DVS, slice = blockIdx.x % slices, item = blockIdx.x / slices / P.H, h = blockIdx.x / slices % P.H,
+              v0 = slice * DVS;
+    const DecayItem it = find_item(P, item, tid < 32 && h == 0);
     if (P.clear && tid == 0 && blockIdx.x + blockIdx.z == 0) *P.status = 0;   // (nothing else can be found then)
+    if (!it.any) return;
     const bool outputs = P.pass != kStates;
-    if (P.pass != kWhole) {
-        if (static_cast<long long>(seg) * P.seg_len >= len) return;
-        row0 += seg * P.seg_len;
-        len = min(len - seg * P.seg_len, P.seg_len);
-    }
+    const int row0 = it.row, len = it.len;
+    const size_t bh = static_cast<size_t>(it.b) * P.H + h;
     const float l = P.log_decay[h];
     if (tid <= kC) pw[tid] = power(l, tid);
 
@@ -123,11 +120,11 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
     const float* in = nullptr;
     float* end = nullptr;
     int i_k = J.s_k, i_v = J.s_v, o_k = J.s_k, o_v = J.s_v;
-    if (P.pass == kWhole) {
+    if (it.slot < 0) {
         in = J.S0 ? J.S0 + bh * elems : nullptr;
         end = J.S_T ? J.S_T + bh * elems : nullptr;
     } else {
-        float* st = P.states[blockIdx.z] + (static_cast<size_t>(bh) * P.nseg + seg) * elems;
+        float* st = P.states[blockIdx.z] + (static_cast<size_t>(it.slot) * P.H + h) * elems;
         i_k = o_k = J.dv;
         i_v = o_v = 1;
         if (P.pass == kStates) end = st;
@@ -288,27 +285,47 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
             }
 }
 
-// Segments' own states -> the states that they begin with, and the last one: an element a thread.
+// Segments' own states -> the states that they begin with, and the last one: a few elements a thread.
+constexpr int kChainElems = 4;
 __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_constant__ DecayParams P) {
     const DecayJob& J = P.job[blockIdx.z];
-    const int elems = J.dk * J.dv, e = blockIdx.x * kThreads + threadIdx.x, bh = blockIdx.y, b = bh / P.H;
-    if (e >= elems) return;
-    int row0, len;
+    const int elems = J.dk * J.dv, b = blockIdx.y / P.H, h = blockIdx.y % P.H;
+    int row0, len, first = b * P.nseg;
     sequence(P, b, row0, len);
-    const float l = P.log_decay[bh % P.H], full = power(l, P.seg_len);
-    const size_t at = static_cast<size_t>(bh) * elems + static_cast<size_t>(e / J.dv) * J.s_k + static_cast<size_t>(e % J.dv) * J.s_v;
-    float* st = P.states[blockIdx.z] + static_cast<size_t>(bh) * P.nseg * elems + e;
-    float S = J.S0 ? J.S0[at] : 0.f;
-    const int n = (len + P.seg_len - 1) / P.seg_len;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const int seg = J.reverse ? n - 1 - i : i;
-        float* p = st + static_cast<size_t>(seg) * elems;
-        const float own = *p;
-        *p = S;
-        S = fmaf(seg == n - 1 ? power(l, len - seg * P.seg_len) : full, S, own);
+    if (P.cu) {
+        if (len <= P.seg_len) return;
+        first = packed_item(P, ~b, false).slot;
+        if (first + segments(len, P.seg_len) > P.slots) return;   // (bounds that run backwards)
     }
-    if (J.S_T) J.S_T[at] = S;
+    const float l = P.log_decay[h], full = power(l, P.seg_len);
+    const int n = segments(len, P.seg_len);
+    const float last = power(l, len - (n - 1) * P.seg_len);
+    const size_t step = static_cast<size_t>(P.H) * elems;
+#pragma unroll 1
+    for (int y = 0; y < kChainElems; ++y) {
+        const int e = (blockIdx.x * kChainElems + y) * kThreads + threadIdx.x;
+        if (e >= elems) break;
+        const size_t at = static_cast<size_t>(blockIdx.y) * elems + static_cast<size_t>(e / J.dv) * J.s_k + static_cast<size_t>(e % J.dv) * J.s_v;
+        float* st = P.states[blockIdx.z] + (static_cast<size_t>(first) * P.H + h) * elems + e;
+        float S = J.S0 ? J.S0[at] : 0.f;
+        // (kBatch segments' loads at a time: one by one, nine segments took 30 us)
+        constexpr int kBatch = 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float own[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (i0 + i < n) own[i] = st[(J.reverse ? n - 1 - i0 - i : i0 + i) * step];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i0 + i >= n) break;
+                const int seg = J.reverse ? n - 1 - i0 - i : i0 + i;
+                st[seg * step] = S;
+                S = fmaf(seg == n - 1 ? last : full, S, own[i]);
+            }
+        }
+        if (J.S_T) J.S_T[at] = S;
+    }
 }
 
 template <int DK, int DVS> cudaError_t start(const DecayParams& P, int n_jobs, cudaStream_t s) {
@@ -317,7 +334,7 @@ template <int DK, int DVS> cudaError_t start(const DecayParams& P, int n_jobs, c
         const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    decay_kernel<DK, DVS><<<dim3(P.n_seq * P.H * (P.job[0].dv / DVS), P.pass == kWhole ? 1 : P.nseg, n_jobs), kThreads, bytes, s>>>(P);
+    decay_kernel<DK, DVS><<<dim3(P.items * P.H * (P.job[0].dv / DVS), 1, n_jobs), kThreads, bytes, s>>>(P);
     return cudaGetLastError();
 }
 
@@ -352,24 +369,32 @@ cudaError_t start_pass(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s
 
 bool use_tc(int io, int dk, int dv, uint32_t flags) { return !(flags & KDN_FLAG_PORTABLE) && decay_tc_supported(io, dk, dv); }
 
-// Few sequences' heads are cut into segments until there are blocks for all SMs.  A segment has a whole number of chunks of
-// both paths.
+// Sequences are cut where there are at most half as many of them as blocks that run at a time.  (Packed ones may be of any
+// lengths, and a long one among many is worked on alone in the end: 24 of 2 to 4095 tokens, 16 heads of 64, take 95 us, of
+// which the longest alone is 90.  Cut into segments of an SM's share of all tokens they took 119: 27 more for the states, 11 for
+// the chaining, and the outputs still 75, as every block has some 5 us before its first chunk is through.)  A segment has
+// a whole number of chunks of both paths.
 DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
-    DecayPlan p = {1, 0};
+    DecayPlan p = {false, 0, 1, n_seq, 0};
     if ((flags & KDN_FLAG_NO_SPLIT) || n_seq <= 0 || n_tok <= 0 || H <= 0) return p;
     const bool tc = use_tc(io, dk, dv, flags);
     const int most = std::max(dk, dv);
-    // blocks a segment in one launch (the gradients' jobs are two and one where dk and dv differ)
-    const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (most + 63) / 64);
-    const long long room = (tc ? kSMs : 2 * kSMs) / per;                                      // segments in all
+    // blocks a segment in one launch (the gradients' jobs are two and one where dk and dv differ), and that run at a time
+    const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (most + 63) / 64),
+                    room = tc ? kSMs : 2 * kSMs, longest = packed ? n_tok : n_tok / n_seq;
     // a segment's two passes and the chaining have to be worth their launches, and what the tensor cores' blocks take to begin
     const int shortest = tc ? 512 : 128;
-    if (room < 2ll * n_seq) return p;
-    const long long n = packed ? room - n_seq : room / n_seq, longest = packed ? n_tok : n_tok / n_seq;
-    const long long len = std::max<long long>(shortest, ((longest + n - 1) / n + 63) / 64 * 64);
+    if (2 * per * n_seq > room) return p;
+    const long long n = packed ? room / per - n_seq : room / per / n_seq;
+    long long len = (longest + n - 1) / n;   // of a segment
+    len = std::max<long long>(shortest, (len + 63) / 64 * 64);
     if (len >= longest) return p;
+    p.split = true;
     p.seg_len = static_cast<int>(len);
     p.nseg = static_cast<int>((longest + len - 1) / len);
+    // (packed: a sequence has at most len / seg_len + 1 segments, and only one longer than seg_len more than one)
+    p.items = packed ? static_cast<int>(n_tok / len) + n_seq : n_seq * p.nseg;
+    p.slots = packed ? static_cast<int>(n_tok / len + std::min<long long>(n_tok / len, n_seq)) : p.items;
     return p;
 }
 
@@ -430,7 +455,7 @@ decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __r
 
 size_t decay_scratch(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
     const DecayPlan p = plan_of(n_seq, n_tok, H, dk, dv, io, flags, packed, n_jobs);
-    return p.nseg > 1 ? static_cast<size_t>(n_jobs) * n_seq * H * p.nseg * dk * dv * sizeof(float) : 0;
+    return static_cast<size_t>(n_jobs) * p.slots * H * dk * dv * sizeof(float);
 }
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
@@ -438,27 +463,27 @@ cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     const bool tc = use_tc(a.io, dk, dv, a.flags) && a.n_tok > 0;
     const DecayPlan plan = plan_of(a.n_seq, a.n_tok, a.H, dk, dv, a.io, a.flags, a.cu != nullptr, a.n_jobs);
     DecayParams P = {};
-    for (int i = 0; i < a.n_jobs; ++i) P.job[i] = a.job[i];
+    for (int i = 0; i < a.n_jobs; ++i) {
+        P.job[i] = a.job[i];
+        P.states[i] = a.scratch + static_cast<size_t>(i) * plan.slots * a.H * dk * dv;
+    }
     P.log_decay = a.log_decay; P.cu = a.cu; P.status = a.status;
     P.n_seq = a.n_seq; P.n_tok = a.n_tok; P.H = a.H; P.io = a.io;
-    P.nseg = plan.nseg; P.seg_len = plan.seg_len;
+    P.nseg = plan.nseg; P.seg_len = plan.seg_len; P.slots = plan.slots;
     P.probe = (a.flags & KDN_FLAG_TIMEOUT_PROBE) ? 1 : 0;
-    P.pass = kWhole;
     // the status word: where the first kernel cannot write it without a race, by a call of its own
-    P.clear = !a.cu && !tc && plan.nseg <= 1;
-    if (!P.clear) {
-        const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s);
-        if (e != cudaSuccess) return e;
+    P.clear = !a.cu && !tc && !plan.split;
+    cudaError_t e = cudaSuccess;
+    if (!P.clear && (e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
+    if (plan.split) {
+        P.pass = kStates;
+        P.items = plan.slots;
+        if ((e = start_pass(P, a.n_jobs, tc, s)) != cudaSuccess) return e;
+        decay_chain_kernel<<<dim3((dk * dv + kChainElems * kThreads - 1) / (kChainElems * kThreads), a.n_seq * a.H, a.n_jobs), kThreads, 0, s>>>(P);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (plan.nseg <= 1) return start_pass(P, a.n_jobs, tc, s);
-    for (int i = 0; i < a.n_jobs; ++i) P.states[i] = a.scratch + static_cast<size_t>(i) * a.n_seq * a.H * plan.nseg * dk * dv;
-    P.pass = kStates;
-    cudaError_t e = start_pass(P, a.n_jobs, tc, s);
-    if (e != cudaSuccess) return e;
-    decay_chain_kernel<<<dim3((dk * dv + kThreads - 1) / kThreads, a.n_seq * a.H, a.n_jobs), kThreads, 0, s>>>(P);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    P.pass = kOutputs;
+    P.pass = plan.split ? kOutputs : kWhole;
+    P.items = plan.items;
     return start_pass(P, a.n_jobs, tc, s);
 }
 

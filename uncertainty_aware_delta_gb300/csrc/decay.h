@@ -22,10 +22,13 @@ struct DecayJob {
 };
 constexpr int kMaxDecayJobs = 3;
 
-// Segments of a sequence that run side by side: one pass gives the states that they end with from zero, a short one chains
-// them, and a last one gives the outputs.
+// Segments of sequences that run side by side: one pass gives the states that they end with from zero, a short one chains
+// them, and a last one gives the outputs.  Dense sequences all have the same segments.  Of packed ones those longer than
+// seg_len are cut (the lengths are known on the device alone), the others run whole in the last pass.
 struct DecayPlan {
-    int nseg, seg_len;       // of the longest sequence there can be; nseg == 1: no split
+    bool split;
+    int seg_len, nseg;       // nseg: of a dense sequence
+    int items, slots;        // blocks a head in the last pass, at most; segments that have a state
 };
 
 struct DecayArgs {
@@ -44,11 +47,11 @@ cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s);
 // What a pass's kernel takes.
 struct DecayParams {
     DecayJob job[kMaxDecayJobs];
-    float* states[kMaxDecayJobs];            // [n_seq, H, nseg, dk, dv] of the job
+    float* states[kMaxDecayJobs];            // [slots, H, dk, dv] of the job
     const float* log_decay;
     const int32_t* cu;
     uint32_t* status;
-    int n_seq, n_tok, H, io, n_jobs, nseg, seg_len, pass, probe, clear;   // pass: kWhole, kStates or kOutputs
+    int n_seq, n_tok, H, io, n_jobs, nseg, seg_len, items, slots, pass, probe, clear;   // pass: kWhole, kStates or kOutputs
 };
 enum { kWhole = 0, kStates = 1, kOutputs = 2 };
 

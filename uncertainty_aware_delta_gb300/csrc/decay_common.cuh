@@ -3,6 +3,7 @@
 
 #include <math.h>
 
+#include "common.cuh"
 #include "decay.h"
 
 namespace kdn {
@@ -10,10 +11,13 @@ namespace kdn {
 // exp(l n) for a whole n >= 0: 1 for n = 0 whatever l is.
 __device__ __forceinline__ float power(float l, int n) { return n == 0 ? 1.f : expf(l * static_cast<float>(n)); }
 
-// exp(l n) as a sum of two fp32 numbers: the states of thousands of chunks are multiplied by it one after another, and the
-// rounding of one number close to 1 would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).
+// exp(l n) as a sum of two fp32 numbers where it is close to 1: the states of thousands of chunks are multiplied by it one after
+// another, and the rounding of one number would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).  Where it is small
+// the power itself has more digits than 1 + expm1 has, and few chunks matter.
 __device__ __forceinline__ float2 power2(float l, int n) {
-    const float e = n == 0 ? 0.f : expm1f(l * static_cast<float>(n)), hi = 1.f + e, lo = e - (hi - 1.f);
+    const float x = n == 0 ? 0.f : l * static_cast<float>(n);
+    if (!(x > -0.5f)) return make_float2(expf(x), 0.f);
+    const float e = expm1f(x), hi = 1.f + e, lo = e - (hi - 1.f);
     return make_float2(hi, fabsf(lo) < INFINITY ? lo : 0.f);
 }
 
@@ -30,6 +34,80 @@ __device__ __forceinline__ bool sequence(const DecayParams& P, int b, int& row, 
     if (x >= 0 && y >= x && y <= P.n_tok) return true;
     row = len = 0;
     return false;
+}
+
+__device__ __forceinline__ int segments(int len, int seg_len) { return len > 0 ? (len - 1) / seg_len + 1 : 0; }
+
+// What a block works on.
+struct DecayItem {
+    int b, row, len;   // sequence; first token and tokens, of the segment if it is one
+    int slot;          // of its state; negative: a whole sequence
+    bool any;
+};
+
+// The segments of packed sequences longer than seg_len are counted through first, then the other sequences: item `want` of
+// them, or (want < 0) the first slot of sequence ~want.  A warp together.
+__device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want, bool report) {
+    const uint32_t all = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    DecayItem it = {0, 0, 0, -1, false};
+    int before = 0;
+#pragma unroll 1
+    for (int whole = 0; whole < 2; ++whole)
+#pragma unroll 1
+        for (int s0 = 0; s0 < P.n_seq; s0 += 32) {
+            int row = 0, len = -1;
+            if (s0 + lane < P.n_seq && !sequence(P, s0 + lane, row, len) && report) set_status(P.status, kStatusRange);
+            const bool cut = len > P.seg_len;
+            const int mine = whole ? (len >= 0 && !cut) : cut ? segments(len, P.seg_len) : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(all, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const bool here = want < 0 ? s0 + lane == ~want : want < before + upto;
+            const uint32_t hit = __ballot_sync(all, here);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                it.b = s0 + at;
+                it.row = __shfl_sync(all, row, at);
+                it.len = __shfl_sync(all, len, at);
+                const int first = __shfl_sync(all, before + upto - mine, at);
+                it.any = true;
+                if (want < 0) {
+                    it.slot = first;
+                } else if (!whole) {
+                    const int seg = want - first;
+                    it.slot = want;
+                    it.row += seg * P.seg_len;
+                    it.len = min(it.len - seg * P.seg_len, P.seg_len);
+                }
+                return it;
+            }
+            before += __shfl_sync(all, upto, 31);
+        }
+    return it;
+}
+
+// Item `item` of a pass.  `report`: the block's first warp notes bounds that are out of range.
+__device__ __forceinline__ DecayItem find_item(const DecayParams& P, int item, bool report) {
+    DecayItem it = {item, 0, 0, -1, true};
+    if (P.pass == kWhole) {
+        if (!sequence(P, item, it.row, it.len) && report) set_status(P.status, kStatusRange);
+    } else if (!P.cu) {
+        it.b = item / P.nseg;
+        it.slot = item;
+        const int seg = item % P.nseg;
+        sequence(P, it.b, it.row, it.len);
+        it.row += seg * P.seg_len;
+        it.len = min(it.len - seg * P.seg_len, P.seg_len);
+    } else {
+        it = packed_item(P, item, report && item == 0);
+        // (where bounds run backwards there may be more segments than room)
+        if (it.slot >= P.slots || (P.pass == kStates && it.slot < 0)) it.any = false;
+    }
+    return it;
 }
 
 }  // namespace kdn

@@ -33,7 +33,7 @@ constexpr int kC = 64;                        // tokens of a chunk
 // two weight warps and two product warps; the state; V' of a chunk's first and second 32 tokens; outputs: a warpgroup each.  (A
 // warp more would leave 80 registers a thread at launch: a quarter of the SM's registers is for six warps then.)
 constexpr int kThreads = 640;
-constexpr int kAuxRegs = 96, kStateRegs = 184, kValueRegs = 64, kOutputRegs = 72;   // 96 + 184 + 2 x 64 + 72 = 5 x 96, as launched
+constexpr int kStateRegs = 184, kValueRegs = 64, kOutputRegs = 72;   // the first warpgroup has 96 as launched: 96 + 184 + 2 x 64 + 72 = 5 x 96
 constexpr uint32_t kWaitLimit = 1u << 20, kProbeLimit = 4096;   // polls of about a microsecond at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kHalf = 8192;              // 64 tokens of 64 channels
@@ -166,26 +166,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                    bar_o_free = bar_o + 8, bar_drain = bar_o_free + 8, bar_probe = bar_drain + 8;   // bar_u1: the first 32 tokens
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // (the jobs of a head side by side: those of one direction read the same tokens at about the same time)
-    const int job = blockIdx.x % P.n_jobs, bh = blockIdx.x / P.n_jobs, b = bh / P.H, h = bh % P.H, seg = blockIdx.y;
+    const int job = blockIdx.x % P.n_jobs, item = blockIdx.x / P.n_jobs / P.H, h = blockIdx.x / P.n_jobs % P.H;
     const DecayJob& J = P.job[job];
     const bool rev = J.reverse != 0;
 
-    int row0, len;
-    if (!sequence(P, b, row0, len) && tid == 0 && h == 0) set_status(P.status, kStatusRange);
+    const DecayItem it = find_item(P, item, tid < 32 && h == 0 && job == 0);
+    if (!it.any) return;
+    const int row0 = it.row, len = it.len;
     constexpr size_t elems = static_cast<size_t>(DK) * DV;
-    if (P.pass != kWhole) {
-        if (static_cast<long long>(seg) * P.seg_len >= len) return;
-        row0 += seg * P.seg_len;
-        len = min(len - seg * P.seg_len, P.seg_len);
-    }
+    const size_t bh = static_cast<size_t>(it.b) * P.H + h;
     const float* in = nullptr;
     float* end = nullptr;
     int s_k = J.s_k, s_v = J.s_v;
-    if (P.pass == kWhole) {
+    if (it.slot < 0) {
         in = J.S0 ? J.S0 + bh * elems : nullptr;
         end = J.S_T ? J.S_T + bh * elems : nullptr;
     } else {
-        float* st = P.states[job] + (static_cast<size_t>(bh) * P.nseg + seg) * elems;
+        float* st = P.states[job] + (static_cast<size_t>(it.slot) * P.H + h) * elems;
         s_k = DV;
         s_v = 1;
         if (P.pass == kStates) end = st;
@@ -731,14 +728,14 @@ template <int DK, int DV, bool OUT, int PARTS> cudaError_t start(const TcParams&
     constexpr int bytes = Layout<DK, DV, OUT>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<DK, DV, OUT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(T.d.n_seq * T.d.H * n_jobs, T.d.pass == kWhole ? 1 : T.d.nseg);
-    decay_tc_kernel<DK, DV, OUT, PARTS><<<grid, kThreads, bytes, s>>>(T);
+    decay_tc_kernel<DK, DV, OUT, PARTS><<<T.d.items * T.d.H * n_jobs, kThreads, bytes, s>>>(T);
     return cudaGetLastError();
 }
 
 template <int DK, int DV> cudaError_t start_pass(const TcParams& T, int n_jobs, cudaStream_t s) {
     if (T.d.pass == kStates) return start<DK, DV, false, 3>(T, n_jobs, s);
-    if (T.d.pass == kOutputs) return start<DK, DV, true, 2>(T, n_jobs, s);
+    // (of packed sequences some may be whole, and have a final state to give)
+    if (T.d.pass == kOutputs && !T.d.cu) return start<DK, DV, true, 2>(T, n_jobs, s);
     return start<DK, DV, true, 3>(T, n_jobs, s);
 }
 
