@@ -617,29 +617,35 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (!await(bar_o, n & 1)) break;
                 tc_fence_after();
                 const int mark0 = marks[n % kMarks][0][j], mark1 = marks[n % kMarks][1][j];
-#pragma unroll 1
-                for (int e = 0; e < 4; ++e) {   // 16 channels and 32 tokens at a time
-                    const uint32_t at = ((e >> 1) * 16u << 16) + 32 * (e & 1);
-                    uint32_t x[16], y[16];
-                    tmem_ld_frag4(ti + at, x);
-                    tmem_ld_frag4(tx + at, y);
-                    float2 f[4];
+                // 16 channels and 32 tokens at a time, the next ones on their way while these are put in order
+                auto at = [](int e) { return ((e >> 1) * 16u << 16) + 32 * (e & 1); };
+                uint32_t x[2][16], y[2][16];
+                tmem_ld_frag4(ti, x[0]);
+                tmem_ld_frag4(tx, y[0]);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) f[t] = *reinterpret_cast<const float2*>(&rf[last][32 * (e & 1) + 8 * t + 2 * (lane % 4)]);
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t (&xi)[16] = x[e & 1], (&yi)[16] = y[e & 1];
                     tmem_wait_ld();
-                    loaded(x);
-                    loaded(y);
-                    if (e == 3) {
+                    loaded(xi);
+                    loaded(yi);
+                    if (e < 3) {
+                        tmem_ld_frag4(ti + at(e + 1), x[~e & 1]);
+                        tmem_ld_frag4(tx + at(e + 1), y[~e & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_o_free);
                     }
                     uint32_t z[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 o = fma2(f[i / 2], make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])),
-                                              make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
-                        z[i] = pack_bf16(o.x, o.y);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 f = *reinterpret_cast<const float2*>(&rf[last][32 * (e & 1) + 4 * i + 2 * (lane % 4)]);
+#pragma unroll
+                        for (int c = i; c < i + 2; ++c) {
+                            const float2 o = fma2(f, make_float2(__uint_as_float(yi[2 * c]), __uint_as_float(yi[2 * c + 1])),
+                                                  make_float2(__uint_as_float(xi[2 * c]), __uint_as_float(xi[2 * c + 1])));
+                            z[c] = pack_bf16(o.x, o.y);
+                        }
                     }
 #pragma unroll
                     for (int t = 0; t < 4; t += 2)
