@@ -168,7 +168,8 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
         }
     };
     if (chunks > 0) fetch(0);
-    const float2 c_full = power2(l, kC);
+    const Carry c_full(l, kC), c_last(l, len - (chunks - 1) * kC);
+    float rest = 0.f;
 #pragma unroll 1
     for (int n = 0; n < chunks; ++n) {
         int t0;
@@ -264,12 +265,12 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
         if (s_mine && (end || n + 1 < chunks)) {
             float u[NS][4] = {};
             warp_product<NS, kC, true>(u, sk + s_row, LQ, wt, sv + s_col, LV, 1);
-            const float2 c = m == kC ? c_full : power2(l, m);
+            const float c = (m == kC ? c_full : c_last).next(rest);
 #pragma unroll
             for (int x = 0; x < NS; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    S[x][e] = fmaf(c.x, S[x][e], fmaf(c.y, S[x][e], u[x][e]));
+                    S[x][e] = fmaf(c, S[x][e], u[x][e]);
                     if (bad && bad_at[s_col + 8 * x + 2 * q + (e & 1)] < kC) S[x][e] = NAN;
                 }
         }

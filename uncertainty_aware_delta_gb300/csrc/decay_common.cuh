@@ -11,15 +11,30 @@ namespace kdn {
 // exp(l n) for a whole n >= 0: 1 for n = 0 whatever l is.
 __device__ __forceinline__ float power(float l, int n) { return n == 0 ? 1.f : expf(l * static_cast<float>(n)); }
 
-// exp(l n) as a sum of two fp32 numbers where it is close to 1: the states of thousands of chunks are multiplied by it one after
-// another, and the rounding of one number would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).  Where it is small
-// the power itself has more digits than 1 + expm1 has, and few chunks matter.
-__device__ __forceinline__ float2 power2(float l, int n) {
-    const float x = n == 0 ? 0.f : l * static_cast<float>(n);
-    if (!(x > -0.5f)) return make_float2(expf(x), 0.f);
-    const float e = expm1f(x), hi = 1.f + e, lo = e - (hi - 1.f);
-    return make_float2(hi, fabsf(lo) < INFINITY ? lo : 0.f);
-}
+// exp(l n), by which the states of thousands of chunks are multiplied one after another: the rounding of one number close to 1
+// would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).  It is held as a sum of two, and next() gives the nearest
+// number to what is left to multiply by, so that the product of any chunks' factors stays within a rounding of the power.
+// Where the power is small it has more digits than 1 + expm1 has, and few chunks matter.
+struct Carry {
+    float hi, lo;
+    __device__ __forceinline__ Carry(float l, int n) {
+        const float x = n == 0 ? 0.f : l * static_cast<float>(n);
+        if (x > -0.5f && x < 0.5f) {
+            const float e = expm1f(x);
+            hi = 1.f + e;
+            lo = e - (hi - 1.f);
+        } else {
+            hi = expf(x);
+            lo = 0.f;
+        }
+    }
+    __device__ __forceinline__ float next(float& rest) const {
+        rest += lo;
+        const float f = hi + rest;
+        rest -= f - hi;
+        return f;
+    }
+};
 
 // Tokens of sequence b: first row and length; false where its bounds run backwards or outside.
 __device__ __forceinline__ bool sequence(const DecayParams& P, int b, int& row, int& len) {

@@ -104,9 +104,9 @@ template <int N> __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {   //
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-// Fragments of 16 lanes: 32-bit column t % 4 of lanes t / 4 and t / 4 + 8 (and again four columns on) ...
-__device__ __forceinline__ void tmem_st_frag2(uint32_t taddr, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
+// Fragments of 16 lanes: 32-bit column t % 4 of lanes t / 4 and t / 4 + 8 ...
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, uint32_t r0, uint32_t r1) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r0), "r"(r1));
 }
 // ... and columns 2 (t % 4), + 1 of lane t / 4, then those of lane t / 4 + 8 (and again eight columns on).
 __device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
@@ -199,6 +199,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
     auto place = [&](int n) { return rev ? chunks - 1 - n : n; };
     auto is_last = [&](int n) { return place(n) == chunks - 1; };
 
+    // copies of chunk n of the walk; the first ones by the first thread, the others by one of those that make weights
+    const int early = P.probe ? 1 : min(chunks, kStages);
+    auto copy = [&](int n) {
+        const int slot = n % kStages, t = row0 + place(n) * kC;
+        const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
+        mbar_expect_tx(full, L::kStage);
+        tma_load_4d(st, &T.k[job], 0, t, 0, h, full);
+        if (OUT) tma_load_4d(st + L::kQ, &T.q[job], 0, t, 0, h, full);
+        tma_load_4d(st + L::kV, &T.v[job], 0, t, 0, h, full);
+        if (P.probe && n == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
+            aborted = 1;
+            set_status(P.status, kStatusTimeout);
+        }
+    };
     if (tid == 0) {
         aborted = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -221,6 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
         mbar_init(bar_drain, OUT ? 2 : 1);
         mbar_init(bar_probe, 1);   // completed by nothing
         mbar_fence_init();
+        fence_proxy_async();
+        for (int i = 0; i < early && !aborted; ++i) copy(i);   // (before all else: the first of them takes longer than that)
     }
     if (tid <= kC) pw[tid] = power(l, tid);
     if (warp == 8) {
@@ -348,29 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             // ---- loader, a lane of the warp that has less to do otherwise (asked for by the warp of the state's products or of
             // the outputs, copies held these up by 600 to 1000 cycles a chunk)
             const bool loads = lane == 0 && warp == (rev ? 1 : 0);
-            int sent = 0, slot = 0;
-            uint32_t phase = 1;
+            int sent = early;
             auto load = [&]() {   // the next chunk, once its stage is free
-                if (sent >= kStages && !wait(bar_empty + 8 * slot, phase)) return;
-                const uint32_t st = sb + slot * L::kStage, full = bar_full + 8 * slot;
-                const int t = row0 + place(sent) * kC;
-                mbar_expect_tx(full, L::kStage);
-                tma_load_4d(st, &T.k[job], 0, t, 0, h, full);
-                if (OUT) tma_load_4d(st + L::kQ, &T.q[job], 0, t, 0, h, full);
-                tma_load_4d(st + L::kV, &T.v[job], 0, t, 0, h, full);
-                if (P.probe && sent == 0 && !mbar_wait(bar_probe, 0, kProbeLimit)) {
-                    aborted = 1;
-                    set_status(P.status, kStatusTimeout);
-                }
+                if (!wait(bar_empty + 8 * (sent % kStages), (sent / kStages - 1) & 1)) return;
+                copy(sent);
                 ++sent;
-                if (++slot == kStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
             };
-            if (loads)
+            if (loads && !OUT)
 #pragma unroll 1
-                while (sent < chunks && (!OUT || sent < kStages) && !aborted) load();
+                while (sent < chunks && !aborted) load();
             __syncwarp();
             // ---- weights: row i of the chunk a thread.  Of the two blocks of 32 columns one is cut by the
             // diagonal, with the same powers in every chunk, and one is seen whole or not at all.
@@ -399,20 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 for (int e = 0; e < (whole ? 2 : 1); ++e) {   // the block that is cut, then the other
                     const int c = low ^ e;
                     uint32_t x[32];
+                    float f[32];
                     tmem_ld32(tw + 32 * c, x);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[j]), "=f"(f[j + 1]), "=f"(f[j + 2]), "=f"(f[j + 3])
+                                     : "r"(mine + e * 32 * kFRow + 4 * j));
                     uint32_t seen = e ? kAll : cut;
                     if (m - 32 * c < 32) seen &= m > 32 * c ? (1u << (m - 32 * c)) - 1u : 0u;
                     tmem_wait_ld();
                     loaded(x);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float f[4];
-                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                                     : "r"(mine + e * 32 * kFRow + 4 * j));
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            x[j + y] = seen >> (j + y) & 1u ? __float_as_uint(__uint_as_float(x[j + y]) * f[y]) : 0u;
-                    }
+                    for (int j = 0; j < 32; ++j) x[j] = seen >> j & 1u ? __float_as_uint(__uint_as_float(x[j]) * f[j]) : 0u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) put(to(n, c, j), x + 8 * j);
                 }
@@ -465,13 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(bar_s);
         };
         if (OUT) give();
-        const float2 f_full = power2(l, kC), f_last = power2(l, m_last);
+        const Carry f_full(l, kC), f_last(l, m_last);
+        float rest = 0.f;
 #pragma unroll 1
         for (int n = 0; n < chunks; ++n) {
             const uint32_t buf = n % M::kBufs, here = tu + 128 * buf;
             if (!await(bar_u + 8 * buf, n / M::kBufs & 1)) break;
             tc_fence_after();
-            const float2 f = is_last(n) ? f_last : f_full, fx = make_float2(f.x, f.x), fy = make_float2(f.y, f.y);
+            const float f = (is_last(n) ? f_last : f_full).next(rest);
+            const float2 ff = make_float2(f, f);
             uint32_t x[2][32];   // the next columns are on their way while these are added
             tmem_ld32(here, x[0]);
 #pragma unroll
@@ -482,8 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     const uint32_t* u = x[c / 32 % 2] + i;
-                    const float2 y = make_float2(S[c + i], S[c + i + 1]),
-                                 z = fma2(fx, y, fma2(fy, y, make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]))));
+                    const float2 z = fma2(ff, make_float2(S[c + i], S[c + i + 1]), make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])));
                     S[c + i] = z.x;
                     S[c + i + 1] = z.y;
                 }
@@ -521,41 +522,35 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
             float2 odd = make_float2(0.f, 0.f);   // NaN where a value is not finite
             // (in a loop, as short as may be: the block's roles together hardly fit the instruction cache)
 #pragma unroll 1
-            for (int t = 0; t < 4; t += 2) {
-                uint32_t v[2][4] = {};
-                float2 f[2];
+            for (int t = 0; t < 4; ++t) {
+                uint32_t v[4] = {};
+                if (j - lane < DV) ldmatrix_t(st + rows + t * 1024, v);
+                const int at = 8 * t + 2 * (lane % 4);
+                const float2 f = *reinterpret_cast<const float2*>(&vf[last][32 * half + at]);
+                if (m < 32) {   // rows of other sequences
+                    const uint32_t there = at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (j - lane < DV) ldmatrix_t(st + rows + (t + e) * 1024, v[e]);
-                    const int at = 8 * (t + e) + 2 * (lane % 4);
-                    f[e] = *reinterpret_cast<const float2*>(&vf[last][32 * half + at]);
-                    if (m < 32) {   // rows of other sequences
-                        const uint32_t there = at + 1 < m ? 0xffffffffu : at < m ? 0xffffu : 0u;
+                    for (int c = 0; c < 4; ++c) v[c] &= there;
+                }
+                uint32_t part[PARTS][4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) v[e][c] &= there;
+                for (int c = 0; c < 4; ++c) {
+                    float2 x = unpack2(v[c]);
+                    if (OUT) odd = fma2(x, make_float2(0.f, 0.f), odd);
+                    x = mul2(x, f);
+                    // (parts cut off, not rounded: three have all 24 bits, and cutting off takes one instruction a pair)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) {
+                        part[p][c] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+                        if (p + 1 < PARTS)
+                            x = fma2(make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
+                                     make_float2(-1.f, -1.f), x);
                     }
                 }
-                uint32_t part[PARTS][2][4];   // of lanes 0 .. 15 and 16 .. 31
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float2 x = unpack2(v[e][c]);
-                        if (OUT) odd = fma2(x, make_float2(0.f, 0.f), odd);
-                        x = mul2(x, f[e]);
-                        // (parts cut off, not rounded: three have all 24 bits, and cutting off takes one instruction a pair)
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {
-                            part[p][c / 2][2 * e + c % 2] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-                            if (p + 1 < PARTS)
-                                x = fma2(make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
-                                         make_float2(-1.f, -1.f), x);
-                        }
-                    }
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    tmem_st_frag2(tv + 96 * buf + 32 * p + 4 * t, part[p][0]);
-                    tmem_st_frag2(tv + 96 * buf + 32 * p + 4 * t + (16u << 16), part[p][1]);
+                for (int p = 0; p < PARTS; ++p) {   // lanes 0 .. 15, and 16 .. 31
+                    tmem_st_frag(tv + 96 * buf + 32 * p + 4 * t, part[p][0], part[p][1]);
+                    tmem_st_frag(tv + 96 * buf + 32 * p + 4 * t + (16u << 16), part[p][2], part[p][3]);
                 }
             }
             if (OUT) {
