@@ -27,11 +27,16 @@ namespace {
 constexpr int kC = 32, kThreads = 256;   // tokens of a chunk; threads of a block
 constexpr int kSMs = 152;                // GB300
 
-__device__ __forceinline__ float4 load4(const void* p, long long i, int io) {
-    if (io == KDN_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                       __uint_as_float(x.y & 0xffff0000u));
+// Four values as they are in memory, and as fp32 (apart from the load, so that it does not have to be waited for).
+template <bool BF> __device__ __forceinline__ float4 load4(const void* p, long long i) {
+    if (!BF) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float2 x = *reinterpret_cast<const float2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    return make_float4(x.x, x.y, 0.f, 0.f);
+}
+template <bool BF> __device__ __forceinline__ float4 widen(float4 v) {
+    if (!BF) return v;
+    const uint32_t x = __float_as_uint(v.x), y = __float_as_uint(v.y);
+    return make_float4(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u), __uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
 }
 
 // x = hi + lo, both TF32: hi rounded to nearest, the rest cut off (to 2^-22 of x, of either sign), by integer operations
@@ -41,58 +46,101 @@ __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
-// A warp's 16 x 8 NT tile of A B in 3xTF32 (fragments: mma_tf32x3.cuh), the MMAs' sums taken over 32 of K and then in fp32
-// (their accumulation is cut off, not rounded).  A(r, k) = A[r lda + k], or A[k lda + r] w[k] where TRANS;
-// B(k, c) = B[k bk + c bc].
-template <int NT, int K, bool TRANS>
-__device__ __forceinline__ void warp_product(float (&out)[NT][4], const float* A, int lda, const float* w, const float* B, int bk,
-                                             int bc) {
+// An operand's fragment: two TF32 parts, or (EXACT: it was bf16) the one that it is.
+template <int N, bool EXACT> struct Parts {
+    uint32_t hi[N], lo[N];
+    __device__ __forceinline__ void set(int i, float x) {
+        if (EXACT) hi[i] = __float_as_uint(x);
+        else split(x, hi[i], lo[i]);
+    }
+};
+// Sums of the products of parts.  (Few tiles: a sum for each product, as the MMAs of one sum wait for one another.)
+template <int NT> constexpr int kSums = NT <= 2 ? 3 : 1;
+template <int NT, bool EA, bool EB>
+__device__ __forceinline__ void multiply(float (&acc)[kSums<NT>][NT][4], int n, const Parts<4, EA>& a, const Parts<2, EB>& b) {
+    constexpr int kLast = kSums<NT> - 1;
+    if (!EA) mma_m16n8k8_tf32(acc[kLast][n], a.lo, b.hi[0], b.hi[1]);
+    if (!EB) mma_m16n8k8_tf32(acc[kLast / 2][n], a.hi, b.lo[0], b.lo[1]);
+    mma_m16n8k8_tf32(acc[0][n], a.hi, b.hi[0], b.hi[1]);
+}
+template <int NT> __device__ __forceinline__ void add_sums(float (&out)[NT][4], const float (&acc)[kSums<NT>][NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[n][e] += kSums<NT> == 1 ? acc[0][n][e] : acc[0][n][e] + (acc[1 % kSums<NT>][n][e] + acc[kSums<NT> - 1][n][e]);
+}
+
+// A warp's 16 x 8 NT tile of A B (fragments: mma_tf32x3.cuh), the MMAs' sums taken over 32 of K and then in fp32 (their
+// accumulation is cut off, not rounded).  A(r, k) = A[r lda + k], or A[k lda + r] w[k] where TRANS; B(k, c) = B[k ldb + c].
+template <int NT, int K, bool TRANS, bool EB>
+__device__ __forceinline__ void warp_product(float (&out)[NT][4], const float* A, int lda, const float* w, const float* B, int ldb) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     constexpr int kSpan = K < 32 ? K : 32;
 #pragma unroll 1
     for (int k0 = 0; k0 < K; k0 += kSpan) {
-        // (few tiles: a sum for each of the three products, as the MMAs of one sum wait for one another)
-        constexpr int kSums = NT <= 2 ? 3 : 1;
-        float acc[kSums][NT][4] = {};
+        float acc[kSums<NT>][NT][4] = {};
 #pragma unroll
         for (int k = k0; k < k0 + kSpan; k += 8) {
-            float a[4];
+            Parts<4, false> a;
             if (TRANS) {
                 const float w0 = w[k + q], w1 = w[k + q + 4];
-                a[0] = A[(k + q) * lda + g] * w0;
-                a[1] = A[(k + q) * lda + g + 8] * w0;
-                a[2] = A[(k + q + 4) * lda + g] * w1;
-                a[3] = A[(k + q + 4) * lda + g + 8] * w1;
+                a.set(0, A[(k + q) * lda + g] * w0);
+                a.set(1, A[(k + q) * lda + g + 8] * w0);
+                a.set(2, A[(k + q + 4) * lda + g] * w1);
+                a.set(3, A[(k + q + 4) * lda + g + 8] * w1);
             } else {
-                a[0] = A[g * lda + k + q];
-                a[1] = A[(g + 8) * lda + k + q];
-                a[2] = A[g * lda + k + q + 4];
-                a[3] = A[(g + 8) * lda + k + q + 4];
+                a.set(0, A[g * lda + k + q]);
+                a.set(1, A[(g + 8) * lda + k + q]);
+                a.set(2, A[g * lda + k + q + 4]);
+                a.set(3, A[(g + 8) * lda + k + q + 4]);
             }
-            uint32_t ah[4], al[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split(a[e], ah[e], al[e]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float* b = B + (k + q) * bk + (8 * n + g) * bc;
-                uint32_t bh0, bl0, bh1, bl1;
-                split(b[0], bh0, bl0);
-                split(b[4 * bk], bh1, bl1);
-                mma_m16n8k8_tf32(acc[kSums - 1][n], al, bh0, bh1);
-                mma_m16n8k8_tf32(acc[kSums / 2][n], ah, bl0, bl1);
-                mma_m16n8k8_tf32(acc[0][n], ah, bh0, bh1);
+                Parts<2, EB> b;
+                b.set(0, B[(k + q) * ldb + 8 * n + g]);
+                b.set(1, B[(k + q + 4) * ldb + 8 * n + g]);
+                multiply<NT>(acc, n, a, b);
             }
         }
+        add_sums<NT>(out, acc);
+    }
+}
+
+// Two products of the same 16 rows of Q: with 8 rows of K (a tile of the weights) and with 8 NT columns of the state.
+template <int NT, int K, bool BF>
+__device__ __forceinline__ void query_products(float (&w)[1][4], float (&o)[NT][4], const float* Q, const float* Kt, int ld, const float* S, int lds) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    constexpr int kSpan = K < 32 ? K : 32;
+#pragma unroll 1
+    for (int k0 = 0; k0 < K; k0 += kSpan) {
+        float aw[3][1][4] = {}, ao[kSums<NT>][NT][4] = {};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int k = k0; k < k0 + kSpan; k += 8) {
+            Parts<4, BF> a;
+            a.set(0, Q[g * ld + k + q]);
+            a.set(1, Q[(g + 8) * ld + k + q]);
+            a.set(2, Q[g * ld + k + q + 4]);
+            a.set(3, Q[(g + 8) * ld + k + q + 4]);
+            Parts<2, BF> b;
+            b.set(0, Kt[g * ld + k + q]);
+            b.set(1, Kt[g * ld + k + q + 4]);
+            multiply<1>(aw, 0, a, b);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[n][e] += kSums == 1 ? acc[0][n][e] : acc[0][n][e] + (acc[1][n][e] + acc[kSums - 1][n][e]);
+            for (int n = 0; n < NT; ++n) {
+                Parts<2, false> s;
+                s.set(0, S[(k + q) * lds + 8 * n + g]);
+                s.set(1, S[(k + q + 4) * lds + 8 * n + g]);
+                multiply<NT>(ao, n, a, s);
+            }
+        }
+        add_sums<1>(w, aw);
+        add_sums<NT>(o, ao);
     }
 }
 
 // One block: a head of a sequence (or of a segment of it) and DVS of its value channels; the state in the registers of its
 // warps as their products' fragments, and in shared memory as the next chunk's operand.
-template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_kernel(const __grid_constant__ DecayParams P) {
+template <int DK, int DVS, bool BF> __global__ void __launch_bounds__(kThreads, 2) decay_kernel(const __grid_constant__ DecayParams P) {
     // (rows apart by 4 or 8 banks: the fragments' loads meet no bank twice, but those of K^T two)
     constexpr int LQ = DK + 4, LV = DVS + 8, LP = kC + 4;
     extern __shared__ __align__(16) float sm[];
@@ -157,14 +205,14 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
             const int e = x * kThreads + tid, t = e / (DK / 4), c = e % (DK / 4) * 4;
             const bool there = t < m;
             const long long r = static_cast<long long>(row0) + t0 + t;
-            fq[x] = there && outputs ? load4(J.q.p, r * J.q.row + h * J.q.head + c, P.io) : zero;
-            fk[x] = there ? load4(J.k.p, r * J.k.row + h * J.k.head + c, P.io) : zero;
+            fq[x] = there && outputs ? load4<BF>(J.q.p, r * J.q.row + h * J.q.head + c) : zero;
+            fk[x] = there ? load4<BF>(J.k.p, r * J.k.row + h * J.k.head + c) : zero;
         }
 #pragma unroll
         for (int x = 0; x < NV; ++x) {
             const int e = x * kThreads + tid, t = e / (DVS / 4), c = e % (DVS / 4) * 4;
             const long long r = static_cast<long long>(row0) + t0 + t;
-            fv[x] = t < m ? load4(J.v.p, r * J.v.row + h * J.v.head + v0 + c, P.io) : zero;
+            fv[x] = t < m ? load4<BF>(J.v.p, r * J.v.row + h * J.v.head + v0 + c) : zero;
         }
     };
     if (chunks > 0) fetch(0);
@@ -187,15 +235,16 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
         for (int x = 0; x < NQ; ++x) {
             const int e = x * kThreads + tid, t = e / (DK / 4), c = e % (DK / 4) * 4;
             if (t < kC) {
-                *reinterpret_cast<float4*>(sq + t * LQ + c) = fq[x];
-                *reinterpret_cast<float4*>(sk + t * LQ + c) = fk[x];
+                *reinterpret_cast<float4*>(sq + t * LQ + c) = widen<BF>(fq[x]);
+                *reinterpret_cast<float4*>(sk + t * LQ + c) = widen<BF>(fk[x]);
             }
         }
 #pragma unroll
         for (int x = 0; x < NV; ++x) {
             const int e = x * kThreads + tid, t = e / (DVS / 4), c = e % (DVS / 4) * 4;
-            if (t < kC) *reinterpret_cast<float4*>(sv + t * LV + c) = fv[x];
-            bad |= !(fabsf(fv[x].x) + fabsf(fv[x].y) + fabsf(fv[x].z) + fabsf(fv[x].w) < INFINITY);
+            const float4 y = widen<BF>(fv[x]);
+            if (t < kC) *reinterpret_cast<float4*>(sv + t * LV + c) = y;
+            bad |= !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
         }
         if (tid < kC) {
             const int left = max(m - 1 - tid, 0);
@@ -223,22 +272,21 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
         }
 
         if (outputs) {
-            // weights: 2 x 4 tiles, one a warp
-            const int r0 = (warp >> 2) * 16, c0 = (warp & 3) * 8;
-            float a[1][4] = {};
-            warp_product<1, DK, false>(a, sq + r0 * LQ, LQ, nullptr, sk + c0 * LQ, 1, LQ);
+            // weights: 2 x 4 tiles, one a warp; the same rows of the outputs in as many parts
+            constexpr int NO = DVS / 32 > 0 ? DVS / 32 : 1;
+            const int r0 = (warp >> 2) * 16, c0 = (warp & 3) * 8, oc = (warp & 3) * NO * 8;
+            float a[1][4] = {}, o[NO][4] = {};
+            // (with 16 value channels half of the warps have no outputs: they work on a tile that is not used)
+            query_products<NO, DK, BF>(a, o, sq + r0 * LQ, sk + c0 * LQ, LQ, ss + (oc < DVS ? oc : 0), LV);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = r0 + g + 8 * (e >> 1), j = c0 + 2 * q + (e & 1), gap = J.reverse ? j - i : i - j;
                 sp[i * LP + j] = gap >= 0 ? a[0][e] * pw[max(gap, 0)] : 0.f;
             }
             __syncthreads();
-            constexpr int NO = DVS / 32 > 0 ? DVS / 32 : 1;
-            const int oc = (warp & 3) * NO * 8;
             if (oc < DVS) {
-                float o[NO][4] = {}, y[NO][4] = {};
-                warp_product<NO, DK, false>(o, sq + r0 * LQ, LQ, nullptr, ss + oc, LV, 1);
-                warp_product<NO, kC, false>(y, sp + r0 * LP, LP, nullptr, sv + oc, LV, 1);
+                float y[NO][4] = {};
+                warp_product<NO, kC, false, BF>(y, sp + r0 * LP, LP, nullptr, sv + oc, LV);
                 if (bad)
 #pragma unroll
                     for (int x = 0; x < NO; ++x)
@@ -256,7 +304,7 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
                     for (int x = 0; x < NO; ++x) {
                         const long long at = ((static_cast<long long>(row0) + t0 + i) * P.H + h) * J.dv + v0 + oc + 8 * x + 2 * q;
                         const float u = fmaf(f, o[x][e], y[x][e]), w = fmaf(f, o[x][e + 1], y[x][e + 1]);
-                        if (P.io == KDN_F32) *reinterpret_cast<float2*>(static_cast<float*>(J.o) + at) = make_float2(u, w);
+                        if (!BF) *reinterpret_cast<float2*>(static_cast<float*>(J.o) + at) = make_float2(u, w);
                         else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(J.o) + at) = __floats2bfloat162_rn(u, w);
                     }
                 }
@@ -264,7 +312,7 @@ template <int DK, int DVS> __global__ void __launch_bounds__(kThreads, 2) decay_
         }
         if (s_mine && (end || n + 1 < chunks)) {
             float u[NS][4] = {};
-            warp_product<NS, kC, true>(u, sk + s_row, LQ, wt, sv + s_col, LV, 1);
+            warp_product<NS, kC, true, BF>(u, sk + s_row, LQ, wt, sv + s_col, LV);
             const float c = (m == kC ? c_full : c_last).next(rest);
 #pragma unroll
             for (int x = 0; x < NS; ++x)
@@ -329,20 +377,24 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
     }
 }
 
-template <int DK, int DVS> cudaError_t start(const DecayParams& P, int n_jobs, cudaStream_t s) {
+template <int DK, int DVS, bool BF> cudaError_t start(const DecayParams& P, int n_jobs, cudaStream_t s) {
     constexpr int bytes = 4 * (2 * kC * (DK + 4) + (kC + DK) * (DVS + 8) + kC * (kC + 4));
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t e = cudaFuncSetAttribute(decay_kernel<DK, DVS, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    decay_kernel<DK, DVS><<<dim3(P.items * P.H * (P.job[0].dv / DVS), 1, n_jobs), kThreads, bytes, s>>>(P);
+    decay_kernel<DK, DVS, BF><<<dim3(P.items * P.H * (P.job[0].dv / DVS), 1, n_jobs), kThreads, bytes, s>>>(P);
     return cudaGetLastError();
 }
 
+template <int DK, int DVS> cudaError_t start_io(const DecayParams& P, int n_jobs, cudaStream_t s) {
+    return P.io == KDN_BF16 ? start<DK, DVS, true>(P, n_jobs, s) : start<DK, DVS, false>(P, n_jobs, s);
+}
+
 template <int DK> cudaError_t start_dv(const DecayParams& P, int n_jobs, cudaStream_t s) {
-    if (P.job[0].dv == 16) return start<DK, 16>(P, n_jobs, s);
-    if (P.job[0].dv == 32) return start<DK, 32>(P, n_jobs, s);
-    return start<DK, 64>(P, n_jobs, s);
+    if (P.job[0].dv == 16) return start_io<DK, 16>(P, n_jobs, s);
+    if (P.job[0].dv == 32) return start_io<DK, 32>(P, n_jobs, s);
+    return start_io<DK, 64>(P, n_jobs, s);
 }
 
 // Jobs of the same head sizes in one launch.
