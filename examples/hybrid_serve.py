@@ -1,8 +1,9 @@
 """Serve requests with a hybrid stack: KDN memories beside attention over a paged 4-bit cache.
 
 Every layer is a Diagonal KDN mixer followed by causal attention (through a sliding window, or none)
-with fewer key heads than query heads; weights are random.  One plan a call gives pages to all layers'
-caches.  Prompts run packed one after another, the attention over what the cache holds of them already
+with fewer key heads than query heads; weights are random.  (``--mixer decay``: the mixer is linear attention
+with a decay for each head instead, its outputs normalised head by head and gated.)  One plan a call gives
+pages to all layers' caches.  Prompts run packed one after another, the attention over what the cache holds of them already
 and over their new tokens; then every request gets a token a step.
 
     python examples/hybrid_serve.py --requests 8 --prompt 700 --steps 32
@@ -26,19 +27,25 @@ class Server:
     """`requests` places; each holds a request's KDN states, its pages and its length."""
 
     def __init__(self, requests, pages, *, layers=2, heads=8, kv_heads=2, d=128, page=64, table_width=64, window=0,
-                 seed=0, device="cuda"):
+                 seed=0, device="cuda", mixer="kdn"):
+        if mixer not in ("kdn", "decay"):
+            raise ValueError(f"mixer must be 'kdn' or 'decay', not {mixer!r}")
         self.R, self.H, self.Hkv, self.d, self.page, self.window = requests, heads, kv_heads, d, page, window
-        self.dim = heads * d
+        self.mixer, self.dim = mixer, heads * d
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weight(n_in, n_out):
             return (torch.randn(n_in, n_out, generator=g, device=device) * n_in ** -0.5).bfloat16()
 
-        self.layers = [dict(mix=weight(self.dim, 5 * self.dim + heads), mix_out=weight(self.dim, self.dim),
+        n_mix = 5 * self.dim + heads if mixer == "kdn" else 4 * self.dim
+        self.layers = [dict(mix=weight(self.dim, n_mix), mix_out=weight(self.dim, self.dim),
                             qkv=weight(self.dim, (heads + 2 * kv_heads) * d), out=weight(self.dim, self.dim),
                             S=torch.zeros(requests, heads, d, d, device=device),
                             p=torch.ones(requests, heads, d, device=device),
                             cache=kdn.cache_alloc(pages, page, kv_heads, d, device)) for _ in range(layers)]
+        # (decay) memories of about 32 tokens in the first head to some 4000 in the last; the norm of a memory's outputs
+        self.log_decay = torch.log1p(-torch.exp2(-5 - 7 * torch.arange(heads, device=device) / max(heads - 1, 1)))
+        self.norm_weight, self.norm_bias = torch.ones(heads, d, device=device), torch.zeros(heads, d, device=device)
         ints = dict(dtype=torch.int32, device=device)
         self.table = torch.full((requests, table_width), -1, **ints)
         self.free = torch.arange(pages - 1, -1, -1, **ints)     # a stack: the next page is its last
@@ -68,6 +75,15 @@ class Server:
         q, k = (F.normalize(t.float(), dim=-1).bfloat16() for t in (q, k))
         return [t.contiguous() for t in (q, k, v, F.logsigmoid(a.float() + 4.6), F.softplus(w.float() - 6.0), r)]
 
+    def _decay_inputs(self, layer, x):
+        """q, k, v and the outputs' gate of tokens x [n, dim]."""
+        q, k, v, gate = (norm(x) @ layer["mix"]).view(x.shape[0], 4, self.H, self.d).unbind(1)
+        q, k = (F.normalize(t.float(), dim=-1).bfloat16() for t in (q, k))
+        return q, k, v, gate
+
+    def _decay_outputs(self, o, gate):
+        return kdn.kdn_group_norm(o, self.norm_weight, self.norm_bias, gate=gate, act="silu")
+
     def _attention_inputs(self, layer, x):
         z = (norm(x) @ layer["qkv"]).view(x.shape[0], self.H + 2 * self.Hkv, self.d)
         return z.split([self.H, self.Hkv, self.Hkv], 1)     # strided rows: taken as they are
@@ -91,13 +107,19 @@ class Server:
         known = self.table[request, place // self.page].long() * self.page + place % self.page
         mine = (place >= torch.tensor(ctx, device=self.device)[request]).nonzero()[:, 0]
         for layer in self.layers:
-            mixed = torch.zeros_like(x).view(-1, self.H, self.d)
-            z = self._mixer_inputs(layer, x)
-            for r in range(self.R):
-                if new[r] and granted[r]:
-                    o, S, p = kdn.kdn_diag_forward(*(t[None, cu[r]:cu[r + 1]] for t in z),
-                                                   layer["S"][r:r + 1], layer["p"][r:r + 1])
-                    mixed[cu[r]:cu[r + 1]], layer["S"][r], layer["p"][r] = o[0], S[0], p[0]
+            if self.mixer == "decay":     # all requests in one call
+                q, k, v, gate = self._decay_inputs(layer, x)
+                o, S = kdn.kdn_decay_forward(q, k, v, self.log_decay, layer["S"], cu=plan.cu_new)
+                layer["S"] = torch.where(plan.granted[:, None, None, None] > 0, S, layer["S"])
+                mixed = self._decay_outputs(o, gate)
+            else:
+                mixed = torch.zeros_like(x).view(-1, self.H, self.d)
+                z = self._mixer_inputs(layer, x)
+                for r in range(self.R):
+                    if new[r] and granted[r]:
+                        o, S, p = kdn.kdn_diag_forward(*(t[None, cu[r]:cu[r + 1]] for t in z),
+                                                       layer["S"][r:r + 1], layer["p"][r:r + 1])
+                        mixed[cu[r]:cu[r + 1]], layer["S"][r], layer["p"][r] = o[0], S[0], p[0]
             x = x + mixed.view_as(x) @ layer["mix_out"]
             q, k, v = self._attention_inputs(layer, x)
             if any(ctx):
@@ -118,7 +140,11 @@ class Server:
             raise RuntimeError("the cache is out of pages: release a request")
         self._take(plan)
         for layer in self.layers:
-            o = kdn.kdn_step("diag", *self._mixer_inputs(layer, x), layer["S"], layer["p"])
+            if self.mixer == "decay":
+                q, k, v, gate = self._decay_inputs(layer, x)
+                o = self._decay_outputs(kdn.kdn_decay_step(q, k, v.contiguous(), self.log_decay, layer["S"]), gate)
+            else:
+                o = kdn.kdn_step("diag", *self._mixer_inputs(layer, x), layer["S"], layer["p"])
             x = x + o.view_as(x) @ layer["mix_out"]
             q, k, v = self._attention_inputs(layer, x)
             kdn.kdn_cache_write(k, v, plan.slot_map, layer["cache"])
@@ -143,10 +169,11 @@ def main():
     ap.add_argument("--prompt", type=int, default=700, help="longest prompt")
     ap.add_argument("--steps", type=int, default=32, help="tokens generated for each request")
     ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--mixer", choices=("kdn", "decay"), default="kdn")
     a = ap.parse_args()
     gen = torch.Generator(device="cuda").manual_seed(1)
     width = -(-(2 * a.prompt + 2 * a.steps) // 64)
-    s = Server(a.requests, a.requests * width, table_width=width, window=a.window)
+    s = Server(a.requests, a.requests * width, table_width=width, window=a.window, mixer=a.mixer)
 
     def tokens(n):
         return torch.randn(n, s.dim, generator=gen, device="cuda").bfloat16()
