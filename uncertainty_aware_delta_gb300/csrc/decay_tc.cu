@@ -22,6 +22,7 @@
 #include "decay.h"
 #include "decay_common.cuh"
 #include "kdn.h"
+#include "packed.cuh"
 #include "sm100.cuh"
 
 namespace kdn {
@@ -124,20 +125,6 @@ __device__ __forceinline__ void stmatrix_t(uint32_t a, uint32_t r0, uint32_t r1,
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                  : "memory");
 }
-// two fp32 operations an instruction
-typedef unsigned long long pair_t;
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<pair_t&>(d))
-        : "l"(reinterpret_cast<pair_t&>(a)), "l"(reinterpret_cast<pair_t&>(b)), "l"(reinterpret_cast<pair_t&>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<pair_t&>(d)) : "l"(reinterpret_cast<pair_t&>(a)), "l"(reinterpret_cast<pair_t&>(b)));
-    return d;
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x) { return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t x;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));

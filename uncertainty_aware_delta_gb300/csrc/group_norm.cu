@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "kdn.h"
+#include "packed.cuh"
 
 namespace kdn {
 namespace {
@@ -33,25 +34,21 @@ struct NormParams {
     int parts;                        // backward: rows of partial sums
 };
 
+constexpr int kPairs = kV / 2;
 template <typename T> struct Vec;     // eight channels, as they are in memory
 template <> struct Vec<__nv_bfloat16> {
     uint4 x;
     __device__ __forceinline__ void load(const void* p, long long i) {
         x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
-    __device__ __forceinline__ void get(float (&y)[kV]) const {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[2 * i] = __uint_as_float(w[i] << 16);
-            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    __device__ __forceinline__ void get(float2 (&y)[kPairs]) const {
+        y[0] = unpack2(x.x); y[1] = unpack2(x.y); y[2] = unpack2(x.z); y[3] = unpack2(x.w);
     }
-    __device__ __forceinline__ static void store(void* p, long long i, const float (&y)[kV]) {
+    __device__ __forceinline__ static void store(void* p, long long i, const float2 (&y)[kPairs]) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(y[j].x, y[j].y);
             w[j] = *reinterpret_cast<const uint32_t*>(&v);
         }
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -64,37 +61,49 @@ template <> struct Vec<float> {
         x = s[0];
         z = s[1];
     }
-    __device__ __forceinline__ void get(float (&y)[kV]) const {
-        y[0] = x.x; y[1] = x.y; y[2] = x.z; y[3] = x.w;
-        y[4] = z.x; y[5] = z.y; y[6] = z.z; y[7] = z.w;
+    __device__ __forceinline__ void get(float2 (&y)[kPairs]) const {
+        y[0] = make_float2(x.x, x.y); y[1] = make_float2(x.z, x.w);
+        y[2] = make_float2(z.x, z.y); y[3] = make_float2(z.z, z.w);
     }
-    __device__ __forceinline__ static void store(void* p, long long i, const float (&y)[kV]) {
+    __device__ __forceinline__ static void store(void* p, long long i, const float2 (&y)[kPairs]) {
         float4* s = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        s[0] = make_float4(y[0], y[1], y[2], y[3]);
-        s[1] = make_float4(y[4], y[5], y[6], y[7]);
+        s[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        s[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
     }
 };
 
-// 1 / (1 + exp(-x)).  The fast exponential is off by |x| 2^-23 of its value, which is nothing beside a rounding to bf16.
-template <typename T> __device__ __forceinline__ float sigmoid(float x) {
+__device__ __forceinline__ float reciprocal(float x) {
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.f + (sizeof(T) == 2 ? __expf(-x) : expf(-x))));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// 1 / (1 + exp(-x)).  The fast exponential is off by |x| 2^-23 of its value, which is nothing beside a rounding to bf16.
+template <typename T> __device__ __forceinline__ float2 sigmoid(float2 x) {
+    float2 e;
+    if (sizeof(T) == 2) {
+        e = mul2(x, both(-1.4426950408889634f));
+        asm("ex2.approx.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.f32 %0, %0;" : "+f"(e.y));
+    } else {
+        e = make_float2(expf(-x.x), expf(-x.y));
+    }
+    e = add2(e, both(1.f));
+    return make_float2(reciprocal(e.x), reciprocal(e.y));
 }
 
 // The activation of x, and its slope.
-template <typename T, int ACT> __device__ __forceinline__ float act(float x, float& slope) {
+template <typename T, int ACT> __device__ __forceinline__ float2 act(float2 x, float2& slope) {
     if (ACT == KDN_ACT_NONE) {
-        slope = 1.f;
+        slope = both(1.f);
         return x;
     }
-    const float h = sigmoid<T>(x);
+    const float2 h = sigmoid<T>(x), rest = fma2(h, both(-1.f), both(1.f));
     if (ACT == KDN_ACT_SIGMOID) {
-        slope = h * (1.f - h);
+        slope = mul2(h, rest);
         return h;
     }
-    slope = h * fmaf(x, 1.f - h, 1.f);
-    return x * h;
+    slope = mul2(h, fma2(x, rest, both(1.f)));
+    return mul2(x, h);
 }
 
 // Sum over the lanes of a group (LANES: how many, 0: `lanes`).
@@ -125,15 +134,31 @@ __device__ __forceinline__ Place place_of(const NormParams& P) {
     return p;
 }
 
+// A thread's channels of a weight or bias [groups, d].
+__device__ __forceinline__ void parameters(const float* x, const Place& p, int d, float other, float2 (&y)[kPairs]) {
+    const float* at = x + p.g * d + p.c;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) y[i] = x && p.mine ? make_float2(at[2 * i], at[2 * i + 1]) : both(other);
+}
+// Deviations from a group's mean, in place; returns 1 / sigma.
+template <int LANES> __device__ __forceinline__ float normalise(float2 (&x)[kPairs], bool mine, float inv, float eps, int lanes) {
+    float2 sum = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+    const float mean = group_sum<LANES>(sum.x + sum.y, lanes) * inv;
+    float2 sq = both(0.f);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        x[i] = add2(x[i], both(-mean));
+        sq = fma2(x[i], x[i], sq);
+    }
+    return rsqrtf(group_sum<LANES>(mine ? sq.x + sq.y : 0.f, lanes) * inv + eps);
+}
+
 template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost) group_norm_kernel(const __grid_constant__ NormParams P) {
     const NormArgs& A = P.a;
     const Place p = place_of(P);
-    float w[kV], b[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        w[i] = A.w && p.mine ? A.w[p.g * A.d + p.c + i] : 1.f;
-        b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
-    }
+    float2 w[kPairs], b[kPairs];
+    parameters(A.w, p, A.d, 1.f, w);
+    parameters(A.b, p, A.d, 0.f, b);
     const float inv = 1.f / A.d;
     // kAt rows at a time, their loads ahead of all else (all lanes of a warp go on together: the sums are shuffles)
     for (int row = p.row; __any_sync(kAll, row < A.rows); row += kAt<T> * p.step) {
@@ -152,25 +177,16 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
         for (int e = 0; e < kAt<T>; ++e) {
             const int r = row + e * p.step;
             const bool mine = p.mine && r < A.rows;
-            float x[kV];
+            float2 x[kPairs];
             v[e].get(x);
-            float sum = 0.f, sq = 0.f;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) sum += x[i];
-            const float mean = group_sum<LANES>(sum, P.lanes) * inv;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                x[i] -= mean;
-                sq = fmaf(x[i], x[i], sq);
-            }
-            const float rstd = rsqrtf(group_sum<LANES>(mine ? sq : 0.f, P.lanes) * inv + A.eps);
+            const float rstd = normalise<LANES>(x, mine, inv, A.eps, P.lanes);
             if (mine) {
-                float z[kV], slope;
+                float2 z[kPairs], slope;
                 if (GATE) gate[e].get(z);
 #pragma unroll
-                for (int i = 0; i < kV; ++i) {
-                    const float n = fmaf(x[i] * rstd, w[i], b[i]);
-                    x[i] = GATE ? n * act<T, ACT>(z[i], slope) : act<T, ACT>(n, slope);
+                for (int i = 0; i < kPairs; ++i) {
+                    const float2 n = fma2(mul2(x[i], both(rstd)), w[i], b[i]);
+                    x[i] = GATE ? mul2(n, act<T, ACT>(z[i], slope)) : act<T, ACT>(n, slope);
                 }
                 Vec<T>::store(A.y, (static_cast<long long>(r) * A.groups + p.g) * A.d + p.c, x);
             }
@@ -182,12 +198,9 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     const NormArgs& A = P.a;
     const Place p = place_of(P);
     if (blockIdx.x + blockIdx.y + threadIdx.x == 0) *A.status = 0;
-    float w[kV], b[kV], dw[kV] = {}, db[kV] = {};
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        w[i] = A.w && p.mine ? A.w[p.g * A.d + p.c + i] : 1.f;
-        b[i] = A.b && p.mine ? A.b[p.g * A.d + p.c + i] : 0.f;
-    }
+    float2 w[kPairs], b[kPairs], dw[kPairs] = {}, db[kPairs] = {};
+    parameters(A.w, p, A.d, 1.f, w);
+    parameters(A.b, p, A.d, 0.f, b);
     const float inv = 1.f / A.d;
     // the next kNext rows' loads are under way while a row is worked on
     Vec<T> v[kNext<T>] = {}, u[kNext<T>] = {}, t[kNext<T>] = {};
@@ -205,49 +218,39 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     for (int e = 0; e < kNext<T>; ++e) {
         const int row = row0 + e * p.step;
         const bool mine = p.mine && row < A.rows;
-        float x[kV], y[kV], z[kV];
+        float2 x[kPairs], y[kPairs], z[kPairs];
         v[e].get(x);
         u[e].get(y);
         if (GATE) t[e].get(z);
         fetch(row + kNext<T> * p.step, e);
-        float sum = 0.f, sq = 0.f;
+        const float rstd = normalise<LANES>(x, mine, inv, A.eps, P.lanes);
+        float2 t1 = both(0.f), t2 = t1;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum += x[i];
-        const float mean = group_sum<LANES>(sum, P.lanes) * inv;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            x[i] -= mean;
-            sq = fmaf(x[i], x[i], sq);
-        }
-        const float rstd = rsqrtf(group_sum<LANES>(mine ? sq : 0.f, P.lanes) * inv + A.eps);
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float xh = x[i] * rstd, n = fmaf(xh, w[i], b[i]);
-            float slope, dn;
+        for (int i = 0; i < kPairs; ++i) {
+            const float2 xh = mul2(x[i], both(rstd)), n = fma2(xh, w[i], b[i]);
+            float2 slope, dn;
             if (GATE) {
-                const float f = act<T, ACT>(z[i], slope);
-                z[i] = y[i] * n * slope;
-                dn = y[i] * f;
+                const float2 f = act<T, ACT>(z[i], slope);
+                z[i] = mul2(mul2(y[i], n), slope);
+                dn = mul2(y[i], f);
             } else {
                 act<T, ACT>(n, slope);
-                dn = y[i] * slope;
+                dn = mul2(y[i], slope);
             }
             if (mine) {
-                dw[i] = fmaf(dn, xh, dw[i]);
-                db[i] += dn;
+                dw[i] = fma2(dn, xh, dw[i]);
+                db[i] = add2(db[i], dn);
             }
             x[i] = xh;
-            y[i] = dn * w[i];
-            s1 += y[i];
-            s2 = fmaf(y[i], xh, s2);
+            y[i] = mul2(dn, w[i]);
+            t1 = add2(t1, y[i]);
+            t2 = fma2(y[i], xh, t2);
         }
-        s1 = group_sum<LANES>(mine ? s1 : 0.f, P.lanes) * inv;
-        s2 = group_sum<LANES>(mine ? s2 : 0.f, P.lanes) * inv;
+        const float s1 = group_sum<LANES>(mine ? t1.x + t1.y : 0.f, P.lanes) * inv, s2 = group_sum<LANES>(mine ? t2.x + t2.y : 0.f, P.lanes) * inv;
         if (!mine) continue;
         const long long at = (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) y[i] = rstd * (y[i] - s1 - x[i] * s2);
+        for (int i = 0; i < kPairs; ++i) y[i] = mul2(both(rstd), fma2(x[i], both(-s2), add2(y[i], both(-s1))));
         Vec<T>::store(A.dx, at, y);
         if (GATE) Vec<T>::store(A.dgate, at, z);
     }
