@@ -141,6 +141,32 @@ def test_strided_rows(io, d):
     assert all(torch.equal(a[n], b[n]) for n in a)
 
 
+@pytest.mark.parametrize("io,d", [("f32", 64), ("bf16", 128), ("bf16", 64)])
+def test_heads_outermost(io, d):
+    """[H, tokens, d] in memory; one head, and one token a sequence, whose strides mean nothing."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    H, T = 3, 130
+    q, k, v, dO = (torch.randn(H, T, d, device="cuda").to(IO[io]).transpose(0, 1)[None] for _ in range(4))
+    l, S0 = torch.tensor([-0.01, -0.3, 0.0], device="cuda"), torch.randn(1, H, d, d, device="cuda")
+    dense = [t.contiguous() for t in (q, k, v)]
+    for a, b in zip(kdn.kdn_decay_forward(q, k, v, l, S0), kdn.kdn_decay_forward(*dense, l, S0)):
+        assert torch.equal(a, b)
+    a, b = kdn.kdn_decay_backward(q, k, v, l, S0, dO, S0), kdn.kdn_decay_backward(*dense, l, S0, dO.contiguous(), S0)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    wide = torch.randn(5, 1, 1, 3 * d, device="cuda").to(IO[io])
+    args = lambda t: (t[..., :d], t[..., d:2 * d], t[..., 2 * d:])   # noqa: E731
+    S0 = torch.randn(5, 1, d, d, device="cuda")
+    for a, b in zip(kdn.kdn_decay_forward(*args(wide), l[:1], S0), kdn.kdn_decay_forward(*(t.contiguous() for t in args(wide)), l[:1], S0)):
+        assert torch.equal(a, b)
+    # rows that overlap, or sequences that do not lie one after another, are refused
+    with pytest.raises((ValueError, kdn.KDNError)):
+        kdn.kdn_decay_forward(dense[0].expand(2, T, H, d), *(t.expand(2, T, H, d) for t in dense[1:]), l)
+    two = torch.randn(2, 200, H, d, device="cuda").to(IO[io])[:, :T]
+    with pytest.raises(ValueError, match="one after another"):
+        kdn.kdn_decay_forward(two, two, two, l)
+
+
 @pytest.mark.parametrize("io,dk,dv", [("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 128), ("f32", 16, 32)])
 def test_steps_continue_a_prompt(io, dk, dv):
     """A prompt, its last tokens one at a time: the whole sequence's outputs and state."""
