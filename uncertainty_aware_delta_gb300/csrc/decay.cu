@@ -10,6 +10,12 @@
 // All powers are of whole numbers >= 0, so none overflows for g <= 1, and g = 0 (log_decay = -infinity) is a memory of the
 // token alone.  What is masked is left out by a choice, not by a factor of zero, so that a later token's infinity or NaN
 // stays out of earlier rows.
+//
+// Measured: 8 x 4096 tokens, 16 heads, fp32: heads of 128 1306 us (floor 158), of 64 526 (79), of 32 237 (40); bf16, heads
+// of 32, 211 (20).  What bounds it: 3xTF32 on warp-level MMAs (2112 of them a chunk of 32 tokens and 64 value channels for
+// heads of 128) and the splitting of every fragment in two, which is two thirds of the instructions; bf16 operands are one
+// TF32 part, so that of two sides at most one is split (heads of 32: 341 us when both were).  Gradients of 3 x 777 tokens,
+// 4 heads of 64 and 128 in fp32: 115 us in segments of 192 tokens (489 whole, before the products were rearranged).
 
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -453,6 +459,8 @@ DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t 
 
 // ---------------------------------------------------------------- one token a sequence
 // S = g S + k v^T, o = S^T q: a head a block, its state read once into registers, written once, and summed over the rows.
+// Bound by the state's bytes: 256 sequences of 16 heads, 128 x 128, 88 us, 6.2 TB/s, 91% of the copy rate (two blocks an SM
+// have 128 KB on their way).
 constexpr int kRegs = 16;   // float4 of the state a thread, for 128 x 128
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)

@@ -7,6 +7,11 @@
 // A group's channels lie in neighbouring lanes, eight a lane, so its sums are a few shuffles and x is read once.  A thread
 // keeps its channels from token to token: weights stay in registers, and the gradients of weights are sums in registers,
 // written once a block and joined by a second kernel in a fixed order.
+//
+// Measured on 32768 tokens of 16 groups of 128, bf16, SiLU of a gate: 74 us, 5.5 TB/s, 80% of the copy rate (one row of a
+// thread at a time 108, two 90, four 74); gradients 121 us, 5.5 TB/s (115 the first kernel; 175 with a row at a time and full
+// exponentials; blocks of four an SM 171, of three 154, of two, each with two rows' loads ahead, 121).  Bound by the bytes, and by
+// the instructions that come with them: issue slots are busy for 65% of the time, and 75% in the gradients.
 
 #include <cuda_bf16.h>
 #include <algorithm>
