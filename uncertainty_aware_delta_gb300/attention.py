@@ -16,6 +16,7 @@ from .binding import KDN_BF16, KDN_F32, KDNError, library
 
 _IO = {torch.bfloat16: KDN_BF16, torch.float32: KDN_F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone, without a Stream object
+_current_device = torch._C._cuda_getDevice          # CUDA is up: a tensor of its has been looked at
 
 
 class CachePlan(NamedTuple):
@@ -84,7 +85,7 @@ def _call(fn, device, stream, args, scratch=()):
             for t in scratch:
                 t.record_stream(stream)
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -97,7 +98,8 @@ def _workspace(given, need, device, made):
     if given is None:
         given = torch.empty(need, dtype=torch.uint8, device=device)
         made.append(given)
-    elif given.device != device:
+        return given.data_ptr(), need
+    if given.device != device:
         raise ValueError(f"workspace is on {given.device}, expected {device}")
     elif not given.is_contiguous():
         raise ValueError("workspace must be contiguous")

@@ -49,6 +49,8 @@ def library_path() -> str:
 def library():
     """Load libkdn.so (once); raises if it has not been built."""
     global _lib
+    if _lib is not None:   # (set when all its prototypes are)
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_PATH):

@@ -15,7 +15,7 @@
 // of 32, 211 (20).  What bounds it: 3xTF32 on warp-level MMAs (2112 of them a chunk of 32 tokens and 64 value channels for
 // heads of 128) and the splitting of every fragment in two, which is two thirds of the instructions; bf16 operands are one
 // TF32 part, so that of two sides at most one is split (heads of 32: 341 us when both were).  Gradients of 3 x 777 tokens,
-// 4 heads of 64 and 128 in fp32: 115 us in segments of 192 tokens (489 whole, before the products were rearranged).
+// 4 heads of 64 and 128 in fp32: 112 us in segments of 192 tokens (489 whole, before the products were rearranged).
 
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -398,8 +398,12 @@ template <int DK, int DVS> cudaError_t start_io(const DecayParams& P, int n_jobs
 }
 
 template <int DK> cudaError_t start_dv(const DecayParams& P, int n_jobs, cudaStream_t s) {
-    if (P.job[0].dv == 16) return start_io<DK, 16>(P, n_jobs, s);
-    if (P.job[0].dv == 32) return start_io<DK, 32>(P, n_jobs, s);
+    const int dv = P.job[0].dv;
+    if (dv == 16) return start_io<DK, 16>(P, n_jobs, s);
+    // 64 value channels a block, or 32 where that gives at most two blocks an SM: a chunk is then worked on in less time (fp32
+    // gradients of 3 x 777, 4 heads of 128: 112 us for 117).  Where there are more blocks, each one's weights would be made twice.
+    const long long blocks = static_cast<long long>(P.items) * P.H * n_jobs * (dv / 32);
+    if (dv == 32 || blocks <= 2 * kSMs) return start_io<DK, 32>(P, n_jobs, s);
     return start_io<DK, 64>(P, n_jobs, s);
 }
 

@@ -16,7 +16,7 @@
 //
 // Measured: 8 sequences of 4096 tokens, 16 heads of 128, 107 us, 5.1 TB/s of what it has to move, 76% of the copy rate
 // on 128 of the 152 SMs (the first form, with the roles' loops unrolled and values read one by one, 250); its gradients 303 us
-// (three walks, 384 blocks: two and a half turns of the SMs); 65536 tokens alone 299 (states 98, chaining 5, outputs 175); 24 of 2
+// (three walks, 384 blocks: two and a half turns of the SMs); 65536 tokens alone 292 to 299 (states 98, chaining 5, outputs 175); 24 of 2
 // to 4095, heads of 64, 93 (the longest one's 64 chunks).  A chunk takes 1.5 us for heads of 128 and 1.35 for heads of 64, where
 // its bytes would take 1.24 and its products 0.7.  What bounds it is the chain of the roles: V' (some 260 instructions a warp and
 // chunk, five cycles each, as an SM's quarter has five warps, all of other roles), the state, the outputs, and what a barrier takes
@@ -24,7 +24,8 @@
 // anywhere helps a little (left out of copies of this file: the weights' arithmetic 7 us, W's products 8, a part and a half
 // of V' 11, the stores 3); longer code costs more than it saves, as the roles' loops hardly fit the instruction caches
 // (V' unrolled, and computed ahead of its turn: 116 us for 106).  Also slower: looking at barriers without suspension (128 for
-// 118), tiles asked for into L2 ahead (119 to 141 for 118), copies asked for by the warps that issue products (see the loader).
+// 118), tiles asked for into L2 ahead (119 to 141 for 118), copies asked for by the warps that issue products (see the loader).  No
+// faster for heads of 64: TMEM for V' of two chunks (89.3 us for 88.2), or for outputs of two (88.8).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -423,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_kernel(const __grid_cons
                 if (loads && n > 0 && sent < chunks && !aborted) load();
                 __syncwarp();
             }
-            // copies already issued land before the block's shared memory goes away
-            if (loads && aborted)
+            // copies already issued land before the block's shared memory goes away (where there are outputs, a walk that was not
+            // given up has waited for all of them here)
+            if (loads && (aborted || !OUT))
                 for (int i = max(sent - kStages, 0); i < sent; ++i) mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1, kWaitLimit);
         }
     } else if (warp < 8) {
