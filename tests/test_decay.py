@@ -56,6 +56,24 @@ def test_bf16(dk, dv, T):
     check_all([T] * 2, 3, dk, dv, "bf16", False)
 
 
+@pytest.mark.parametrize("T", [1, 5, 31, 32])
+def test_short_sequences(T):
+    """Dense, heads of 64: the same bits as on CUDA cores, which work on them; packed ones are on tensor cores."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    check_all([T] * 5, 3, 64, 64, "bf16", True)
+    x = inputs([T] * 5, 3, 64, 64, "bf16", False)
+    args, dO, dS = tuple(x[n] for n in ("q", "k", "v", "log_decay", "S0")), x["dO"], x["dS"]
+    for a, b in zip(*(kdn.kdn_decay_forward(*args, flags=f) for f in (0, kdn.KDN_FLAG_PORTABLE))):
+        assert torch.equal(a, b)
+    a, b = (kdn.kdn_decay_backward(*args, dO, dS, flags=f) for f in (0, kdn.KDN_FLAG_PORTABLE))
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    want, size = ref.forward(*args)
+    o, S = kdn.kdn_decay_forward(*args)
+    ref.check(o, want[0], size[0], False, "o")
+    ref.check(S, want[1], size[1], False, "S_T")
+
+
 @pytest.mark.parametrize("io,dk,dv,flags", [("f32", 64, 32, 0), ("bf16", 128, 128, 0), ("bf16", 64, 64, 0), ("bf16", 128, 64, 1)])
 def test_packed(io, dk, dv, flags):
     check_all([5, 0, 130, 1, 64, 97, 0], 2, dk, dv, io, True, flags)

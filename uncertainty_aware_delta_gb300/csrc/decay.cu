@@ -431,6 +431,12 @@ cudaError_t start_pass(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s
 }
 
 bool use_tc(int io, int dk, int dv, uint32_t flags) { return !(flags & KDN_FLAG_PORTABLE) && decay_tc_supported(io, dk, dv); }
+// Heads of 64 in dense sequences of one chunk of the CUDA cores: a tensor-core block, one an SM, has taken some 5 us before its first
+// chunk is through.  256 sequences of 1 to 32 tokens, 16 heads: forward 99 to 105 us for 145, gradients 210 to 237 for 405; of 64
+// tokens 152 for 145.  (Heads of 128: 307 to 323 for 194 to 199.  Packed sequences may have a long one among them.)
+bool short_ones(const DecayArgs& a) {
+    return !a.cu && a.job[0].dk == 64 && a.job[0].dv == 64 && a.n_tok <= static_cast<long long>(kC) * a.n_seq;
+}
 
 // Sequences are cut where there are at most half as many of them as blocks that run at a time.  (Packed ones may be of any
 // lengths, and a long one among many is worked on alone in the end: 24 of 2 to 4095 tokens, 16 heads of 64, take 95 us, of
@@ -525,7 +531,7 @@ size_t decay_scratch(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     const int dk = a.job[0].dk, dv = a.job[0].dv;
-    const bool tc = use_tc(a.io, dk, dv, a.flags) && a.n_tok > 0;
+    const bool tc = use_tc(a.io, dk, dv, a.flags) && a.n_tok > 0 && !short_ones(a);
     const DecayPlan plan = plan_of(a.n_seq, a.n_tok, a.H, dk, dv, a.io, a.flags, a.cu != nullptr, a.n_jobs);
     DecayParams P = {};
     for (int i = 0; i < a.n_jobs; ++i) {
