@@ -76,18 +76,20 @@ def kdn_decay_forward(q, k, v, log_decay, S0=None, *, cu=None, flags=0, out=None
     n, cu_ptr = _sequences(q, cu, device)
     keys, dv, f32 = q.shape, v.shape[-1], torch.float32
     shape, tok, dt = (*keys[:-1], dv), _int(tok, "tokens"), q.dtype
-    made = []
+    states = (n, H, dk, dv)
     if out is None:
-        made = [torch.empty(shape, dtype=dt, device=device), torch.empty((n, H, dk, dv), dtype=f32, device=device)]
-        out = tuple(made)
-    o, S_T = out
+        made = [torch.empty(shape, dtype=dt, device=device), torch.empty(states, dtype=f32, device=device)]
+        o, S_T = made
+        outs = o.data_ptr(), S_T.data_ptr()
+    else:
+        made, (o, S_T) = [], out
+        outs = _tensor(o, "o", dt, shape, device), _tensor(S_T, "S_T", f32, states, device)
     need = lib.kdn_decay_workspace_size(n, tok, H, dk, dv, io, flags)
     ws, ws_bytes = _workspace(workspace, need, device, made)
     _call(lib.kdn_decay_forward, device, stream,
           (n, tok, H, dk, dv, io, flags, *_operand(q, "q", dt, keys, device), *_operand(k, "k", dt, keys, device),
            *_operand(v, "v", dt, shape, device), _tensor(log_decay, "log_decay", f32, (H,), device),
-           _maybe(S0, "S0", f32, (n, H, dk, dv), device), cu_ptr, _tensor(o, "o", dt, shape, device),
-           _tensor(S_T, "S_T", f32, (n, H, dk, dv), device), ws, ws_bytes), made)
+           _maybe(S0, "S0", f32, states, device), cu_ptr, *outs, ws, ws_bytes), made)
     return o, S_T
 
 
@@ -100,10 +102,13 @@ def kdn_decay_step(q, k, v, log_decay, S, *, o=None, stream=None):
     if o is None:
         o = torch.empty((B, H, dv), dtype=q.dtype, device=device)
         made.append(o)
+        out = o.data_ptr()
+    else:
+        out = _tensor(o, "o", q.dtype, (B, H, dv), device)
     _call(library().kdn_decay_step, device, stream,
           (_int(B, "B"), H, dk, dv, io, _tensor(q, "q", q.dtype, (B, H, dk), device), _tensor(k, "k", q.dtype, (B, H, dk), device),
            _tensor(v, "v", q.dtype, (B, H, dv), device), _tensor(log_decay, "log_decay", torch.float32, (H,), device),
-           _tensor(S, "S", torch.float32, (B, H, dk, dv), device), _tensor(o, "o", q.dtype, (B, H, dv), device)), made)
+           _tensor(S, "S", torch.float32, (B, H, dk, dv), device), out), made)
     return o
 
 
@@ -147,11 +152,14 @@ def kdn_group_norm(x, weight=None, bias=None, *, gate=None, act="none", eps=1e-5
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=device)
         made.append(out)
+        y = out.data_ptr()
+    else:
+        y = _tensor(out, "out", x.dtype, shape, device)
     gates = (None, 0, 0) if gate is None else _operand(gate, "gate", x.dtype, shape, device)
     _call(library().kdn_group_norm, device, stream,
           (_int(rows, "rows"), G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
            _maybe(weight, "weight", torch.float32, (G, d), device), _maybe(bias, "bias", torch.float32, (G, d), device), *gates,
-           _tensor(out, "out", x.dtype, shape, device)), made)
+           y), made)
     return out
 
 
