@@ -481,7 +481,7 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *          weights g^(i-j) (q_i k_j) and the state that a chunk begins with are rounded to bf16 for
  *          their products with v and q; what is added to the state is not (g^(m-1-j) v_j goes in as
  *          three bf16 parts), and the state itself is fp32.
- *          Few sequences' heads, and packed sequences much longer than the others, are cut into segments
+ *          Few long sequences' heads, and packed sequences much longer than the others, are cut into segments
  *          that run side by side, as those of the mixer's forward (KDN_FLAG_NO_SPLIT: they are not).
  * Workspace: kdn_decay_workspace_size() bytes; its first 256 hold the status word.
  */

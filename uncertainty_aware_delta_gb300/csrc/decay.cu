@@ -438,32 +438,75 @@ bool short_ones(const DecayArgs& a) {
     return !a.cu && a.job[0].dk == 64 && a.job[0].dv == 64 && a.n_tok <= static_cast<long long>(kC) * a.n_seq;
 }
 
-// Sequences are cut where there are at most half as many of them as blocks that run at a time.  (Packed ones may be of any
-// lengths, and a long one among many is worked on alone in the end: 24 of 2 to 4095 tokens, 16 heads of 64, take 95 us, of
-// which the longest alone is 90.  Cut into segments of an SM's share of all tokens they took 119: 27 more for the states, 11 for
-// the chaining, and the outputs still 75, as every block has some 5 us before its first chunk is through.)  A segment has
-// a whole number of chunks of both paths.
+// Tokens of a dense sequence's segments, or none (0) where it is faster whole.  The segments' states take some six tenths of the time
+// of their outputs, chaining them 0.3 us a segment, and the launches 9 to 13.  Measured with 420 calls (1 to 5 sequences of 250 to
+// 8000 tokens, 2 to 16 heads of 32, 64 and 128, both directions, each whole and with up to nine lengths of segments): this rule's choice
+// takes 1 to 2% more than the best on average, 27% at most; cutting wherever at most half as many blocks would be at work, into
+// segments of at least 512 tokens (128 on CUDA cores), 6 to 12%, and 85 at most.  8 heads of 64: bf16, 1000 tokens 25 us for 29 whole, 500
+// tokens 20 for 18; fp32, 500 tokens 21 for 37, 250 tokens 19 for 20.
+int dense_segment(long long sequences, int T, int H, int dk, int dv, bool tc, int jobs) {
+    // the gradients' jobs are two (of dv keys and dk values) and one in a launch where dk and dv differ
+    const bool two = jobs == 3 && dk != dv;
+    const int count[2] = {two ? 2 : jobs, 1}, keys[2] = {two ? dv : dk, dk}, values[2] = {two ? dk : dv, dv};
+    const long long n = (T + 63) / 64, heads = sequences * H;
+    // segments that run at a time (two blocks of 64 channels an SM on CUDA cores), but no more than chaining them is worth
+    long long blocks = 0;
+    for (int i = 0; i <= two; ++i) blocks = std::max(blocks, heads * count[i] * (tc ? 1 : std::max(1, values[i] / 64)));
+    const long long fill = (tc ? kSMs : 2 * kSMs) / blocks;
+    if (fill < 2) return 0;
+    const long long least = std::max(std::max(1ll, static_cast<long long>(sqrt(n / 7.))), (n + fill - 1) / fill);
+    if (least >= n) return 0;
+    if (tc) return n > 1.7 * least + 0.25 * n / least + 9 ? static_cast<int>(64 * least) : 0;   // in chunks of a whole walk, 1.2 us
+    // a walk's chunks in segments of `len` times 64 tokens
+    const auto time = [&](long long len) {
+        const long long nseg = (n + len - 1) / len;
+        double sum = 0;
+        for (int i = 0; i <= two; ++i) {
+            // blocks of 32 channels, or of 64 (start_dv), and the time of their chunks to that with a block of 32 an SM
+            const long long b = heads * count[i] * std::max(1, values[i] / 32) * nseg;
+            const double load = b <= kSMs                             ? 1.
+                                : b <= 2 * kSMs || values[i] <= 32    ? 1.7 * ((b + 2 * kSMs - 1) / (2 * kSMs))
+                                : b / 2 <= kSMs                       ? 2.
+                                                                      : 2.8 * std::max(1., b / 2 / (2. * kSMs));
+            sum += 2 * len * (0.8 + 0.022 * keys[i]) * load;
+        }
+        return nseg == 1 ? sum : 13 + 0.3 * nseg + 1.6 * sum;
+    };
+    long long len = least;
+    for (const long long x : {least + 1, 2 * least})
+        if (x < n && time(x) < time(len)) len = x;
+    return time(len) < 0.97 * time(n) ? static_cast<int>(64 * len) : 0;
+}
+
+// Dense sequences are cut where that is faster, packed ones where there are at most half as many of them as blocks that run at
+// a time.  (Packed ones may be of any lengths, and a long one among many is worked on alone in the end: 24 of 2 to 4095 tokens,
+// 16 heads of 64, take 95 us, of which the longest alone is 90.  Cut into segments of an SM's share of all tokens they took 119: 27
+// more for the states, 11 for the chaining, and the outputs still 75, as every block has some 5 us before its first chunk is
+// through.)  A segment has a whole number of chunks of both paths.
 DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
     DecayPlan p = {false, 0, 1, n_seq, 0};
     if ((flags & KDN_FLAG_NO_SPLIT) || n_seq <= 0 || n_tok <= 0 || H <= 0) return p;
     const bool tc = use_tc(io, dk, dv, flags);
-    const int most = std::max(dk, dv);
-    // blocks a segment in one launch (the gradients' jobs are two and one where dk and dv differ), and that run at a time
-    const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (most + 63) / 64),
-                    room = tc ? kSMs : 2 * kSMs, longest = packed ? n_tok : n_tok / n_seq;
-    // a segment's two passes and the chaining have to be worth their launches, and what the tensor cores' blocks take to begin
-    const int shortest = tc ? 512 : 128;
-    if (2 * per * n_seq > room) return p;
-    const long long n = packed ? room / per - n_seq : room / per / n_seq;
-    long long len = (longest + n - 1) / n;   // of a segment
-    len = std::max<long long>(shortest, (len + 63) / 64 * 64);
-    if (len >= longest) return p;
+    long long len;   // of a segment
+    if (packed) {
+        // blocks a segment in one launch, and that run at a time
+        const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (std::max(dk, dv) + 63) / 64),
+                        room = tc ? kSMs : 2 * kSMs;
+        if (2 * per * n_seq > room) return p;
+        const long long n = room / per - n_seq;
+        len = std::max<long long>(tc ? 512 : 128, ((n_tok + n - 1) / n + 63) / 64 * 64);
+        if (len >= n_tok) return p;
+        // (a sequence has at most its tokens / len + 1 segments, and only one longer than len more than one)
+        p.items = static_cast<int>(n_tok / len) + n_seq;
+        p.slots = static_cast<int>(n_tok / len + std::min<long long>(n_tok / len, n_seq));
+    } else {
+        len = dense_segment(n_seq, n_tok / n_seq, H, dk, dv, tc, n_jobs);
+        if (len == 0) return p;
+        p.nseg = static_cast<int>((n_tok / n_seq + len - 1) / len);
+        p.items = p.slots = n_seq * p.nseg;
+    }
     p.split = true;
     p.seg_len = static_cast<int>(len);
-    p.nseg = static_cast<int>((longest + len - 1) / len);
-    // (packed: a sequence has at most len / seg_len + 1 segments, and only one longer than seg_len more than one)
-    p.items = packed ? static_cast<int>(n_tok / len) + n_seq : n_seq * p.nseg;
-    p.slots = packed ? static_cast<int>(n_tok / len + std::min<long long>(n_tok / len, n_seq)) : p.items;
     return p;
 }
 
@@ -530,7 +573,7 @@ size_t decay_scratch(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32
 }
 
 cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
-    const int dk = a.job[0].dk, dv = a.job[0].dv;
+    const int dk = a.job[a.n_jobs - 1].dk, dv = a.job[a.n_jobs - 1].dv;   // (the call's: those of the first gradients' jobs change places)
     const bool tc = use_tc(a.io, dk, dv, a.flags) && a.n_tok > 0 && !short_ones(a);
     const DecayPlan plan = plan_of(a.n_seq, a.n_tok, a.H, dk, dv, a.io, a.flags, a.cu != nullptr, a.n_jobs);
     DecayParams P = {};
