@@ -275,6 +275,23 @@ def test_bounds_out_of_order(io, d):
     assert torch.equal(S[2], x["S0"][2]) and torch.equal(S[:2], good[1][:2]) and bool((o[130:] == 7).all())
 
 
+@pytest.mark.parametrize("io,d", [("f32", 32), ("f32", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("T", [1, 40, 1300])
+def test_status_word(io, d, T):
+    """Whatever the workspace held before: nothing found is zero, on every path, whole and in segments."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    x = inputs([T], 1, d, d, io, False)
+    args = tuple(x[n] for n in ("q", "k", "v", "log_decay", "S0"))
+    sizes = (1, T, 1, d, d, int(io == "bf16"))
+    ws = torch.full((kdn.decay_workspace_size(*sizes),), 255, dtype=torch.uint8, device="cuda")
+    kdn.kdn_decay_forward(*args, workspace=ws)
+    assert kdn.kdn_read_device_status(ws) == 0
+    ws = torch.full((kdn.decay_backward_workspace_size(*sizes),), 255, dtype=torch.uint8, device="cuda")
+    kdn.kdn_decay_backward(*args, x["dO"], x["dS"], workspace=ws)
+    assert kdn.kdn_read_device_status(ws) == 0
+
+
 def test_nothing_to_do():
     import uncertainty_aware_delta_gb300 as kdn
 

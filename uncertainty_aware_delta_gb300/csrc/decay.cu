@@ -15,7 +15,7 @@
 // of 32, 211 (20).  What bounds it: 3xTF32 on warp-level MMAs (2112 of them a chunk of 32 tokens and 64 value channels for
 // heads of 128) and the splitting of every fragment in two, which is two thirds of the instructions; bf16 operands are one
 // TF32 part, so that of two sides at most one is split (heads of 32: 341 us when both were).  Gradients of 3 x 777 tokens,
-// 4 heads of 64 and 128 in fp32: 112 us in segments of 192 tokens (489 whole, before the products were rearranged).
+// 4 heads of 64 and 128 in fp32: 110 us in segments of 192 tokens (100 in a graph; 148 whole).
 
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -585,8 +585,8 @@ cudaError_t launch_decay(const DecayArgs& a, cudaStream_t s) {
     P.n_seq = a.n_seq; P.n_tok = a.n_tok; P.H = a.H; P.io = a.io;
     P.nseg = plan.nseg; P.seg_len = plan.seg_len; P.slots = plan.slots;
     P.probe = (a.flags & KDN_FLAG_TIMEOUT_PROBE) ? 1 : 0;
-    // the status word: where the first kernel cannot write it without a race, by a call of its own
-    P.clear = !a.cu && !tc && !plan.split;
+    // the status word: where a kernel may find something, by a call of its own (else the kernels clear it)
+    P.clear = !a.cu && !tc;
     cudaError_t e = cudaSuccess;
     if (!P.clear && (e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;
     if (plan.split) {
