@@ -478,35 +478,38 @@ int dense_segment(long long sequences, int T, int H, int dk, int dv, bool tc, in
     return time(len) < 0.97 * time(n) ? static_cast<int>(64 * len) : 0;
 }
 
-// Dense sequences are cut where that is faster, packed ones where there are at most half as many of them as blocks that run at
-// a time.  (Packed ones may be of any lengths, and a long one among many is worked on alone in the end: 24 of 2 to 4095 tokens,
-// 16 heads of 64, take 95 us, of which the longest alone is 90.  Cut into segments of an SM's share of all tokens they took 119: 27
-// more for the states, 11 for the chaining, and the outputs still 75, as every block has some 5 us before its first chunk is
-// through.)  A segment has a whole number of chunks of both paths.
+// The same for packed sequences, whose lengths the host does not know.  The longest has at least their mean, so where dense ones of
+// the mean would be cut, they are.  Else, of six or more, one may be far longer than the others and be worked on alone in the end:
+// segments a quarter longer than the mean leave sequences of about one length whole, which costs them the launches (some 6 us).
+// 2000 tokens and 7 times 20, 4 heads of 64, fp32: 53 us for 139 whole; 8000 and 9 times 100, 8 heads of 64, bf16: 59 for 159;
+// 16 times 300, 4 heads of 128, fp32: 79 for 70 (145 when cut).  Where all sequences' heads fill the GPU they are not cut: 24 of 2 to
+// 4095 tokens, 16 heads of 64, take 93, of which the longest alone is 90; in segments of an SM's share of all tokens they took 119 (27
+// more for the states, 11 for the chaining, the outputs still 75, as every block has some 5 us before its first chunk is through).
+long long packed_segment(int n_seq, int n_tok, int H, int dk, int dv, bool tc, int jobs) {
+    const int len = dense_segment(n_seq, n_tok / n_seq, H, dk, dv, tc, jobs);
+    if (len > 0 || n_seq < 6) return len;
+    const int most = std::max(dk, dv);
+    const long long n = (n_tok + 63) / 64, per = static_cast<long long>(H) * (jobs == 3 && dk != dv ? 2 : jobs) * (tc ? 1 : std::max(1, most / 64));
+    const long long fill = (tc ? kSMs : 2 * kSMs) / per - n_seq;
+    const double alone = tc ? 9 + 1.2 * n : 2 * n * (0.8 + 0.022 * most);   // one of all tokens, us
+    if (fill < 2 || alone < (tc ? 50 : 100)) return 0;
+    const long long least = std::max(static_cast<long long>(sqrt(n / 7.)), (n + fill - 1) / fill);
+    return 64 * std::max(least, (n_tok / n_seq * 5ll / 4 + 63) / 64);
+}
+
+// Sequences are cut into segments where that is faster.  A segment has a whole number of chunks of both paths.
 DecayPlan plan_of(int n_seq, int n_tok, int H, int dk, int dv, int io, uint32_t flags, bool packed, int n_jobs) {
     DecayPlan p = {false, 0, 1, n_seq, 0};
     if ((flags & KDN_FLAG_NO_SPLIT) || n_seq <= 0 || n_tok <= 0 || H <= 0) return p;
     const bool tc = use_tc(io, dk, dv, flags);
-    long long len;   // of a segment
-    if (packed) {
-        // blocks a segment in one launch, and that run at a time
-        const long long per = static_cast<long long>(H) * (n_jobs == 3 && dk != dv ? 2 : n_jobs) * (tc ? 1 : (std::max(dk, dv) + 63) / 64),
-                        room = tc ? kSMs : 2 * kSMs;
-        if (2 * per * n_seq > room) return p;
-        const long long n = room / per - n_seq;
-        len = std::max<long long>(tc ? 512 : 128, ((n_tok + n - 1) / n + 63) / 64 * 64);
-        if (len >= n_tok) return p;
-        // (a sequence has at most its tokens / len + 1 segments, and only one longer than len more than one)
-        p.items = static_cast<int>(n_tok / len) + n_seq;
-        p.slots = static_cast<int>(n_tok / len + std::min<long long>(n_tok / len, n_seq));
-    } else {
-        len = dense_segment(n_seq, n_tok / n_seq, H, dk, dv, tc, n_jobs);
-        if (len == 0) return p;
-        p.nseg = static_cast<int>((n_tok / n_seq + len - 1) / len);
-        p.items = p.slots = n_seq * p.nseg;
-    }
+    const long long len = packed ? packed_segment(n_seq, n_tok, H, dk, dv, tc, n_jobs) : dense_segment(n_seq, n_tok / n_seq, H, dk, dv, tc, n_jobs);
+    if (len == 0 || len >= n_tok) return p;
     p.split = true;
     p.seg_len = static_cast<int>(len);
+    p.nseg = static_cast<int>((n_tok / n_seq + len - 1) / len);
+    // (packed: a sequence has at most its tokens / len + 1 segments, and only one longer than len more than one)
+    p.items = packed ? static_cast<int>(n_tok / len) + n_seq : n_seq * p.nseg;
+    p.slots = packed ? static_cast<int>(n_tok / len + std::min<long long>(n_tok / len, n_seq)) : p.items;
     return p;
 }
 
