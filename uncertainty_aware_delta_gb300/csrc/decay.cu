@@ -340,16 +340,17 @@ template <int DK, int DVS, bool BF> __global__ void __launch_bounds__(kThreads, 
             }
 }
 
-// Segments' own states -> the states that they begin with, and the last one: a few elements a thread.
+// Segments' own states -> the states that they begin with, and the last one: a few elements a thread.  Bounds that are out of range
+// are noted here, by the first block of a sequence.
 constexpr int kChainElems = 4;
 __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_constant__ DecayParams P) {
     const DecayJob& J = P.job[blockIdx.z];
     const int elems = J.dk * J.dv, b = blockIdx.y / P.H, h = blockIdx.y % P.H;
     int row0, len, first = b * P.nseg;
-    sequence(P, b, row0, len);
+    if (!sequence(P, b, row0, len) && threadIdx.x == 0 && blockIdx.x + h + blockIdx.z == 0) set_status(P.status, kStatusRange);
     if (P.cu) {
         if (len <= P.seg_len) return;
-        first = packed_item(P, ~b, false).slot;
+        first = packed_item(P, ~b).slot;
         if (first + segments(len, P.seg_len) > P.slots) return;   // (bounds that run backwards)
     }
     const float l = P.log_decay[h], full = power(l, P.seg_len);

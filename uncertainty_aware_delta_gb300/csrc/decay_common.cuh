@@ -62,7 +62,7 @@ struct DecayItem {
 
 // The segments of packed sequences longer than seg_len are counted through first, then the other sequences: item `want` of
 // them, or (want < 0) the first slot of sequence ~want.  A warp together.
-__device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want, bool report) {
+__device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want) {
     const uint32_t all = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     DecayItem it = {0, 0, 0, -1, false};
@@ -72,7 +72,7 @@ __device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want,
 #pragma unroll 1
         for (int s0 = 0; s0 < P.n_seq; s0 += 32) {
             int row = 0, len = -1;
-            if (s0 + lane < P.n_seq && !sequence(P, s0 + lane, row, len) && report) set_status(P.status, kStatusRange);
+            if (s0 + lane < P.n_seq) sequence(P, s0 + lane, row, len);
             const bool cut = len > P.seg_len;
             const int mine = whole ? (len >= 0 && !cut) : cut ? segments(len, P.seg_len) : 0;
             int upto = mine;
@@ -105,7 +105,8 @@ __device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want,
     return it;
 }
 
-// Item `item` of a pass.  `report`: the block's first warp notes bounds that are out of range.
+// Item `item` of a pass.  `report`: bounds that are out of range are noted, where every sequence is an item (of packed sequences that
+// are cut, the search for an item ends where it is found: the chaining, which goes through all sequences, notes them).
 __device__ __forceinline__ DecayItem find_item(const DecayParams& P, int item, bool report) {
     DecayItem it = {item, 0, 0, -1, true};
     if (P.pass == kWhole) {
@@ -118,7 +119,7 @@ __device__ __forceinline__ DecayItem find_item(const DecayParams& P, int item, b
         it.row += seg * P.seg_len;
         it.len = min(it.len - seg * P.seg_len, P.seg_len);
     } else {
-        it = packed_item(P, item, report && item == 0);
+        it = packed_item(P, item);
         // (where bounds run backwards there may be more segments than room)
         if (it.slot >= P.slots || (P.pass == kStates && it.slot < 0)) it.any = false;
     }
