@@ -1,4 +1,5 @@
-"""Packed bounds that are wrong, in calls whose long sequences are cut into segments: every sequence's are looked at."""
+"""Packed bounds that are wrong, in calls whose long sequences are cut into segments: every sequence's are looked at, and the ones
+that are right keep their results."""
 import pytest
 import torch
 
@@ -61,3 +62,24 @@ def test_reported_wherever_they_are(io, d, back, what):
     assert all(torch.equal(a[first:upto], b[first:upto]) for a, b in zip(got[0], good[0]))
     if what == "last" and not back:
         assert bool((got[0][0][cu[N - 1]:] == 7).all())
+
+
+@FORMS
+@pytest.mark.parametrize("back", [False, True])
+def test_sequences_behind_bounds_that_run_backwards(io, d, back):
+    """The long sequence's rows in four of them: more segments than the tokens have.  Those behind share no row with them."""
+    x = inputs(LENGTHS, 1, d, d, io, True)
+    tail = [LONG + 20 * i for i in range(N - 6)]
+    wrong = [0, LONG, 0, LONG, 0, LONG, 0] + tail
+    right = [0, LONG, LONG, LONG, LONG, LONG, LONG] + tail
+    right[1:7] = [0, 0, 0, 0, 0, 0]
+    assert len(wrong) == len(right) == N + 1
+    tok = sum(LENGTHS)
+    good, status = run(x, right, io, d, back, tok)
+    assert status == 0
+    got, status = run(x, wrong, io, d, back, tok)
+    assert status == 9
+    assert torch.equal(got[1][7:], good[1][7:])
+    assert all(torch.equal(a[LONG:tail[-1]], b[LONG:tail[-1]]) for a, b in zip(got[0], good[0]))
+    if not back:
+        assert bool((got[0][0][tail[-1]:] == 7).all())

@@ -350,8 +350,9 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
     if (!sequence(P, b, row0, len) && threadIdx.x == 0 && blockIdx.x + h + blockIdx.z == 0) set_status(P.status, kStatusRange);
     if (P.cu) {
         if (len <= P.seg_len) return;
-        first = packed_item(P, ~b).slot;
-        if (first + segments(len, P.seg_len) > P.slots) return;   // (bounds that run backwards)
+        const DecayItem it = packed_item(P, ~b);
+        if (it.len == 0) return;   // (it begins before another one's end)
+        first = it.slot;
     }
     const float l = P.log_decay[h], full = power(l, P.seg_len);
     const int n = segments(len, P.seg_len);

@@ -61,18 +61,26 @@ struct DecayItem {
 };
 
 // The segments of packed sequences longer than seg_len are counted through first, then the other sequences: item `want` of
-// them, or (want < 0) the first slot of sequence ~want.  A warp together.
+// them, or (want < 0) the first slot of sequence ~want.  A sequence that begins before an earlier one's end (bounds before it ran
+// backwards) counts as empty, so that there are no more segments than all tokens have.  A warp together.
 __device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want) {
     const uint32_t all = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     DecayItem it = {0, 0, 0, -1, false};
     int before = 0;
 #pragma unroll 1
-    for (int whole = 0; whole < 2; ++whole)
+    for (int whole = 0; whole < 2; ++whole) {
+        int end = 0;   // of all sequences before
 #pragma unroll 1
         for (int s0 = 0; s0 < P.n_seq; s0 += 32) {
             int row = 0, len = -1;
             if (s0 + lane < P.n_seq) sequence(P, s0 + lane, row, len);
+            int reach = max(end, row + len);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) reach = max(reach, __shfl_sync(all, reach, max(lane - o, 0)));
+            const int before_it = __shfl_sync(all, reach, max(lane - 1, 0));
+            if (len > 0 && row < (lane ? before_it : end)) row = len = 0;
+            end = __shfl_sync(all, reach, 31);
             const bool cut = len > P.seg_len;
             const int mine = whole ? (len >= 0 && !cut) : cut ? segments(len, P.seg_len) : 0;
             int upto = mine;
@@ -102,6 +110,7 @@ __device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want)
             }
             before += __shfl_sync(all, upto, 31);
         }
+    }
     return it;
 }
 
@@ -120,8 +129,7 @@ __device__ __forceinline__ DecayItem find_item(const DecayParams& P, int item, b
         it.len = min(it.len - seg * P.seg_len, P.seg_len);
     } else {
         it = packed_item(P, item);
-        // (where bounds run backwards there may be more segments than room)
-        if (it.slot >= P.slots || (P.pass == kStates && it.slot < 0)) it.any = false;
+        if (P.pass == kStates && it.slot < 0) it.any = false;
     }
     return it;
 }
