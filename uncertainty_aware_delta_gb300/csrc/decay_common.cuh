@@ -74,13 +74,16 @@ __device__ __forceinline__ DecayItem packed_item(const DecayParams& P, int want)
 #pragma unroll 1
         for (int s0 = 0; s0 < P.n_seq; s0 += 32) {
             int row = 0, len = -1;
-            if (s0 + lane < P.n_seq) sequence(P, s0 + lane, row, len);
-            int reach = max(end, row + len);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) reach = max(reach, __shfl_sync(all, reach, max(lane - o, 0)));
-            const int before_it = __shfl_sync(all, reach, max(lane - 1, 0));
-            if (len > 0 && row < (lane ? before_it : end)) row = len = 0;
-            end = __shfl_sync(all, reach, 31);
+            const bool wrong = s0 + lane < P.n_seq && !sequence(P, s0 + lane, row, len);
+            const int upto_here = max(end, __reduce_max_sync(all, row + len));
+            if (__any_sync(all, wrong || (len > 0 && row < end))) {   // (else every one of these begins where the last ends)
+                int reach = row + len;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) reach = max(reach, __shfl_sync(all, reach, max(lane - o, 0)));
+                reach = __shfl_sync(all, reach, max(lane - 1, 0));
+                if (len > 0 && row < (lane ? max(reach, end) : end)) row = len = 0;
+            }
+            end = upto_here;
             const bool cut = len > P.seg_len;
             const int mine = whole ? (len >= 0 && !cut) : cut ? segments(len, P.seg_len) : 0;
             int upto = mine;
