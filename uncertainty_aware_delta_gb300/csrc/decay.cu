@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
         if (it.len == 0) return;   // (it begins before another one's end)
         first = it.slot;
     }
-    const float l = P.log_decay[h], full = power(l, P.seg_len);
+    const float l = P.log_decay[h];
     const int n = segments(len, P.seg_len);
-    const float last = power(l, len - (n - 1) * P.seg_len);
+    const Carry full(l, P.seg_len), last(l, len - (n - 1) * P.seg_len);
     const size_t step = static_cast<size_t>(P.H) * elems;
 #pragma unroll 1
     for (int y = 0; y < kChainElems; ++y) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
         if (e >= elems) break;
         const size_t at = static_cast<size_t>(blockIdx.y) * elems + static_cast<size_t>(e / J.dv) * J.s_k + static_cast<size_t>(e % J.dv) * J.s_v;
         float* st = P.states[blockIdx.z] + (static_cast<size_t>(first) * P.H + h) * elems + e;
-        float S = J.S0 ? J.S0[at] : 0.f;
+        float S = J.S0 ? J.S0[at] : 0.f, rest = 0.f;
         // (kBatch segments' loads at a time: one by one, nine segments took 30 us)
         constexpr int kBatch = 8;
 #pragma unroll 1
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) decay_chain_kernel(const __grid_cons
                 if (i0 + i >= n) break;
                 const int seg = J.reverse ? n - 1 - i0 - i : i0 + i;
                 st[seg * step] = S;
-                S = fmaf(seg == n - 1 ? last : full, S, own[i]);
+                S = fmaf((seg == n - 1 ? last : full).next(rest), S, own[i]);
             }
         }
         if (J.S_T) J.S_T[at] = S;

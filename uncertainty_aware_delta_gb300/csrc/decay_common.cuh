@@ -11,8 +11,8 @@ namespace kdn {
 // exp(l n) for a whole n >= 0: 1 for n = 0 whatever l is.
 __device__ __forceinline__ float power(float l, int n) { return n == 0 ? 1.f : expf(l * static_cast<float>(n)); }
 
-// exp(l n), by which the states of thousands of chunks are multiplied one after another: the rounding of one number close to 1
-// would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).  It is held as a sum of two, and next() gives the nearest
+// exp(l n), by which the states of thousands of chunks, or of hundreds of segments, are multiplied one after another: the rounding
+// of one number close to 1 would add up (2e-5 over 800 chunks of 64 tokens at l = -1e-4).  It is held as a sum of two, and next() gives the nearest
 // number to what is left to multiply by, so that the product of any chunks' factors stays within a rounding of the power.
 // Where the power is small it has more digits than 1 + expm1 has, and few chunks matter.
 struct Carry {
