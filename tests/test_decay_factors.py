@@ -62,3 +62,38 @@ def test_segments(io, d):
         assert bool((drift(S[0], S0, l, T) <= limit).all()), i
         g = kdn.kdn_decay_backward(x, x, x, l, None, x, S0[None])
         assert bool((drift(g["S0"][0], S0, l, T) <= limit).all()), i
+
+
+@pytest.mark.parametrize("io,d", [("f32", 64), ("bf16", 128)])
+def test_steps(io, d):
+    """Decoding: one token a call."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    H, n, once = 16, 16384, 512
+    l = -1e-4 * (1 + torch.arange(H, device="cuda") / H)
+    S0, x = states(H, d), torch.zeros(1, H, d, dtype=IO[io], device="cuda")
+    S, o = S0[None].clone(), torch.empty_like(x)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(once):
+            kdn.kdn_decay_step(x, x, x, l, S, o=o)
+    for _ in range(n // once):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert bool((drift(S[0], S0, l, n) <= allowed(l, n, n, d * d)).all())
+
+
+@pytest.mark.parametrize("log_decay", [0.0, -0.3, -0.6, -20.0, -float("inf")])
+def test_steps_of_any_decay(log_decay):
+    """exp(log_decay) S + k v^T.  Of k v^T the product is rounded, its sum with what the factor's small part gives, and the whole sum: three
+    times 2^-24.  Of the old state the whole sum (and 2^-48 of the small part), and its factor is good to two units in the last place, 2^-22."""
+    import uncertainty_aware_delta_gb300 as kdn
+
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(2, 3, 64, generator=g).cuda() for _ in range(3))
+    S0, l = torch.randn(2, 3, 64, 64, generator=g).cuda(), torch.full((3,), log_decay, device="cuda")
+    S = S0.clone()
+    kdn.kdn_decay_step(q, k, v, l, S)
+    own, old = k.cpu().double()[..., :, None] * v.cpu().double()[..., None, :], math.exp(log_decay) * S0.cpu().double()
+    assert bool(((S.cpu().double() - own - old).abs() <= 2.0 ** -24 * (3 * own.abs() + 6 * old.abs())).all())
