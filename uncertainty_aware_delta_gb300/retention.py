@@ -12,12 +12,19 @@ from .binding import KDN_BF16, library
 _ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 
 
+def _fits(t, name):
+    """The sizes of a tensor as 32-bit arguments (ctypes would cut them off; those of one with few elements need no look)."""
+    if not 0 < t.numel() <= 0x7fffffff and max(t.shape) > 0x7fffffff:
+        raise ValueError(f"a size of {name}, {max(t.shape)}, does not fit 32 bits")
+    return t.shape
+
+
 def _tokens(t, name):
     """Tokens, heads and channels of [B, T, heads, d] or [tokens, heads, d]."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
         raise ValueError(f"{name} must be a tensor [B, T, heads, d] or [tokens, heads, d]")
-    s = t.shape
-    return (s[0] * s[1], s[2], s[3]) if len(s) == 4 else (s[0], s[1], s[2])
+    s = _fits(t, name)
+    return (_int(s[0] * s[1], "tokens"), s[2], s[3]) if len(s) == 4 else s
 
 
 def _operand(t, name, dtype, shape, device):
@@ -51,7 +58,7 @@ def _sequences(q, cu, device):
         raise ValueError("with cu, tokens are packed as [tokens, H, d]")
     if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu must be a tensor [sequences + 1]")
-    return cu.shape[0] - 1, _tensor(cu, "cu", torch.int32, cu.shape, device)
+    return _int(cu.shape[0] - 1, "sequences"), _tensor(cu, "cu", torch.int32, cu.shape, device)
 
 
 def decay_workspace_size(n_seq, n_tok, H, dk, dv, io=KDN_BF16, flags=0) -> int:
@@ -74,8 +81,8 @@ def kdn_decay_forward(q, k, v, log_decay, S0=None, *, cu=None, flags=0, out=None
     device, io, flags = q.device, _io(q, "q"), _int(flags, "flags")
     tok, H, dk = _tokens(q, "q")
     n, cu_ptr = _sequences(q, cu, device)
-    keys, dv, f32 = q.shape, v.shape[-1], torch.float32
-    shape, tok, dt = (*keys[:-1], dv), _int(tok, "tokens"), q.dtype
+    keys, dv, f32 = q.shape, _fits(v, "v")[-1], torch.float32
+    shape, dt = (*keys[:-1], dv), q.dtype
     states = (n, H, dk, dv)
     if out is None:
         made = [torch.empty(shape, dtype=dt, device=device), torch.empty(states, dtype=f32, device=device)]
@@ -97,8 +104,8 @@ def kdn_decay_step(q, k, v, log_decay, S, *, o=None, stream=None):
     """One token of the same recurrence per sequence: q, k [B, H, dk], v [B, H, dv]; S [B, H, dk, dv] fp32 is updated in
     place.  Returns o [B, H, dv]."""
     device, io = q.device, _io(q, "q")
-    B, H, dk = q.shape
-    dv, made = v.shape[-1], []
+    B, H, dk = _fits(q, "q")
+    dv, made = _fits(v, "v")[-1], []
     if o is None:
         o = torch.empty((B, H, dv), dtype=q.dtype, device=device)
         made.append(o)
@@ -106,7 +113,7 @@ def kdn_decay_step(q, k, v, log_decay, S, *, o=None, stream=None):
     else:
         out = _tensor(o, "o", q.dtype, (B, H, dv), device)
     _call(library().kdn_decay_step, device, stream,
-          (_int(B, "B"), H, dk, dv, io, _tensor(q, "q", q.dtype, (B, H, dk), device), _tensor(k, "k", q.dtype, (B, H, dk), device),
+          (B, H, dk, dv, io, _tensor(q, "q", q.dtype, (B, H, dk), device), _tensor(k, "k", q.dtype, (B, H, dk), device),
            _tensor(v, "v", q.dtype, (B, H, dv), device), _tensor(log_decay, "log_decay", torch.float32, (H,), device),
            _tensor(S, "S", torch.float32, (B, H, dk, dv), device), out), made)
     return o
@@ -119,8 +126,8 @@ def kdn_decay_backward(q, k, v, log_decay, S0=None, dO=None, dS_T=None, *, cu=No
     device, io, flags = q.device, _io(q, "q"), _int(flags, "flags")
     tok, H, dk = _tokens(q, "q")
     n, cu_ptr = _sequences(q, cu, device)
-    keys, dv, f32 = q.shape, v.shape[-1], torch.float32
-    values, tok, dt = (*keys[:-1], dv), _int(tok, "tokens"), q.dtype
+    keys, dv, f32 = q.shape, _fits(v, "v")[-1], torch.float32
+    values, dt = (*keys[:-1], dv), q.dtype
     states = (n, H, dk, dv)
     grads = {name: torch.empty(shape, dtype=dt, device=device) for name, shape in (("q", keys), ("k", keys), ("v", values))}
     grads["S0"] = torch.empty(states, dtype=f32, device=device)
@@ -157,7 +164,7 @@ def kdn_group_norm(x, weight=None, bias=None, *, gate=None, act="none", eps=1e-5
         y = _tensor(out, "out", x.dtype, shape, device)
     gates = (None, 0, 0) if gate is None else _operand(gate, "gate", x.dtype, shape, device)
     _call(library().kdn_group_norm, device, stream,
-          (_int(rows, "rows"), G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
+          (rows, G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
            _maybe(weight, "weight", torch.float32, (G, d), device), _maybe(bias, "bias", torch.float32, (G, d), device), *gates,
            y), made)
     return out
@@ -180,7 +187,7 @@ def kdn_group_norm_backward(x, dy, weight=None, bias=None, *, gate=None, act="no
              "bias": None if bias is None else torch.empty((G, d), **f32)}
     made = [t for t in grads.values() if t is not None]
     gates = (None, 0, 0) if gate is None else _operand(gate, "gate", x.dtype, shape, device)
-    ws, ws_bytes = _workspace(workspace, lib.kdn_group_norm_backward_workspace_size(_int(rows, "rows"), G, d, io), device, made)
+    ws, ws_bytes = _workspace(workspace, lib.kdn_group_norm_backward_workspace_size(rows, G, d, io), device, made)
     _call(lib.kdn_group_norm_backward, device, stream,
           (rows, G, d, kind, eps, io, *_operand(x, "x", x.dtype, shape, device),
            _maybe(weight, "weight", torch.float32, (G, d), device), _maybe(bias, "bias", torch.float32, (G, d), device), *gates,
