@@ -537,7 +537,8 @@ typedef enum { KDN_ACT_NONE = 0, KDN_ACT_SILU = 1, KDN_ACT_SIGMOID = 2 } kdn_act
  * Inputs : x, gate [rows, groups, d] io_dtype; weight, bias [groups, d] fp32, each may be NULL
  *          (one, zero); eps >= 0.
  * Output : y [rows, groups, d] io_dtype, dense.  No workspace, no status.
- * Sizes  : d a multiple of 8 up to 256; sums in fp32.
+ * Sizes  : d a multiple of 8 up to 256; sums in fp32 (of squares that would leave its range, after the deviations have been
+ *          taken by a power of two; a group whose values' sum passes 3.4e38 counts as infinite).
  */
 kdn_status kdn_group_norm(int rows, int groups, int d, int act, float eps, int io_dtype,
                           const void *x, int64_t x_row, int64_t x_head,

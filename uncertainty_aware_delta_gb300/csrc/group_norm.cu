@@ -9,7 +9,7 @@
 // written once a block and joined by a second kernel in a fixed order.
 //
 // Measured on 32768 tokens of 16 groups of 128, bf16, SiLU of a gate: 74 us, 5.5 TB/s, 80% of the copy rate (one row of a
-// thread at a time 108, two 90, four 74); gradients 121 us, 5.5 TB/s (115 the first kernel; 175 with a row at a time and full
+// thread at a time 108, two 90, four 74); gradients 121 us, 5.5 TB/s (175 with a row at a time and full
 // exponentials; blocks of four an SM 171, of three 154, of two, each with two rows' loads ahead, 121).  Bound by the bytes, and by
 // the instructions that come with them: issue slots are busy for 65% of the time, and 75% in the gradients.
 
@@ -158,6 +158,92 @@ template <int LANES> __device__ __forceinline__ float normalise(float2 (&x)[kPai
     return rsqrtf(group_sum<LANES>(mine ? sq.x + sq.y : 0.f, lanes) * inv + eps);
 }
 
+// Whether the squares of deviations have kept to fp32's range, by what came out for 1 / sigma: not 0 (they were infinite), nor so large
+// that they, with eps, were small and have lost digits.  As an unsigned number less one, 0 is the largest (and NaN is out of range, too).
+// The kernels keep the worst of a thread's rows, one instruction a row (32768 tokens of 16 groups of 128, bf16, gate: 72.9 us for 72.1 without, gradients 119.4
+// for 119.0, in graphs; with a branch in the loop the forward took 74 to 76).
+constexpr uint32_t kMostRstd = (127 + 50) << 23;   // 2^50
+__device__ __forceinline__ bool in_range(float rstd) { return __float_as_uint(rstd) - 1 < kMostRstd; }
+__device__ __forceinline__ uint32_t largest(float rstd, uint32_t x) { return __viaddmax_u32(__float_as_uint(rstd), 0xffffffffu, x); }
+
+// Rows that were out of range once more, a warp together: their deviations are taken by a power of two before they are squared.  `part_w`,
+// `part_b`: the thread's sums for the gradients of weight and bias, which these rows' norms are not in yet.
+template <typename T, int ACT, bool GATE, bool BACK> __device__ __forceinline__ void rows_again(const NormParams& P, float* part_w, float* part_b) {
+    const NormArgs& A = P.a;
+    const Place p = place_of(P);
+    float2 w[kPairs], b[kPairs], dw[kPairs] = {}, db[kPairs] = {};
+    parameters(A.w, p, A.d, 1.f, w);
+    parameters(A.b, p, A.d, 0.f, b);
+    const float inv = 1.f / A.d;
+#pragma unroll 1
+    for (int row = p.row; __any_sync(kAll, row < A.rows); row += p.step) {
+        const bool mine = p.mine && row < A.rows;
+        Vec<T> v = {}, u = {}, t = {};
+        if (mine) {
+            v.load(A.x.p, row * A.x.row + p.g * A.x.head + p.c);
+            if (BACK) u.load(A.dy.p, row * A.dy.row + p.g * A.dy.head + p.c);
+            if (GATE) t.load(A.gate.p, row * A.gate.row + p.g * A.gate.head + p.c);
+        }
+        float2 x[kPairs], y[kPairs], z[kPairs];
+        v.get(x);
+        const bool now = !in_range(normalise<0>(x, mine, inv, A.eps, P.lanes)) && mine;
+        float most = 0.f;
+        for (int i = 0; i < kPairs; ++i) most = fmaxf(most, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        most = mine ? most : 0.f;
+        for (int o = P.lanes >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+        // 2^-e for a largest deviation of 2^e (from 2^-100 to 2^126)
+        const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 27), 253);
+        const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        float2 sq = both(0.f);
+        for (int i = 0; i < kPairs; ++i) {
+            x[i] = mul2(x[i], both(scale));
+            sq = fma2(x[i], x[i], sq);
+        }
+        const float r = rsqrtf(fmaf(group_sum<0>(mine ? sq.x + sq.y : 0.f, P.lanes), inv, A.eps * scale * scale)), rstd = r * scale;
+        u.get(y);
+        if (GATE) t.get(z);
+        float2 t1 = both(0.f), t2 = t1, slope;
+        for (int i = 0; i < kPairs; ++i) {
+            x[i] = mul2(x[i], both(r));
+            const float2 n = fma2(x[i], w[i], b[i]);
+            if (!BACK) {
+                x[i] = GATE ? mul2(n, act<T, ACT>(z[i], slope)) : act<T, ACT>(n, slope);
+                continue;
+            }
+            const float2 f = act<T, ACT>(GATE ? z[i] : n, slope), dn = mul2(y[i], GATE ? f : slope);
+            if (GATE) z[i] = mul2(mul2(y[i], n), slope);
+            if (now) dw[i] = fma2(dn, x[i], dw[i]);
+            if (now && !GATE) db[i] = add2(db[i], dn);
+            y[i] = mul2(dn, w[i]);
+            t1 = add2(t1, y[i]);
+            t2 = fma2(y[i], x[i], t2);
+        }
+        const long long at = (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c;
+        if (!BACK) {
+            if (now) Vec<T>::store(A.y, at, x);
+            continue;
+        }
+        const float s1 = group_sum<0>(mine ? t1.x + t1.y : 0.f, P.lanes) * inv, s2 = group_sum<0>(mine ? t2.x + t2.y : 0.f, P.lanes) * inv;
+        if (!now) continue;
+        for (int i = 0; i < kPairs; ++i) y[i] = mul2(both(rstd), fma2(x[i], both(-s2), add2(y[i], both(-s1))));
+        Vec<T>::store(A.dx, at, y);
+        if (GATE) Vec<T>::store(A.dgate, at, z);
+    }
+    auto add = [&](float* part, const float2 (&more)[kPairs]) {
+        if (!part || !p.mine) return;
+        float2 sum[kPairs];
+        Vec<float> had;
+        had.load(part, 0);
+        had.get(sum);
+        for (int i = 0; i < kPairs; ++i) sum[i] = add2(sum[i], more[i]);
+        Vec<float>::store(part, 0, sum);
+    };
+    if (BACK) {
+        add(part_w, dw);
+        add(part_b, db);
+    }
+}
+
 template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost) group_norm_kernel(const __grid_constant__ NormParams P) {
     const NormArgs& A = P.a;
     const Place p = place_of(P);
@@ -165,6 +251,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     parameters(A.w, p, A.d, 1.f, w);
     parameters(A.b, p, A.d, 0.f, b);
     const float inv = 1.f / A.d;
+    uint32_t worst = 0;
     // kAt rows at a time, their loads ahead of all else (all lanes of a warp go on together: the sums are shuffles)
     for (int row = p.row; __any_sync(kAll, row < A.rows); row += kAt<T> * p.step) {
         Vec<T> v[kAt<T>], gate[kAt<T>];
@@ -186,6 +273,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
             v[e].get(x);
             const float rstd = normalise<LANES>(x, mine, inv, A.eps, P.lanes);
             if (mine) {
+                worst = largest(rstd, worst);
                 float2 z[kPairs], slope;
                 if (GATE) gate[e].get(z);
 #pragma unroll
@@ -197,6 +285,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
             }
         }
     }
+    if (__any_sync(kAll, worst >= kMostRstd)) rows_again<T, ACT, GATE, false>(P, nullptr, nullptr);
 }
 
 template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bounds__(kMost, kBackwardBlocks) group_norm_backward_kernel(const __grid_constant__ NormParams P) {
@@ -218,6 +307,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
     };
 #pragma unroll
     for (int e = 0; e < kNext<T>; ++e) fetch(p.row + e * p.step, e);
+    uint32_t worst = 0;
     for (int row0 = p.row; __any_sync(kAll, row0 < A.rows); row0 += kNext<T> * p.step)
 #pragma unroll
     for (int e = 0; e < kNext<T>; ++e) {
@@ -229,6 +319,7 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
         if (GATE) t[e].get(z);
         fetch(row + kNext<T> * p.step, e);
         const float rstd = normalise<LANES>(x, mine, inv, A.eps, P.lanes);
+        const bool now = in_range(rstd) && mine;   // (else what its norm adds to the weights' gradients comes later)
         float2 t1 = both(0.f), t2 = t1;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
@@ -242,10 +333,8 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
                 act<T, ACT>(n, slope);
                 dn = mul2(y[i], slope);
             }
-            if (mine) {
-                dw[i] = fma2(dn, xh, dw[i]);
-                db[i] = add2(db[i], dn);
-            }
+            if (now) dw[i] = fma2(dn, xh, dw[i]);
+            if (GATE ? mine : now) db[i] = add2(db[i], dn);   // (with a gate dn does not depend on the norm)
             x[i] = xh;
             y[i] = mul2(dn, w[i]);
             t1 = add2(t1, y[i]);
@@ -253,16 +342,19 @@ template <typename T, int ACT, bool GATE, int LANES> __global__ void __launch_bo
         }
         const float s1 = group_sum<LANES>(mine ? t1.x + t1.y : 0.f, P.lanes) * inv, s2 = group_sum<LANES>(mine ? t2.x + t2.y : 0.f, P.lanes) * inv;
         if (!mine) continue;
+        worst = largest(rstd, worst);
         const long long at = (static_cast<long long>(row) * A.groups + p.g) * A.d + p.c;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) y[i] = mul2(both(rstd), fma2(x[i], both(-s2), add2(y[i], both(-s1))));
         Vec<T>::store(A.dx, at, y);
         if (GATE) Vec<T>::store(A.dgate, at, z);
     }
-    if (!p.mine) return;
-    float* part = A.scratch + static_cast<size_t>(p.row) * A.groups * A.d + p.g * A.d + p.c;
-    if (A.dw) Vec<float>::store(part, 0, dw);
-    if (A.db) Vec<float>::store(part + static_cast<size_t>(P.parts) * A.groups * A.d, 0, db);
+    float *const part = A.scratch + static_cast<size_t>(p.row) * A.groups * A.d + p.g * A.d + p.c, *const other = part + static_cast<size_t>(P.parts) * A.groups * A.d;
+    if (p.mine) {
+        if (A.dw) Vec<float>::store(part, 0, dw);
+        if (A.db) Vec<float>::store(other, 0, db);
+    }
+    if (__any_sync(kAll, worst >= kMostRstd)) rows_again<T, ACT, GATE, true>(P, A.dw ? part : nullptr, A.db ? other : nullptr);
 }
 
 // Sums of the parts, a channel a lane: eight warps take every eighth part, and one adds them up.
