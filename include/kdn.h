@@ -476,11 +476,12 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *          an empty sequence is its S0).
  * Sizes  : dk, dv in {16, 32, 64, 128}; n_tok below 2^31 - 2^25.
  * flags  : 0, KDN_FLAG_PORTABLE, KDN_FLAG_NO_SPLIT, KDN_FLAG_TIMEOUT_PROBE.
- * Paths  : bf16 with dk and dv 64 or 128 on tcgen05 tensor cores, everything else (and heads of 64 in
- *          dense sequences of at most 32 tokens) on CUDA cores (products in 3xTF32).  On tcgen05 the
- *          weights g^(i-j) (q_i k_j) and the state that a chunk begins with are rounded to bf16 for
- *          their products with v and q; what is added to the state is not (g^(m-1-j) v_j goes in as
- *          three bf16 parts), and the state itself is fp32.
+ * Paths  : bf16 with dk and dv 64 or 128 on tcgen05, everything else (with KDN_FLAG_PORTABLE all, and
+ *          heads of 64 in dense sequences of at most 32 tokens) on warp-level matrix products in
+ *          3xTF32.  On tcgen05 the weights g^(i-j) (q_i k_j) and the state that a chunk begins with are
+ *          rounded to bf16 for their products with v and q; what is added to the state is not
+ *          (g^(m-1-j) v_j goes in as three bf16 parts, as two where dense sequences that were cut
+ *          are walked for their outputs alone), and the state itself is fp32.
  *          Few long sequences' heads, and packed sequences much longer than the others, are cut into segments
  *          that run side by side, as those of the mixer's forward (KDN_FLAG_NO_SPLIT: they are not).
  * Workspace: kdn_decay_workspace_size() bytes; its first 256 hold the status word.
@@ -498,6 +499,7 @@ kdn_status kdn_decay_forward(int n_seq, int n_tok, int H, int dk, int dv, int io
  * One token of the same recurrence for each of B sequences, the states updated IN PLACE.
  * Inputs : q, k [B, H, dk], v [B, H, dv] io_dtype, dense; log_decay [H].
  * In/out : S [B, H, dk, dv] fp32.   Output: o [B, H, dv] io_dtype.   No workspace, no status.
+ * The decay is taken in two parts, as its rounding to fp32 would add up over the steps.
  */
 kdn_status kdn_decay_step(int B, int H, int dk, int dv, int io_dtype,
                           const void *q, const void *k, const void *v, const float *log_decay,

@@ -1,5 +1,5 @@
-// Linear attention with a decay for each head: the CUDA-core path (fp32 and small heads), the chaining of segments, and the
-// step of one token a sequence.  The tcgen05 path is decay_tc.cu.
+// Linear attention with a decay for each head: the path of warp-level matrix products (fp32 and small heads), the chaining of
+// segments, and the step of one token a sequence.  The tcgen05 path is decay_tc.cu.
 //
 // Chunk form, for tokens 0 .. m - 1 of a chunk, the state S that it begins with and g = exp(log_decay):
 //   o_i  = sum_{j <= i} g^(i - j) (q_i k_j) v_j + g^(i + 1) S^T q_i
@@ -433,7 +433,7 @@ cudaError_t start_pass(const DecayParams& P, int n_jobs, bool tc, cudaStream_t s
 }
 
 bool use_tc(int io, int dk, int dv, uint32_t flags) { return !(flags & KDN_FLAG_PORTABLE) && decay_tc_supported(io, dk, dv); }
-// Heads of 64 in dense sequences of one chunk of the CUDA cores: a tensor-core block, one an SM, has taken some 5 us before its first
+// Heads of 64 in dense sequences of one chunk of this path: a block of the tcgen05 path, one an SM, has taken some 5 us before its first
 // chunk is through.  256 sequences of 1 to 32 tokens, 16 heads: forward 99 to 105 us for 145, gradients 210 to 237 for 405; of 64
 // tokens 152 for 145.  (Heads of 128: 307 to 323 for 194 to 199.  Packed sequences may have a long one among them.)
 bool short_ones(const DecayArgs& a) {
@@ -444,14 +444,14 @@ bool short_ones(const DecayArgs& a) {
 // of their outputs, chaining them 0.3 us a segment, and the launches 9 to 13.  Measured with 420 calls (1 to 5 sequences of 250 to
 // 8000 tokens, 2 to 16 heads of 32, 64 and 128, both directions, each whole and with up to nine lengths of segments): this rule's choice
 // takes 1 to 2% more than the best on average, 27% at most; cutting wherever at most half as many blocks would be at work, into
-// segments of at least 512 tokens (128 on CUDA cores), 6 to 12%, and 85 at most.  8 heads of 64: bf16, 1000 tokens 25 us for 29 whole, 500
+// segments of at least 512 tokens (128 on this path), 6 to 12%, and 85 at most.  8 heads of 64: bf16, 1000 tokens 25 us for 29 whole, 500
 // tokens 20 for 18; fp32, 500 tokens 21 for 37, 250 tokens 19 for 20.
 int dense_segment(long long sequences, int T, int H, int dk, int dv, bool tc, int jobs) {
     // the gradients' jobs are two (of dv keys and dk values) and one in a launch where dk and dv differ
     const bool two = jobs == 3 && dk != dv;
     const int count[2] = {two ? 2 : jobs, 1}, keys[2] = {two ? dv : dk, dk}, values[2] = {two ? dk : dv, dv};
     const long long n = (T + 63) / 64, heads = sequences * H;
-    // segments that run at a time (two blocks of 64 channels an SM on CUDA cores), but no more than chaining them is worth
+    // segments that run at a time (two blocks of 64 channels an SM on this path), but no more than chaining them is worth
     long long blocks = 0;
     for (int i = 0; i <= two; ++i) blocks = std::max(blocks, heads * count[i] * (tc ? 1 : std::max(1, values[i] / 64)));
     const long long fill = (tc ? kSMs : 2 * kSMs) / blocks;

@@ -8,10 +8,11 @@
 // keeps its channels from token to token: weights stay in registers, and the gradients of weights are sums in registers,
 // written once a block and joined by a second kernel in a fixed order.
 //
-// Measured on 32768 tokens of 16 groups of 128, bf16, SiLU of a gate: 74 us, 5.5 TB/s, 80% of the copy rate (one row of a
-// thread at a time 108, two 90, four 74); gradients 121 us, 5.5 TB/s (175 with a row at a time and full
-// exponentials; blocks of four an SM 171, of three 154, of two, each with two rows' loads ahead, 121).  Bound by the bytes, and by
-// the instructions that come with them: issue slots are busy for 65% of the time, and 75% in the gradients.
+// Measured on 32768 tokens of 16 groups of 128, bf16, SiLU of a gate: 75 us, 5.4 TB/s, 79% of the copy rate (one row of a
+// thread at a time 108, two 90, four 74); gradients 123 us, 5.5 TB/s (175 with a row at a time and full exponentials; blocks of
+// four an SM 171, of three 154, of two, each with two rows' loads ahead, 121).  fp32: 129 and 201 us in graphs, 92 and 98% of the
+// rate.  Bound by the bytes, and in bf16 by the instructions that come with them: issue slots are busy for 61% of the time, and
+// 64% in the gradients.
 
 #include <cuda_bf16.h>
 #include <algorithm>
@@ -160,8 +161,8 @@ template <int LANES> __device__ __forceinline__ float normalise(float2 (&x)[kPai
 
 // Whether the squares of deviations have kept to fp32's range, by what came out for 1 / sigma: not 0 (they were infinite), nor so large
 // that they, with eps, were small and have lost digits.  As an unsigned number less one, 0 is the largest (and NaN is out of range, too).
-// The kernels keep the worst of a thread's rows, one instruction a row (32768 tokens of 16 groups of 128, bf16, gate: 72.9 us for 72.1 without, gradients 119.4
-// for 119.0, in graphs; with a branch in the loop the forward took 74 to 76).
+// The kernels keep the worst of a thread's rows, one instruction a row (32768 tokens of 16 groups of 128, bf16, gate, in graphs: 72.9 us
+// for 72.1 without, gradients 119.4 for 119.0; with a branch in the loop the forward took 74 to 76).
 constexpr uint32_t kMostRstd = (127 + 50) << 23;   // 2^50
 __device__ __forceinline__ bool in_range(float rstd) { return __float_as_uint(rstd) - 1 < kMostRstd; }
 __device__ __forceinline__ uint32_t largest(float rstd, uint32_t x) { return __viaddmax_u32(__float_as_uint(rstd), 0xffffffffu, x); }
