@@ -456,8 +456,9 @@ kdn_status kdn_forward_noalloc(int variant, int B, int T, int H, int dk, int dv,
  *   - Sequences are dense (cu NULL: n_tok / n_seq tokens each, one after another, which is
  *     [B, T, H, d]) or packed: sequence s has the rows cu[s] .. cu[s + 1].  cu [n_seq + 1] is
  *     device data: a sequence whose bounds run backwards or outside n_tok is taken as empty, and
- *     KDN_ERR_RANGE is recorded.  Rows of no sequence are left unwritten; what sequences
- *     that share rows give is then not defined, and the others keep their results.
+ *     KDN_ERR_RANGE is recorded.  Rows of no sequence are left unwritten.  What later sequences
+ *     that begin before an earlier one's end give is then not defined, nor what shares rows
+ *     with them; the others keep their results.
  *   - States are [n_seq, H, dk, dv] fp32.
  *   - A value that is not finite makes the outputs that depend on it not finite (infinities
  *     may become NaN) and no others: not those of earlier tokens, of other heads or sequences.
